@@ -322,6 +322,181 @@ const char* signrot_int4_linear_kernel_name(const uint8_t* codes, int64_t tokens
                                             int64_t ldw, int64_t rows);
 
 /*
+ * ---- 8-bit integer products and the norms around a block ------------------
+ *
+ * The projections of a block whose inputs need no online rotation run on
+ * 8-bit integers (one scale per token, one per output channel), the
+ * down-projection runs on the rotated INT4 codes with 8-bit weights, and the
+ * norms around the block hand their result to the product as integer codes.
+ */
+
+/* Element types of the calls below. */
+typedef enum { SIGNROT_F32 = 0, SIGNROT_BF16 = 1 } signrot_type;
+
+/*
+ * Symmetric per-token INT8 quantizer.  Per row, with a = max_j |x_j|:
+ *   scale = a / 127, or 1 when a == 0;
+ *   q_j   = rint(127 x_j / a) (ties to even; 0 when a == 0), -127 .. 127.
+ * The scale is the binary32 quotient correctly rounded; the codes are the
+ * exact rint of the rational 127 x_j / a (a bf16 row makes it decidable in
+ * binary32), so they do not depend on the order of anything.  Run on the rows
+ * of a weight [rows][n] it is the per-output-channel weight quantizer.  A row
+ * that holds an infinity or NaN gets a non-finite scale (and unspecified
+ * codes), so every product with it is non-finite too.
+ *
+ *   x_bf16  device, [tokens][ld] bf16, ld >= n.
+ *   codes   device, [tokens][ldc] int8, ldc >= n.
+ *   scale   device, [tokens] float.
+ *   sum     device, [tokens] int32, or NULL: sum_j q_j.
+ *
+ * 1 <= n <= 131071; any alignment and stride (16-byte aligned rows are the
+ * fast case).  tokens < 0 or >= 2^31, n out of range, ld < n, ldc < n or a
+ * null pointer -> SIGNROT_EINVAL.  No allocation.  Asynchronous.
+ */
+int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, int8_t* codes, int64_t ldc,
+                       float* scale, int32_t* sum, void* stream);
+
+/*
+ * The 8-bit product (W8A8):
+ *   out[t][k] = scale[t] * w_scale[k] * sum_j q[t][j] * w[k][j] + bias[k].
+ * The sum is a whole number in int32 (exact, whatever the order); it is
+ * widened to binary32, scaled, and rounded once to the output type.
+ *
+ *   codes    device, [tokens][ldc] int8, ldc >= n.
+ *   scale    device, [tokens] float.
+ *   w        device, [rows][ldw] int8, ldw >= n: row k is output channel k.
+ *   w_scale  device, [rows] float.
+ *   bias     device, [rows] float, or NULL.
+ *   out      device, [tokens][ldo] of out_type, ldo >= rows.
+ *   workspace, workspace_bytes
+ *            device scratch of at least signrot_int8_linear_workspace(tokens,
+ *            n, rows) bytes, 16-byte aligned; NULL when that is 0.  Its
+ *            contents are unspecified before and after the call; it must not
+ *            be used by anything else until the call's work has ended.
+ *
+ * 1 <= n <= 131071 (an int32 sum cannot overflow); any alignment and stride
+ * of codes, w and out (16-byte aligned rows with n a multiple of 16 take the
+ * faster kernels).  tokens == 0 or rows == 0 is a no-op.  Negative or
+ * over-large sizes (>= 2^31), a leading dimension below its row, an unknown
+ * out_type, a workspace that is too small or a null pointer ->
+ * SIGNROT_EINVAL.  No allocation.  Asynchronous.
+ */
+int signrot_int8_linear(const int8_t* codes, int64_t ldc, const float* scale, int64_t tokens, int64_t n,
+                        const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int64_t rows,
+                        void* out, int64_t ldo, int out_type, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/*
+ * The consumer of the rotated INT4 activations with 8-bit weights (W8A4):
+ *   out[t][k] = scale[t] * w_scale[k]
+ *               * (sum_j q[t][j] * w[k][j] - zero[t] * w_sum[k]) + bias[k],
+ * which is sum_j yhat[t][j] * (w_scale[k] w[k][j]) with yhat = scale * (q -
+ * zero); the product runs on the unsigned integer codes.
+ *
+ *   codes    device, [tokens][n/2] uint8, as signrot_rotate_quant_int4 writes
+ *            them (channel 2m in the low nibble of byte m).
+ *   scale, zero  device, [tokens] float each.
+ *   w_sum    device, [rows] int32: sum_j w[k][j] (signrot_quant_int8's sum).
+ *   workspace  as above, signrot_int4_w8_linear_workspace bytes.
+ *   the other arguments as for signrot_int8_linear.
+ *
+ * n even, 2 <= n <= 131070; the other errors as for signrot_int8_linear.  No
+ * allocation.  Asynchronous.
+ */
+int signrot_int4_w8_linear(const uint8_t* codes, const float* scale, const float* zero, int64_t tokens, int64_t n,
+                           const int8_t* w, int64_t ldw, const float* w_scale, const int32_t* w_sum,
+                           const float* bias, int64_t rows, void* out, int64_t ldo, int out_type, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Scratch bytes the two products need for a shape (0: none, the pointer may
+ * be NULL), or -1 when the sizes are invalid.  Host-only. */
+int64_t signrot_int8_linear_workspace(int64_t tokens, int64_t n, int64_t rows);
+int64_t signrot_int4_w8_linear_workspace(int64_t tokens, int64_t n, int64_t rows);
+
+/* Which kernel the two products would launch for these operands (a static
+ * string), or NULL when the sizes are invalid.  Host-only. */
+const char* signrot_int8_linear_kernel_name(const int8_t* codes, int64_t ldc, int64_t tokens, int64_t n,
+                                            const int8_t* w, int64_t ldw, int64_t rows);
+const char* signrot_int4_w8_linear_kernel_name(const uint8_t* codes, int64_t tokens, int64_t n, const int8_t* w,
+                                               int64_t ldw, int64_t rows);
+
+/* Norms of signrot_residual_norm, of a row x with weight w and bias b:
+ *   RMS    x / sqrt(mean_j x_j^2 + eps) * w + b
+ *   LAYER  (x - mean x) / sqrt(mean_j (x_j - mean x)^2 + eps) * w + b
+ *   NONE   x (weight and bias are not applied) */
+typedef enum { SIGNROT_NORM_NONE = 0, SIGNROT_NORM_RMS = 1, SIGNROT_NORM_LAYER = 2 } signrot_norm;
+
+/*
+ * The norm after a block, the block's gate and residual scale, the residual
+ * sum and the norm before the next block, in one pass over the rows:
+ *   h'[t] = beta * h[t] + alpha * gate[r] * Norm_post(y[t])
+ *   u[t]  = Norm_pre(h'[t]) * (1 + mod_scale[r]) + mod_shift[r]
+ * with r the modulation row of token t: 0 where the stride (ldg, ldm) is 0,
+ * else mod_index[t] (clamped into [0, mod_rows)), or t when mod_index is
+ * NULL.  u leaves as bf16, or as the symmetric per-token INT8 codes and
+ * scales of signrot_quant_int8 (of the binary32 u), or both.  Norm_pre reads
+ * h' before it is rounded to the stream's type.  All arithmetic is binary32;
+ * each output is rounded once.  A row that holds an infinity or NaN gives
+ * unspecified outputs in that row only; its code scale is non-finite.
+ *
+ *   tokens, n     rows, and channels of a row: 0 <= tokens < 2^31,
+ *                 1 <= n <= 131071.
+ *   h, ldh        device, [tokens][ldh] of h_type: the residual stream.
+ *   y, ldy        device, [tokens][ldy] bf16: the block's output, or NULL: no
+ *                 branch, h' = beta * h.
+ *   h_out, ldho   device, [tokens][ldho] of h_type, or NULL: h' is not stored.
+ *                 May be h itself (same pointer and stride); may not overlap
+ *                 h in another way.
+ *   u, ldu        device, [tokens][ldu] bf16, or NULL.
+ *   codes, ldc, code_scale   device, [tokens][ldc] int8 and [tokens] float,
+ *                 or both NULL.
+ *   post_weight, post_bias, pre_weight, pre_bias   device, [n] of param_type,
+ *                 each may be NULL (weight 1, bias 0).
+ *   gate, ldg     device, [n] (ldg == 0) or [mod_rows][ldg], or NULL (1).
+ *   mod_scale, mod_shift, ldm   device, the same two layouts, each may be NULL.
+ *   mod_index, mod_rows  device, [tokens] int32 or NULL; the number of rows of
+ *                 gate, mod_scale and mod_shift where their stride is not 0
+ *                 (at least tokens when mod_index is NULL).
+ *
+ * Any alignment and stride (16-byte aligned rows are the fast case).  A null
+ * h, a leading dimension below n (0 for a shared modulation row), no output
+ * at all, codes without code_scale or the reverse, an unknown norm or type,
+ * a non-finite or negative eps or non-finite alpha or beta, sizes out of
+ * range -> SIGNROT_EINVAL.  tokens == 0 is a no-op.  No allocation.
+ * Asynchronous.
+ */
+typedef struct {
+  int64_t tokens, n;
+  const void* h;
+  int64_t ldh;
+  const void* y;
+  int64_t ldy;
+  void* h_out;
+  int64_t ldho;
+  void* u;
+  int64_t ldu;
+  int8_t* codes;
+  int64_t ldc;
+  float* code_scale;
+  const void* post_weight;
+  const void* post_bias;
+  const void* gate;
+  int64_t ldg;
+  const void* pre_weight;
+  const void* pre_bias;
+  const void* mod_scale;
+  const void* mod_shift;
+  int64_t ldm;
+  const int32_t* mod_index;
+  int64_t mod_rows;
+  float alpha, beta, eps_post, eps_pre;
+  int32_t post_norm, pre_norm;  /* signrot_norm */
+  int32_t h_type, param_type;   /* signrot_type */
+} signrot_residual_norm_args;
+
+int signrot_residual_norm(const signrot_residual_norm_args* args, void* stream);
+
+/*
  * Measurement aid, not part of the method: a kernel that moves the bytes the
  * online path moves per token -- reads the bf16 row (2n bytes), writes n/2
  * bytes to out [tokens][n/2] and one float each to s0 [tokens] and

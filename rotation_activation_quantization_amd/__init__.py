@@ -65,6 +65,22 @@ def lib() -> ctypes.CDLL:
     L.signrot_int4_linear.restype = ctypes.c_int
     L.signrot_int4_linear_kernel_name.argtypes = [vp, i64, i64, vp, i64, i64]
     L.signrot_int4_linear_kernel_name.restype = ctypes.c_char_p
+    L.signrot_quant_int8.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, vp]
+    L.signrot_quant_int8.restype = ctypes.c_int
+    L.signrot_int8_linear.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, ctypes.c_int, vp, i64, vp]
+    L.signrot_int8_linear.restype = ctypes.c_int
+    L.signrot_int4_w8_linear.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp, vp, i64, vp, i64, ctypes.c_int, vp,
+                                         i64, vp]
+    L.signrot_int4_w8_linear.restype = ctypes.c_int
+    for name in ("signrot_int8_linear_workspace", "signrot_int4_w8_linear_workspace"):
+        getattr(L, name).argtypes = [i64, i64, i64]
+        getattr(L, name).restype = i64
+    L.signrot_int8_linear_kernel_name.argtypes = [vp, i64, i64, i64, vp, i64, i64]
+    L.signrot_int8_linear_kernel_name.restype = ctypes.c_char_p
+    L.signrot_int4_w8_linear_kernel_name.argtypes = [vp, i64, i64, vp, i64, i64]
+    L.signrot_int4_w8_linear_kernel_name.restype = ctypes.c_char_p
+    L.signrot_residual_norm.argtypes = [vp, vp]
+    L.signrot_residual_norm.restype = ctypes.c_int
     L.signrot_stream_ceiling.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
     L.signrot_stream_ceiling.restype = ctypes.c_int
     L.signrot_strerror.argtypes = [ctypes.c_int]
@@ -100,6 +116,14 @@ EXPORTED = (
     "signrot_weight_rowsum",
     "signrot_int4_linear",
     "signrot_int4_linear_kernel_name",
+    "signrot_quant_int8",
+    "signrot_int8_linear",
+    "signrot_int8_linear_workspace",
+    "signrot_int8_linear_kernel_name",
+    "signrot_int4_w8_linear",
+    "signrot_int4_w8_linear_workspace",
+    "signrot_int4_w8_linear_kernel_name",
+    "signrot_residual_norm",
     "signrot_strerror",
     "signrot_last_error",
     "signrot_debug_h28",
@@ -367,6 +391,277 @@ def int4_linear_kernel_name(codes, w) -> str | None:
     return r.decode() if r else None
 
 
+# ---- 8-bit products and the norms around a block -----------------------------
+
+_F32, _BF16 = 0, 1
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _type_of(dtype, what):
+    import torch
+
+    if dtype is torch.bfloat16:
+        return _BF16
+    if dtype is torch.float32:
+        return _F32
+    raise ValueError(f"{what} must be bfloat16 or float32, not {dtype}")
+
+
+def _matrix(v, name, rows, n, dtype, device):
+    """(pointer, row stride) of a [rows, n] tensor with contiguous rows; None sizes are free."""
+    if v.dtype is not dtype or v.dim() != 2 or v.device != device:
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor on {device}")
+    shape = v.shape
+    if (rows is not None and shape[0] != rows) or (n is not None and shape[1] != n):
+        raise ValueError(f"{name} has shape {tuple(shape)}, not [{'*' if rows is None else rows}, "
+                         f"{'*' if n is None else n}]")
+    step, unit = v.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if shape[0] <= 1:
+        step = shape[1]
+    elif step < shape[1]:
+        raise ValueError(f"{name} rows overlap")
+    return v.data_ptr(), step
+
+
+def _vector(v, name, size, dtype, device):
+    """Pointer of a contiguous vector of `size` entries, or None for None."""
+    if v is None:
+        return None
+    if v.dtype is not dtype or v.numel() != size or v.device != device or not v.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {size} entries on {device}")
+    return v.data_ptr()
+
+
+def _on_gpu(v, name):
+    if not v.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return v.device
+
+
+def signrot_quant_int8(x, sums: bool = False, out=None):
+    """bf16 [T, n] -> (codes int8 [T, n], scale f32 [T][, sum int32 [T]]): per
+    row scale = max|x| / 127 and codes = rint(127 x / max|x|); sum holds the
+    code sums.  On a weight [rows, n] the rows are the output channels.  `out`
+    may pass preallocated (codes, scale[, sum])."""
+    import torch
+
+    device = _on_gpu(x, "x")
+    ptr, ld = _matrix(x, "x", None, None, torch.bfloat16, device)
+    t, n = x.shape
+    if out is None:
+        out = (torch.empty((t, n), dtype=torch.int8, device=device),
+               torch.empty(t, dtype=torch.float32, device=device))
+        if sums:
+            out += (torch.empty(t, dtype=torch.int32, device=device),)
+    elif len(out) < (3 if sums else 2):
+        raise ValueError("out must hold (codes, scale[, sum])")
+    codes, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
+    check(lib().signrot_quant_int8(ptr, t, n, ld, codes, ldc, _vector(out[1], "scale", t, torch.float32, device),
+                                   _vector(out[2], "sum", t, torch.int32, device) if sums else None, _stream_of(x)),
+          "signrot_quant_int8")
+    return tuple(out[:3 if sums else 2])
+
+
+def _product_out(out, dtype, t, rows, device):
+    import torch
+
+    if out is None:
+        out = torch.empty((t, rows), dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+    elif dtype is not None and out.dtype is not dtype:
+        raise ValueError(f"out is {out.dtype}, dtype {dtype}")
+    kind = _type_of(out.dtype, "out")
+    ptr, ldo = _matrix(out, "out", t, rows, out.dtype, device)
+    return out, kind, ptr, ldo
+
+
+def _workspace(size, device):
+    """(pointer, bytes, owner) of a call's scratch, from torch's allocator on the current stream."""
+    import torch
+
+    if size <= 0:
+        return None, 0, None
+    w = torch.empty(size, dtype=torch.uint8, device=device)
+    return w.data_ptr(), size, w
+
+
+def signrot_int8_linear(codes, scale, w, w_scale, bias=None, dtype=None, out=None):
+    """INT8 activations (codes int8 [T, n], scale f32 [T]) times INT8 weights
+    (w int8 [rows, n], w_scale f32 [rows]) -> [T, rows] of `dtype` (bfloat16,
+    the default, or float32): scale * w_scale * (codes . w^T) + bias, the sum
+    exact in int32.  `out` may pass the result's tensor."""
+    import torch
+
+    device = _on_gpu(codes, "codes")
+    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, device)
+    t, n = codes.shape
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, device)
+    rows = w.shape[0]
+    sptr = _vector(scale, "scale", t, torch.float32, device)
+    vptr = _vector(w_scale, "w_scale", rows, torch.float32, device)
+    bptr = _vector(bias, "bias", rows, torch.float32, device)
+    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
+    L = lib()
+    ws, size, _owner = _workspace(L.signrot_int8_linear_workspace(t, n, rows), device)
+    check(L.signrot_int8_linear(aptr, lda, sptr, t, n, wptr, ldw, vptr, bptr, rows, optr, ldo, kind, ws, size,
+                                _stream_of(codes)), "signrot_int8_linear")
+    return out
+
+
+def signrot_int4_w8_linear(codes, scale, zero, w, w_scale, w_sum, bias=None, dtype=None, out=None):
+    """The rotated INT4 activations (codes u8 [T, n/2], scale and zero f32 [T],
+    as signrot_rotate_quant_int4 returns them) times INT8 weights (w int8
+    [rows, n], w_scale f32 [rows], w_sum int32 [rows] = w.sum(1)) ->
+    [T, rows] of `dtype` (bfloat16, the default, or float32)."""
+    import torch
+
+    device = _on_gpu(codes, "codes")
+    if codes.dtype is not torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous 2-D uint8 tensor")
+    t, n = codes.shape[0], codes.shape[1] * 2
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, device)
+    rows = w.shape[0]
+    sptr = _vector(scale, "scale", t, torch.float32, device)
+    zptr = _vector(zero, "zero", t, torch.float32, device)
+    vptr = _vector(w_scale, "w_scale", rows, torch.float32, device)
+    uptr = _vector(w_sum, "w_sum", rows, torch.int32, device)
+    bptr = _vector(bias, "bias", rows, torch.float32, device)
+    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
+    L = lib()
+    ws, size, _owner = _workspace(L.signrot_int4_w8_linear_workspace(t, n, rows), device)
+    check(L.signrot_int4_w8_linear(codes.data_ptr(), sptr, zptr, t, n, wptr, ldw, vptr, uptr, bptr, rows, optr, ldo,
+                                   kind, ws, size, _stream_of(codes)), "signrot_int4_w8_linear")
+    return out
+
+
+def int8_linear_kernel_name(codes, w) -> str | None:
+    import torch
+
+    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, codes.device)
+    wptr, ldw = _matrix(w, "w", None, codes.shape[1], torch.int8, codes.device)
+    r = lib().signrot_int8_linear_kernel_name(aptr, lda, codes.shape[0], codes.shape[1], wptr, ldw, w.shape[0])
+    return r.decode() if r else None
+
+
+def int4_w8_linear_kernel_name(codes, w) -> str | None:
+    import torch
+
+    n = codes.shape[1] * 2
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, codes.device)
+    r = lib().signrot_int4_w8_linear_kernel_name(codes.data_ptr(), codes.shape[0], n, wptr, ldw, w.shape[0])
+    return r.decode() if r else None
+
+
+class _ResidualNormArgs(ctypes.Structure):
+    _fields_ = [(name, kind) for names, kind in (
+        (("tokens", "n"), ctypes.c_int64), (("h",), ctypes.c_void_p), (("ldh",), ctypes.c_int64),
+        (("y",), ctypes.c_void_p), (("ldy",), ctypes.c_int64), (("h_out",), ctypes.c_void_p),
+        (("ldho",), ctypes.c_int64), (("u",), ctypes.c_void_p), (("ldu",), ctypes.c_int64),
+        (("codes",), ctypes.c_void_p), (("ldc",), ctypes.c_int64),
+        (("code_scale", "post_weight", "post_bias", "gate"), ctypes.c_void_p), (("ldg",), ctypes.c_int64),
+        (("pre_weight", "pre_bias", "mod_scale", "mod_shift"), ctypes.c_void_p), (("ldm",), ctypes.c_int64),
+        (("mod_index",), ctypes.c_void_p), (("mod_rows",), ctypes.c_int64),
+        (("alpha", "beta", "eps_post", "eps_pre"), ctypes.c_float),
+        (("post_norm", "pre_norm", "h_type", "param_type"), ctypes.c_int32)) for name in names]
+
+
+def _modulation(v, name, t, n, index, dtype, device):
+    """(pointer, stride, rows) of a gate or modulation: [n] shared by all rows, or [m, n]."""
+    if v is None:
+        return None, 0, None
+    if v.dim() == 1:
+        return _vector(v, name, n, dtype, device), 0, None
+    ptr, step = _matrix(v, name, None, n, dtype, device)
+    if v.shape[0] < (1 if index is not None else t):
+        raise ValueError(f"{name} has {v.shape[0]} rows for {t} tokens")
+    return ptr, step, v.shape[0]
+
+
+def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
+                   mod_scale, mod_shift, mod_index, h_out, u, codes, code_scale, where):
+    import torch
+
+    device = _on_gpu(h, "h")
+    h_type = _type_of(h.dtype, "h")
+    t, n = h.shape if h.dim() == 2 else (0, 0)
+    hptr, ldh = _matrix(h, "h", None, None, h.dtype, device)
+    yptr, ldy = (None, 0) if y is None else _matrix(y, "y", t, n, torch.bfloat16, device)
+    post_norm = norm if post_norm is None else post_norm
+    if norm not in _NORMS or post_norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}")
+    param = torch.bfloat16
+    for v in (weight, post_weight, bias, post_bias, gate, mod_scale, mod_shift):
+        if v is not None:
+            param = v.dtype
+            break
+    p_type = _type_of(param, "the norm's parameters")
+    gptr, ldg, grows = _modulation(gate, "gate", t, n, mod_index, param, device)
+    mptr, ldm, mrows = _modulation(mod_scale, "mod_scale", t, n, mod_index, param, device)
+    cptr, ldm2, crows = _modulation(mod_shift, "mod_shift", t, n, mod_index, param, device)
+    if mptr is None:
+        ldm = ldm2
+    elif cptr is not None and ldm != ldm2:
+        raise ValueError("mod_scale and mod_shift must have the same row stride")
+    per_row = [r for r in (grows, mrows, crows) if r is not None]
+    hoptr, ldho = (None, 0) if h_out is None else _matrix(h_out, "h_out", t, n, h.dtype, device)
+    uptr, ldu = (None, 0) if u is None else _matrix(u, "u", t, n, torch.bfloat16, device)
+    qptr, ldc = (None, 0) if codes is None else _matrix(codes, "codes", t, n, torch.int8, device)
+    args = _ResidualNormArgs(
+        t, n, hptr, ldh, yptr, ldy, hoptr, ldho, uptr, ldu, qptr, ldc,
+        _vector(code_scale, "scale", t, torch.float32, device),
+        _vector(post_weight, "post_weight", n, param, device), _vector(post_bias, "post_bias", n, param, device),
+        gptr, ldg, _vector(weight, "weight", n, param, device), _vector(bias, "bias", n, param, device),
+        mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, device), min(per_row) if per_row else 0,
+        alpha, beta, eps if post_eps is None else post_eps, eps, _NORMS[post_norm], _NORMS[norm], h_type, p_type)
+    check(lib().signrot_residual_norm(ctypes.addressof(args), _stream_of(h)), where)
+
+
+def signrot_residual_norm(h, y=None, norm: str = "rms", post_norm: str | None = None, eps: float = 1e-6,
+                          post_eps: float | None = None, post_weight=None, post_bias=None, gate=None,
+                          alpha: float = 1.0, beta: float = 1.0, weight=None, bias=None, mod_scale=None,
+                          mod_shift=None, mod_index=None, h_out=None, out=None):
+    """The norms around a block with its gate and residual scale, one pass:
+
+        h' = beta h + alpha gate * Norm_post(y)
+        u  = Norm(h') * (1 + mod_scale) + mod_shift
+
+    h (bf16 or f32) and y (bf16, None: no branch) are [T, n]; norm and
+    post_norm (default: the same) are "rms", "layer" or "none"; weights and
+    biases are [n]; gate, mod_scale and mod_shift are [n], or [m, n] with a row
+    per token, or one per sequence picked by mod_index (int32 [T]); all of
+    them bf16, or all f32.  Returns (h' of h's type, u bf16).  h_out may be h,
+    to update the stream in place; `out` may pass u's tensor."""
+    import torch
+
+    if h_out is None:
+        h_out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if out is None:
+        out = torch.empty(h.shape, dtype=torch.bfloat16, device=h.device)
+    _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
+                   mod_scale, mod_shift, mod_index, h_out, out, None, None, "signrot_residual_norm")
+    return h_out, out
+
+
+def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: str | None = None, eps: float = 1e-6,
+                                     post_eps: float | None = None, post_weight=None, post_bias=None, gate=None,
+                                     alpha: float = 1.0, beta: float = 1.0, weight=None, bias=None, mod_scale=None,
+                                     mod_shift=None, mod_index=None, h_out=None, out=None):
+    """signrot_residual_norm with u quantized as signrot_quant_int8 does, from
+    its binary32 values: returns (h', codes int8 [T, n], scale f32 [T]).
+    `out` may pass (codes, scale)."""
+    import torch
+
+    if h_out is None:
+        h_out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if out is None:
+        out = (torch.empty(h.shape, dtype=torch.int8, device=h.device),
+               torch.empty(h.shape[0], dtype=torch.float32, device=h.device))
+    _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
+                   mod_scale, mod_shift, mod_index, h_out, None, out[0], out[1], "signrot_residual_norm")
+    return h_out, out[0], out[1]
+
+
 def signrot_stream_ceiling(x, out=None):
     """The memory-traffic ceiling kernel (a measurement aid: the online path's
     bytes per token, no arithmetic) on bf16 [T, n] -> (u8 [T, n/2], f32 [T],
@@ -393,3 +688,8 @@ dequant = signrot_dequant
 fold_weights = signrot_fold_weights
 weight_rowsum = signrot_weight_rowsum
 int4_linear = signrot_int4_linear
+quant_int8 = signrot_quant_int8
+int8_linear = signrot_int8_linear
+int4_w8_linear = signrot_int4_w8_linear
+residual_norm = signrot_residual_norm
+residual_norm_quant_int8 = signrot_residual_norm_quant_int8

@@ -29,6 +29,9 @@ SOURCES = [
     "calib_dequant.hip",
     "ceiling.hip",
     "linear.hip",
+    "linear_w8.hip",
+    "quant_int8.hip",
+    "residual_norm.hip",
     "hadamard28.cpp",
     "outer.cpp",
 ]

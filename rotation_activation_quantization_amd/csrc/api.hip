@@ -623,6 +623,179 @@ const char* signrot_int4_linear_kernel_name(const uint8_t* codes, int64_t tokens
   return int4_linear_name(a);
 }
 
+int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, int8_t* codes, int64_t ldc,
+                       float* scale, int32_t* sum, void* stream) {
+  g_last_error[0] = '\0';
+  if (tokens < 0 || tokens >= (int64_t{1} << 31)) return fail_einval("tokens must be in [0, 2^31)");
+  if (n < 1 || n > kW8MaxN) return fail_einval("n must be in [1, 131071]");
+  if (ld < n || ldc < n) return fail_einval("ld and ldc must be >= n");
+  if (tokens == 0) return SIGNROT_OK;
+  if (!x_bf16 || !codes || !scale) return fail_einval("null device pointer");
+  if ((reinterpret_cast<uintptr_t>(x_bf16) & 1u) || (reinterpret_cast<uintptr_t>(scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(sum) & 3u))
+    return fail_einval("a pointer is not aligned to its type");
+  const hipError_t e = launch_quant_int8(static_cast<const uint16_t*>(x_bf16), tokens, static_cast<int>(n), ld, codes,
+                                         ldc, scale, sum, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "quant_int8 launch");
+  return SIGNROT_OK;
+}
+
+namespace {
+// Sizes of the 8-bit products, shared by the calls and their host-only helpers.
+int w8_sizes(int64_t tokens, int64_t n, int64_t rows, bool a4) {
+  if (tokens < 0 || rows < 0 || tokens >= (int64_t{1} << 31) || rows >= (int64_t{1} << 31))
+    return fail_einval("tokens and rows must be in [0, 2^31)");
+  if (n < 1 || n > kW8MaxN) return fail_einval("n must be in [1, 131071]");
+  if (a4 && (n & 1)) return fail_einval("n must be even");
+  return SIGNROT_OK;
+}
+
+int w8_linear(W8Args& a, int64_t tokens, int64_t n, int64_t rows, int out_type, void* workspace,
+              int64_t workspace_bytes, void* stream, const char* where) {
+  g_last_error[0] = '\0';
+  const int st = w8_sizes(tokens, n, rows, a.a4 != 0);
+  if (st != SIGNROT_OK) return st;
+  if (a.lda < (a.a4 ? n / 2 : n) || a.ldw < n) return fail_einval("ldc and ldw must be >= n");
+  if (a.ldo < rows) return fail_einval("ldo < rows");
+  if (out_type != SIGNROT_F32 && out_type != SIGNROT_BF16) return fail_einval("unknown out_type");
+  if (tokens == 0 || rows == 0) return SIGNROT_OK;
+  if (!a.a || !a.scale || !a.w || !a.w_scale || !a.out) return fail_einval("null device pointer");
+  if (a.a4 && (!a.zero || !a.w_sum)) return fail_einval("null device pointer");
+  auto odd = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  if (odd(a.scale) || odd(a.zero) || odd(a.w_scale) || odd(a.w_sum) || odd(a.bias) ||
+      (out_type == SIGNROT_F32 ? odd(a.out) : (reinterpret_cast<uintptr_t>(a.out) & 1u) != 0))
+    return fail_einval("a pointer is not aligned to its type");
+  const int64_t need = w8_workspace(tokens, n, rows, a.a4 != 0);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return fail_einval("workspace too small");
+    if (!aligned16(workspace)) return fail_einval("workspace must be 16-byte aligned");
+  }
+  a.partial = static_cast<int32_t*>(workspace);
+  a.out_bf16 = out_type == SIGNROT_BF16;
+  a.T = static_cast<int>(tokens);
+  a.R = static_cast<int>(rows);
+  a.n = static_cast<int>(n);
+  const hipError_t e = launch_w8(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, where);
+  return SIGNROT_OK;
+}
+}  // namespace
+
+int signrot_int8_linear(const int8_t* codes, int64_t ldc, const float* scale, int64_t tokens, int64_t n,
+                        const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int64_t rows,
+                        void* out, int64_t ldo, int out_type, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  W8Args a;
+  memset(&a, 0, sizeof(a));
+  a.a = reinterpret_cast<const uint8_t*>(codes);
+  a.lda = ldc;
+  a.scale = scale;
+  a.w = w;
+  a.ldw = ldw;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.out = out;
+  a.ldo = ldo;
+  return w8_linear(a, tokens, n, rows, out_type, workspace, workspace_bytes, stream, "int8_linear launch");
+}
+
+int signrot_int4_w8_linear(const uint8_t* codes, const float* scale, const float* zero, int64_t tokens, int64_t n,
+                           const int8_t* w, int64_t ldw, const float* w_scale, const int32_t* w_sum,
+                           const float* bias, int64_t rows, void* out, int64_t ldo, int out_type, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  W8Args a;
+  memset(&a, 0, sizeof(a));
+  a.a4 = 1;
+  a.a = codes;
+  a.lda = n / 2;
+  a.scale = scale;
+  a.zero = zero;
+  a.w = w;
+  a.ldw = ldw;
+  a.w_scale = w_scale;
+  a.w_sum = w_sum;
+  a.bias = bias;
+  a.out = out;
+  a.ldo = ldo;
+  return w8_linear(a, tokens, n, rows, out_type, workspace, workspace_bytes, stream, "int4_w8_linear launch");
+}
+
+int64_t signrot_int8_linear_workspace(int64_t tokens, int64_t n, int64_t rows) {
+  return w8_sizes(tokens, n, rows, false) == SIGNROT_OK ? w8_workspace(tokens, n, rows, false) : -1;
+}
+
+int64_t signrot_int4_w8_linear_workspace(int64_t tokens, int64_t n, int64_t rows) {
+  return w8_sizes(tokens, n, rows, true) == SIGNROT_OK ? w8_workspace(tokens, n, rows, true) : -1;
+}
+
+namespace {
+const char* w8_kernel_name(const uint8_t* codes, int64_t lda, int64_t tokens, int64_t n, const int8_t* w, int64_t ldw,
+                           int64_t rows, bool a4) {
+  if (w8_sizes(tokens, n, rows, a4) != SIGNROT_OK || lda < (a4 ? n / 2 : n) || ldw < n) return nullptr;
+  W8Args a;
+  memset(&a, 0, sizeof(a));
+  a.a4 = a4;
+  a.a = codes;
+  a.lda = lda;
+  a.w = w;
+  a.ldw = ldw;
+  a.T = static_cast<int>(tokens);
+  a.R = static_cast<int>(rows);
+  a.n = static_cast<int>(n);
+  return w8_name(a);
+}
+}  // namespace
+
+const char* signrot_int8_linear_kernel_name(const int8_t* codes, int64_t ldc, int64_t tokens, int64_t n,
+                                            const int8_t* w, int64_t ldw, int64_t rows) {
+  return w8_kernel_name(reinterpret_cast<const uint8_t*>(codes), ldc, tokens, n, w, ldw, rows, false);
+}
+
+const char* signrot_int4_w8_linear_kernel_name(const uint8_t* codes, int64_t tokens, int64_t n, const int8_t* w,
+                                               int64_t ldw, int64_t rows) {
+  return w8_kernel_name(codes, n / 2, tokens, n, w, ldw, rows, true);
+}
+
+int signrot_residual_norm(const signrot_residual_norm_args* args, void* stream) {
+  g_last_error[0] = '\0';
+  if (!args) return fail_einval("args is NULL");
+  const signrot_residual_norm_args& a = *args;
+  if (a.tokens < 0 || a.tokens >= (int64_t{1} << 31)) return fail_einval("tokens must be in [0, 2^31)");
+  if (a.n < 1 || a.n > kW8MaxN) return fail_einval("n must be in [1, 131071]");
+  if (a.h_type != SIGNROT_F32 && a.h_type != SIGNROT_BF16) return fail_einval("unknown h_type");
+  if (a.param_type != SIGNROT_F32 && a.param_type != SIGNROT_BF16) return fail_einval("unknown param_type");
+  if (a.post_norm < SIGNROT_NORM_NONE || a.post_norm > SIGNROT_NORM_LAYER || a.pre_norm < SIGNROT_NORM_NONE ||
+      a.pre_norm > SIGNROT_NORM_LAYER)
+    return fail_einval("unknown norm");
+  if (!isfinite(a.alpha) || !isfinite(a.beta)) return fail_einval("alpha and beta must be finite");
+  if (!isfinite(a.eps_post) || !isfinite(a.eps_pre) || a.eps_post < 0.f || a.eps_pre < 0.f)
+    return fail_einval("eps must be finite and >= 0");
+  if (a.ldh < a.n || (a.y && a.ldy < a.n) || (a.h_out && a.ldho < a.n) || (a.u && a.ldu < a.n) ||
+      (a.codes && a.ldc < a.n))
+    return fail_einval("a leading dimension is below n");
+  const bool per_row = (a.gate && a.ldg != 0) || ((a.mod_scale || a.mod_shift) && a.ldm != 0);
+  if ((a.gate && a.ldg != 0 && a.ldg < a.n) || ((a.mod_scale || a.mod_shift) && a.ldm != 0 && a.ldm < a.n))
+    return fail_einval("a modulation stride is neither 0 nor >= n");
+  if (per_row && a.mod_rows < 1 && a.tokens > 0) return fail_einval("mod_rows must be >= 1");
+  if (per_row && !a.mod_index && a.mod_rows < a.tokens) return fail_einval("mod_rows < tokens without mod_index");
+  if (a.tokens == 0) return SIGNROT_OK;
+  if (!a.h) return fail_einval("null device pointer");
+  if (!a.h_out && !a.u && !a.codes) return fail_einval("no output");
+  if (!a.codes != !a.code_scale) return fail_einval("codes and code_scale go together");
+  auto odd = [](const void* p, int type) {
+    return (reinterpret_cast<uintptr_t>(p) & (type == SIGNROT_F32 ? 3u : 1u)) != 0;
+  };
+  if (odd(a.h, a.h_type) || odd(a.h_out, a.h_type) || odd(a.y, SIGNROT_BF16) || odd(a.u, SIGNROT_BF16) ||
+      odd(a.code_scale, SIGNROT_F32) || odd(a.mod_index, SIGNROT_F32) || odd(a.post_weight, a.param_type) ||
+      odd(a.post_bias, a.param_type) || odd(a.gate, a.param_type) || odd(a.pre_weight, a.param_type) ||
+      odd(a.pre_bias, a.param_type) || odd(a.mod_scale, a.param_type) || odd(a.mod_shift, a.param_type))
+    return fail_einval("a pointer is not aligned to its type");
+  if (a.h_out == a.h && a.ldho != a.ldh) return fail_einval("h_out is h with another stride");
+  const hipError_t e = launch_residual_norm(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "residual_norm launch");
+  return SIGNROT_OK;
+}
+
 int signrot_stream_ceiling(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, uint8_t* out, float* s0,
                            float* s1, void* stream) {
   g_last_error[0] = '\0';

@@ -6,6 +6,8 @@
 
 #include <vector>
 
+#include "../../include/signrot.h"
+
 namespace signrot {
 
 // Factorisation n = m * 2^k (n <= 32768): m = 1 for n = 2^k (k >= 1);
@@ -144,5 +146,36 @@ const char* int4_linear_name(const LinearArgs& a);
 hipError_t launch_int4_linear(LinearArgs a, hipStream_t s);
 hipError_t launch_weight_rowsum(const uint16_t* w, int64_t rows, int64_t n, int64_t ld, float* rowsum,
                                 hipStream_t s);
+
+// The 8-bit products: a = int8 codes [T][lda], or with a4 packed INT4 codes
+// (lda = n / 2 bytes) and their zero-points.
+struct W8Args {
+  const uint8_t* a;
+  int64_t lda;           // bytes
+  const float* scale;    // [T]
+  const float* zero;     // [T], a4 only
+  const int8_t* w;       // [R][ldw]
+  int64_t ldw;
+  const float* w_scale;  // [R]
+  const int32_t* w_sum;  // [R], a4 only
+  const float* bias;     // [R] or nullptr
+  void* out;             // [T][ldo]
+  int64_t ldo;
+  int32_t* partial;      // workspace
+  int out_bf16;
+  int a4;
+  int T;
+  int R;
+  int n;
+};
+constexpr int kW8MaxN = 131071;  // 128 * 128 * n stays below 2^31
+int64_t w8_workspace(int64_t tokens, int64_t n, int64_t rows, bool a4);
+const char* w8_name(const W8Args& a);
+hipError_t launch_w8(const W8Args& a, hipStream_t s);
+
+hipError_t launch_quant_int8(const uint16_t* x, int64_t tokens, int n, int64_t ld, int8_t* codes, int64_t ldc,
+                             float* scale, int32_t* sum, hipStream_t s);
+
+hipError_t launch_residual_norm(const signrot_residual_norm_args& a, hipStream_t s);
 
 }  // namespace signrot
