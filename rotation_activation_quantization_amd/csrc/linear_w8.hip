@@ -82,8 +82,11 @@ struct Tile {
 // of step s - 1 came after every wave's wait for it).
 //
 // LDS rows of 64 bytes, four 16-byte chunks: logical chunk c of row r sits at
-// physical chunk c ^ ((r >> 2) & 3), so the sixteen lanes that read one chunk
-// of sixteen consecutive rows cover the 64 banks once.  A lane (g = lane / 16,
+// physical chunk c ^ 2 ((r >> 3) & 1).  A 16-byte LDS read serves sixteen lanes
+// at a time, among them lanes 0-3 and 12-15 of one group of sixteen with 4-11 of
+// the next; rows 4 apart share banks, and this swizzle gives those lanes
+// four chunks of their own (SQ_LDS_BANK_CONFLICT reads zero; c ^ ((r >> 2) & 3)
+// cost 4 cycles a read).  A lane (g = lane / 16,
 // i = lane % 16) reads row i, chunk g of a 16-row group: k = 16 g .. 16 g + 15
 // of the step for both operands.  The packed codes (32 bytes a row) are kept
 // per 16-row group as the first 16 bytes of every row, then the second; a lane
@@ -118,7 +121,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
       wave::buffer_rsrc(a.a + static_cast<int64_t>(m0) * a.lda,
                         static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n));
   uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
-  const int chunk_w = (lane & 3) ^ (lane >> 4);  // logical chunk of the lane's slot: row lane / 4 of 16
+  const int chunk_w = (lane & 3) ^ (2 * (lane >> 5));  // logical chunk of the lane's slot: row lane / 4 of 16
   const int chunk_t = A4 ? (g & 1) : chunk_w;
 #pragma unroll
   for (int l = 0; l < C::kWLoads; ++l) {
@@ -154,9 +157,9 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   };
   constexpr int kLoads = C::kWLoads + C::kTLoads;
 
-  const int read_w = (64 * wk * FK / 4) * kStep + i * kStep + 16 * (g ^ (i >> 2));
+  const int read_w = (64 * wk * FK / 4) * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
   const int read_t = A4 ? 512 * (wt * FT) + 256 * (g >> 1) + 16 * i + 8 * (g & 1)
-                        : 16 * wt * FT * kStep + i * kStep + 16 * (g ^ (i >> 2));
+                        : 16 * wt * FT * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
   auto weight = [&](int kt, int f) {
     return *reinterpret_cast<const i32x4_t*>(lds_w + (kt & (kStages - 1)) * C::kWStage + read_w + 16 * kStep * f);
   };
