@@ -37,15 +37,10 @@ __device__ __forceinline__ float finish(const W8Args& a, int t, int k, int32_t a
 
 // ---- large tiles ------------------------------------------------------------
 //
-// Block id -> (token tile, channel tile).  Consecutive block ids go to
-// different XCDs (round-robin dispatch), so ids are first regrouped into one
-// contiguous range per XCD; inside a range, tiles run token-tile fastest over
-// groups of eight token tiles, so the work-groups resident on one XCD share a
-// few panels of tokens and weights in its L2.
-__device__ __forceinline__ void tile_of(int bid, int nblocks, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int q = nblocks >> 3, rem = nblocks & 7;
-  const int x = bid & 7, j = bid >> 3;
-  const int p = (x < rem ? x * (q + 1) : rem * (q + 1) + (x - rem) * q) + j;
+// Tile p of the order -> (token tile, channel tile): token tiles fastest over
+// groups of eight, so that neighbours share a few panels of tokens and weights
+// in an L2.
+__device__ __forceinline__ void tile_at(int p, int tiles_m, int tiles_n, int& tm, int& tn) {
   constexpr int kGroup = 8;
   const int per_group = kGroup * tiles_n;
   const int group = p / per_group;
@@ -56,30 +51,38 @@ __device__ __forceinline__ void tile_of(int bid, int nblocks, int tiles_m, int t
   tn = r / gm;
 }
 
-constexpr int kStep = 64;    // k per step, one MFMA deep
-constexpr int kStages = 4;   // LDS ring
+constexpr int kStep = 64;  // k per step, one MFMA deep
 
-// WK x WT waves of FK x FT 16 x 16 results each.
-template <bool A4, int WK, int WT, int FK, int FT>
+// WK x WT waves of FK x FT 16 x 16 results each, a ring of S steps.
+template <bool A4, int WK, int WT, int FK, int FT, int S>
 struct Tile {
   static constexpr int kWaves = WK * WT;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kBN = 16 * WK * FK;                     // channels
-  static constexpr int kBM = 16 * WT * FT;                     // tokens
-  static constexpr int kTokRow = A4 ? kStep / 2 : kStep;       // bytes of a token row and step
+  static constexpr int kBN = 16 * WK * FK;                // channels
+  static constexpr int kBM = 16 * WT * FT;                // tokens
+  static constexpr int kTokRow = A4 ? kStep / 2 : kStep;  // bytes of a token row and step
   static constexpr int kWStage = kBN * kStep;
   static constexpr int kTStage = kBM * kTokRow;
-  static constexpr int kWLoads = kWStage / 1024 / kWaves;      // LDS loads per wave and step
+  static constexpr int kWLoads = kWStage / 1024 / kWaves;  // LDS loads per wave and step
   static constexpr int kTLoads = kTStage / 1024 / kWaves;
+  static constexpr int kLoads = kWLoads + kTLoads;
   static_assert(kWLoads * 1024 * kWaves == kWStage && kTLoads * 1024 * kWaves == kTStage, "whole loads per wave");
   static_assert(FK % 4 == 0, "a lane's channels come in sixteens");
+  static_assert(S >= 4 && S * (kWStage + kTStage) <= 160 * 1024, "ring");
 };
 
 // Both operands stream global -> LDS (16 bytes a lane, no registers) through a
-// four-deep ring of k steps; one barrier a step.  Step s: the MFMAs of step s,
-// the loads of step s + 3 into the buffers step s - 1 used, and at its end the
-// first operand reads of step s + 1 (which has landed: the barrier at the end
-// of step s - 1 came after every wave's wait for it).
+// ring of S k steps; one barrier a step.  Step s: the MFMAs of step s, the
+// loads of step s + S - 1 into the buffers step s - 1 used, and towards its
+// end the first operand reads of step s + 1 (which has landed: the barrier at
+// the end of step s - 1 came after every wave's wait for it).
+//
+// A work-group takes the tiles p, p + stride, ... below `end`, and the ring
+// runs on from tile to tile: the last steps of a tile load the first ones of
+// the next, which arrive while its results are scaled and stored.
+//
+// Step 0 of a tile is the last, possibly short one of the row: its chunks
+// beyond n are read as chunk 0 and the token operand is zeroed there.
 //
 // LDS rows of 64 bytes, four 16-byte chunks: logical chunk c of row r sits at
 // physical chunk c ^ 2 ((r >> 3) & 1).  A 16-byte LDS read serves sixteen lanes
@@ -95,102 +98,134 @@ struct Tile {
 // Slot 16 f + i of a 64-channel group holds channel 16 (i / 4) + 4 f + i % 4:
 // the four 16 x 16 results f = 0 .. 3 then leave a lane sixteen consecutive
 // channels of a token, stored as whole vectors.
-template <bool A4, int WK, int WT, int FK, int FT>
+template <bool A4, int WK, int WT, int FK, int FT, int S>
 __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_n) {
-  using C = Tile<A4, WK, WT, FK, FT>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * (C::kWStage + C::kTStage)];
+  using C = Tile<A4, WK, WT, FK, FT, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * (C::kWStage + C::kTStage)];
   uint8_t* const lds_w = lds;
-  uint8_t* const lds_t = lds + kStages * C::kWStage;
+  uint8_t* const lds_t = lds + S * C::kWStage;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wid % WK, wt = wid / WK;
   const int g = lane >> 4, i = lane & 15;
 
-  int tm, tn;
-  tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
-  const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+  // Consecutive block ids go to different XCDs: each XCD takes one contiguous
+  // range of the tiles, its work-groups (gridDim / 8 of them) the tiles of that
+  // range in turn.  A grid that is not a multiple of eight is one tile each.
+  int p, end, stride;
+  {
+    const int tiles = tiles_m * tiles_n;
+    const int q = tiles >> 3, rem = tiles & 7;
+    const int x = blockIdx.x & 7;
+    const int start = x < rem ? x * (q + 1) : rem * (q + 1) + (x - rem) * q;
+    p = start + (blockIdx.x >> 3);
+    end = start + q + (x < rem ? 1 : 0);
+    stride = (gridDim.x & 7) ? tiles : gridDim.x >> 3;
+  }
   const int last = (a.n + kStep - 1) / kStep - 1;
-  const int tail = a.n - last * kStep;  // k of the short step, which comes first
+  const int tail = a.n - last * kStep;  // k of step 0
 
-  // Sources of this lane's loads (rows clamped; their results are not stored)
-  const int rows_w = min(C::kBN, a.R - n0), rows_t = min(C::kBM, a.T - m0);
-  const __amdgpu_buffer_rsrc_t src_w =
-      wave::buffer_rsrc(a.w + static_cast<int64_t>(n0) * a.ldw,
-                        static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + a.n);
-  const __amdgpu_buffer_rsrc_t src_t =
-      wave::buffer_rsrc(a.a + static_cast<int64_t>(m0) * a.lda,
-                        static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n));
-  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
+  // What is loaded next: step ik of tile src_p.  Rows beyond the tensor are
+  // clamped (their results are not stored).
   const int chunk_w = (lane & 3) ^ (2 * (lane >> 5));  // logical chunk of the lane's slot: row lane / 4 of 16
   const int chunk_t = A4 ? (g & 1) : chunk_w;
+  const uint32_t cut_w = 16 * chunk_w >= tail ? -16 * chunk_w : 0;
+  const uint32_t cut_t = (A4 ? 32 : 16) * chunk_t >= tail ? -16 * chunk_t : 0;
+  int src_p = p, ik = 0;
+  const int8_t* base_w;
+  const uint8_t* base_t;
+  uint32_t size_w, size_t_, off_w[C::kWLoads], off_t[C::kTLoads];
+  auto set_source = [&]() {
+    int tm, tn;
+    tile_at(src_p, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+    const int rows_w = min(C::kBN, a.R - n0), rows_t = min(C::kBM, a.T - m0);
+    base_w = a.w + static_cast<int64_t>(n0) * a.ldw;
+    base_t = a.a + static_cast<int64_t>(m0) * a.lda;
+    size_w = static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + a.n;
+    size_t_ = static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n);
 #pragma unroll
-  for (int l = 0; l < C::kWLoads; ++l) {
-    const int slot = 16 * (C::kWLoads * wid + l) + (lane >> 2);
-    const int at = slot & 15;
-    const int ch = (slot & ~63) + 16 * (at >> 2) + 4 * ((slot >> 4) & 3) + (at & 3);
-    off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + 16 * chunk_w;
-  }
+    for (int l = 0; l < C::kWLoads; ++l) {
+      const int slot = 16 * (C::kWLoads * wid + l) + (lane >> 2);
+      const int at = slot & 15;
+      const int ch = (slot & ~63) + 16 * (at >> 2) + 4 * ((slot >> 4) & 3) + (at & 3);
+      off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + 16 * chunk_w + cut_w;
+    }
 #pragma unroll
-  for (int l = 0; l < C::kTLoads; ++l) {
-    const int row = A4 ? 32 * (C::kTLoads * wid + l) + 16 * (lane >> 5) + i : 16 * (C::kTLoads * wid + l) + (lane >> 2);
-    off_t[l] = static_cast<uint32_t>(min(row, rows_t - 1)) * static_cast<uint32_t>(a.lda) + 16 * chunk_t;
-  }
-  // Load l of step kt.  Step 0 is the last 64 k of the row, chunks beyond n
-  // read as chunk 0; step kt > 0 is k = 64 (kt - 1) ..  Every step issues the
-  // same number of loads (clamped to the last one at the end), so the vmcnt
-  // threshold is exact.
-  auto issue = [&](int kt, int l) {
-    const int ks = kt == 0 ? last : max(min(kt, last), 1) - 1;
-    const int buf = kt & (kStages - 1);
-    if (l < C::kWLoads) {
-      const uint32_t at = kt == 0 && 16 * chunk_w >= tail ? off_w[l] - 16 * chunk_w : off_w[l];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          src_w, (__attribute__((address_space(3))) void*)(lds_w + buf * C::kWStage + 1024 * (C::kWLoads * wid + l)), 16,
-          at, kStep * ks, 0, 0);
-    } else {
-      const int j = l - C::kWLoads;
-      const uint32_t at = kt == 0 && (A4 ? 32 : 16) * chunk_t >= tail ? off_t[j] - 16 * chunk_t : off_t[j];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          src_t, (__attribute__((address_space(3))) void*)(lds_t + buf * C::kTStage + 1024 * (C::kTLoads * wid + j)), 16,
-          at, C::kTokRow * ks, 0, 0);
+    for (int l = 0; l < C::kTLoads; ++l) {
+      const int r =
+          A4 ? 32 * (C::kTLoads * wid + l) + 16 * (lane >> 5) + i : 16 * (C::kTLoads * wid + l) + (lane >> 2);
+      off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda) + 16 * chunk_t + cut_t;
     }
   };
-  constexpr int kLoads = C::kWLoads + C::kTLoads;
+  int wr_w = 0, wr_t = 0;  // ring position that is filled
+  int ks = last;           // 64 k-block of step ik
+  auto issue = [&](int l) {
+    if (l < C::kWLoads) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wave::buffer_rsrc(base_w, size_w),
+          (__attribute__((address_space(3))) void*)(lds_w + wr_w + 1024 * (C::kWLoads * wid + l)), 16,
+          off_w[l], kStep * ks, 0, 0);
+    } else {
+      const int j = l - C::kWLoads;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wave::buffer_rsrc(base_t, size_t_),
+          (__attribute__((address_space(3))) void*)(lds_t + wr_t + 1024 * (C::kTLoads * wid + j)), 16,
+          off_t[j], C::kTokRow * ks, 0, 0);
+    }
+  };
+  // Past the last tile the loads go on with that tile's: every step issues the
+  // same number, so the vmcnt threshold is exact.
+  auto issued = [&]() {
+    wr_w = wr_w == (S - 1) * C::kWStage ? 0 : wr_w + C::kWStage;
+    wr_t = wr_t == (S - 1) * C::kTStage ? 0 : wr_t + C::kTStage;
+    if (ik == 0 && tail < kStep) {
+#pragma unroll
+      for (int l = 0; l < C::kWLoads; ++l) off_w[l] -= cut_w;
+#pragma unroll
+      for (int l = 0; l < C::kTLoads; ++l) off_t[l] -= cut_t;
+    }
+    ik = __builtin_amdgcn_readfirstlane(ik == last ? 0 : ik + 1);
+    if (ik == 0) {
+      src_p = src_p + stride < end ? src_p + stride : src_p;
+      set_source();
+    }
+    ks = __builtin_amdgcn_readfirstlane(ik == 0 ? last : ik - 1);
+  };
 
   const int read_w = (64 * wk * FK / 4) * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
   const int read_t = A4 ? 512 * (wt * FT) + 256 * (g >> 1) + 16 * i + 8 * (g & 1)
                         : 16 * wt * FT * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
-  auto weight = [&](int kt, int f) {
-    return *reinterpret_cast<const i32x4_t*>(lds_w + (kt & (kStages - 1)) * C::kWStage + read_w + 16 * kStep * f);
+  int rd_w = 0, rd_t = 0;  // ring position that is multiplied
+  auto weight = [&](int at, int f) {
+    return *reinterpret_cast<const i32x4_t*>(lds_w + at + read_w + 16 * kStep * f);
   };
 
   i32x4_t acc[FK][FT];
-#pragma unroll
-  for (int f = 0; f < FK; ++f)
-#pragma unroll
-    for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
-
   i32x4_t tok[2][FT];  // token operands of this and the next step
   wave::u32x2_t code[FT];
-  auto read_token = [&](int kt, int j, i32x4_t& dst) {
-    const uint8_t* p = lds_t + (kt & (kStages - 1)) * C::kTStage + read_t;
+  auto read_token = [&](int at, int j, i32x4_t& dst) {
+    const uint8_t* s = lds_t + at + read_t;
     if (A4)
-      code[j] = *reinterpret_cast<const wave::u32x2_t*>(p + 512 * j);
+      code[j] = *reinterpret_cast<const wave::u32x2_t*>(s + 512 * j);
     else
-      dst = *reinterpret_cast<const i32x4_t*>(p + 16 * kStep * j);
+      dst = *reinterpret_cast<const i32x4_t*>(s + 16 * kStep * j);
   };
   auto widen = [&](int j, i32x4_t& dst) {
     uint32_t w0, w1, w2, w3;
     widen8(code[j][0], w0, w1);
     widen8(code[j][1], w2, w3);
     dst = i32x4_t{static_cast<int>(w0), static_cast<int>(w1), static_cast<int>(w2), static_cast<int>(w3)};
+    asm volatile("" : "+v"(dst));  // here, not where the next step uses it
   };
 
+  set_source();
+  for (int s = 0; s < S - 1; ++s) {
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
-#pragma unroll
-    for (int l = 0; l < kLoads; ++l) issue(s, l);
-  wave::wait_vmcnt<kLoads>();
+    for (int l = 0; l < C::kLoads; ++l) issue(l);
+    issued();
+  }
+  wave::wait_vmcnt<(S - 3) * C::kLoads>();
   __builtin_amdgcn_s_barrier();
   i32x4_t wf[FK + 2];
   wf[0] = weight(0, 0);
@@ -199,10 +234,11 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   for (int j = 0; j < FT; ++j) {
     read_token(0, j, tok[0][j]);
     if (A4) widen(j, tok[0][j]);
-    if (16 * g >= tail) tok[0][j] = i32x4_t{0, 0, 0, 0};
   }
 
-  auto step = [&](int kt, i32x4_t (&now)[FT], i32x4_t (&next)[FT]) {
+  auto step = [&](i32x4_t (&now)[FT], i32x4_t (&next)[FT]) {
+    const int nx_w = rd_w == (S - 1) * C::kWStage ? 0 : rd_w + C::kWStage;
+    const int nx_t = rd_t == (S - 1) * C::kTStage ? 0 : rd_t + C::kTStage;
 #pragma unroll
     for (int f = 0; f < FK; ++f) {
       // The reads follow the block's first MFMA: the wait before that one is
@@ -210,98 +246,126 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
       acc[f][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[f], now[0], acc[f][0], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
       // two reads ahead, the last two from the next step
-      wf[f + 2] = f + 2 < FK ? weight(kt, f + 2) : weight(kt + 1, f + 2 - FK);
+      wf[f + 2] = f + 2 < FK ? weight(rd_w, f + 2) : weight(nx_w, f + 2 - FK);
+      // the next step's tokens: packed codes are read over the first half of
+      // the blocks and widened, between the MFMAs, over the second
+      constexpr int kOver = A4 ? FK / 2 : FK;
+      if (f < kOver) {
 #pragma unroll
-      for (int j = f * FT / FK; j < (f + 1) * FT / FK; ++j) {
-        if (A4) {
-          if (j > 0) widen(j - 1, next[j - 1]);
-        }
-        read_token(kt + 1, j, next[j]);
+        for (int j = f * FT / kOver; j < (f + 1) * FT / kOver; ++j) read_token(nx_t, j, next[j]);
+      } else {
+#pragma unroll
+        for (int j = (f - kOver) * FT / kOver; j < (f - kOver + 1) * FT / kOver; ++j) widen(j, next[j]);
       }
 #pragma unroll
-      for (int l = f * kLoads / FK; l < (f + 1) * kLoads / FK; ++l) issue(kt + 3, l);
+      for (int l = f * C::kLoads / FK; l < (f + 1) * C::kLoads / FK; ++l) issue(l);
 #pragma unroll
       for (int j = 1; j < FT; ++j)
         acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[f], now[j], acc[f][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (A4) widen(FT - 1, next[FT - 1]);
     wf[0] = wf[FK];
     wf[1] = wf[FK + 1];
-    wave::wait_vmcnt<kLoads>();
+    rd_w = nx_w;
+    rd_t = nx_t;
+    issued();
+    wave::wait_vmcnt<(S - 3) * C::kLoads>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  int kt = 0;
-  for (; kt < last; kt += 2) {
-    step(kt, tok[0], tok[1]);
-    step(kt + 1, tok[1], tok[0]);
-  }
-  if (kt == last) step(kt, tok[0], tok[1]);
-  wave::wait_vmcnt<0>();
 
-  // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.
   const bool wide = (a.ldo % 8 == 0) && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  for (; p < end; p += stride) {
 #pragma unroll
-  for (int q = 0; q < FK / 4; ++q) {
-    const int k0 = n0 + 16 * wk * FK + 64 * q + 16 * g;
-    if (k0 >= a.R) continue;
-    const bool whole = wide && k0 + 16 <= a.R;
-    float v[16], b[16], ws[16];
+    for (int f = 0; f < FK; ++f)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int k = min(k0 + e, a.R - 1);
-      v[e] = a.w_scale[k];
-      b[e] = a.bias ? a.bias[k] : 0.f;
-      ws[e] = A4 ? static_cast<float>(a.w_sum[k]) : 0.f;
+      for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
+    if (tail < kStep) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        if (16 * g >= tail) tok[0][j] = i32x4_t{0, 0, 0, 0};
     }
+    for (int kt = 0; kt < last; kt += 2) {
+      step(tok[0], tok[1]);
+      step(tok[1], tok[0]);
+    }
+    if ((last & 1) == 0) {
+      step(tok[0], tok[1]);
 #pragma unroll
-    for (int j = 0; j < FT; ++j) {
-      const int t = m0 + 16 * (wt * FT + j) + i;
-      if (t >= a.T) continue;
-      const float s = a.scale[t], z = A4 ? a.zero[t] : 0.f;
-      float o[16];
+      for (int j = 0; j < FT; ++j) tok[0][j] = tok[1][j];
+    }
+
+    // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.
+    int tm, tn;
+    tile_at(p, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+#pragma unroll
+    for (int q = 0; q < FK / 4; ++q) {
+      const int k0 = n0 + 16 * wk * FK + 64 * q + 16 * g;
+      if (k0 >= a.R) continue;
+      const bool whole = wide && k0 + 16 <= a.R;
+      float v[16], b[16], ws[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        float x = static_cast<float>(acc[4 * q + (e >> 2)][j][e & 3]);
-        if (A4) x = fmaf(-z, ws[e], x);
-        x = x * s * v[e];
-        o[e] = a.bias ? x + b[e] : x;
+        const int k = min(k0 + e, a.R - 1);
+        v[e] = a.w_scale[k];
+        ws[e] = A4 ? static_cast<float>(a.w_sum[k]) : 0.f;
+        b[e] = 0.f;
       }
-      const int64_t at = static_cast<int64_t>(t) * a.ldo + k0;
-      if (whole && a.out_bf16) {
-        uint32_t h[8];
+      if (a.bias) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          h[e] = row::f32_bf16(o[2 * e]) | static_cast<uint32_t>(row::f32_bf16(o[2 * e + 1])) << 16;
-        wave::u32x4_t* p = reinterpret_cast<wave::u32x4_t*>(static_cast<uint16_t*>(a.out) + at);
-        p[0] = wave::u32x4_t{h[0], h[1], h[2], h[3]};
-        p[1] = wave::u32x4_t{h[4], h[5], h[6], h[7]};
-      } else if (whole) {
-        wave::f32x4_t* p = reinterpret_cast<wave::f32x4_t*>(static_cast<float*>(a.out) + at);
+        for (int e = 0; e < 16; ++e) b[e] = a.bias[min(k0 + e, a.R - 1)];
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = wave::f32x4_t{o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]};
-      } else {
+      for (int j = 0; j < FT; ++j) {
+        const int t = m0 + 16 * (wt * FT + j) + i;
+        if (t >= a.T) continue;
+        const float sc = a.scale[t], z = A4 ? a.zero[t] : 0.f;
+        float o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (k0 + e < a.R) row::store_elem(a.out, at + e, o[e], a.out_bf16);
+        for (int e = 0; e < 16; ++e) {
+          float x = static_cast<float>(acc[4 * q + (e >> 2)][j][e & 3]);
+          if (A4) x = fmaf(-z, ws[e], x);
+          o[e] = fmaf(x * sc, v[e], b[e]);
+        }
+        const int64_t at = static_cast<int64_t>(t) * a.ldo + k0;
+        if (whole && a.out_bf16) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[e] = row::f32_bf16(o[2 * e]) | static_cast<uint32_t>(row::f32_bf16(o[2 * e + 1])) << 16;
+          wave::u32x4_t* out = reinterpret_cast<wave::u32x4_t*>(static_cast<uint16_t*>(a.out) + at);
+          out[0] = wave::u32x4_t{h[0], h[1], h[2], h[3]};
+          out[1] = wave::u32x4_t{h[4], h[5], h[6], h[7]};
+        } else if (whole) {
+          wave::f32x4_t* out = reinterpret_cast<wave::f32x4_t*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = wave::f32x4_t{o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (k0 + e < a.R) row::store_elem(a.out, at + e, o[e], a.out_bf16);
+        }
       }
     }
   }
+  wave::wait_vmcnt<0>();
 }
 
-template <bool A4, int WK, int WT, int FK, int FT>
+template <bool A4, int WK, int WT, int FK, int FT, int S>
 __global__ __launch_bounds__(64 * WK * WT) __attribute__((amdgpu_waves_per_eu(WK * WT / 4)))
 void w8_tile_kernel(W8Args a, int tiles_m, int tiles_n) {
-  w8_tile<A4, WK, WT, FK, FT>(a, tiles_m, tiles_n);
+  w8_tile<A4, WK, WT, FK, FT, S>(a, tiles_m, tiles_n);
 }
 
-template <bool A4, int WK, int WT, int FK, int FT>
+template <bool A4, int WK, int WT, int FK, int FT, int S>
 void run_tile(const W8Args& a, hipStream_t s) {
-  using C = Tile<A4, WK, WT, FK, FT>;
+  using C = Tile<A4, WK, WT, FK, FT, S>;
   const int tiles_m = (a.T + C::kBM - 1) / C::kBM, tiles_n = (a.R + C::kBN - 1) / C::kBN;
-  w8_tile_kernel<A4, WK, WT, FK, FT><<<dim3(static_cast<unsigned>(tiles_m * tiles_n)), dim3(C::kThreads), 0, s>>>(
-      a, tiles_m, tiles_n);
+  const int tiles = tiles_m * tiles_n;
+  const int cus = device_cu_count() & ~7;
+  w8_tile_kernel<A4, WK, WT, FK, FT, S><<<dim3(static_cast<unsigned>(cus > 0 && tiles > cus ? cus : tiles)),
+                                          dim3(C::kThreads), 0, s>>>(a, tiles_m, tiles_n);
 }
 
 // Rows that start on 16-byte boundaries and end on one.
@@ -416,9 +480,9 @@ hipError_t launch_w8(const W8Args& all, hipStream_t s) {
     a.out = static_cast<uint8_t*>(a.out) + t * a.ldo * (a.out_bf16 ? 2 : 4);
     if (aligned_rows(a) && a.T > 64) {
       if (a.a4)
-        run_tile<true, 2, 4, 8, 4>(a, s);
+        run_tile<true, 2, 4, 8, 4, 4>(a, s);
       else
-        run_tile<false, 2, 4, 8, 4>(a, s);
+        run_tile<false, 4, 2, 4, 8, 4>(a, s);
       continue;
     }
     const dim3 grid(static_cast<unsigned>(((a.T + kAnyTile - 1) / kAnyTile) * tiles_n)), block(256);
