@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsignrot.so")
@@ -186,10 +187,20 @@ def debug_h28():
     return [list(buf[r * 28:(r + 1) * 28]) for r in range(28)]
 
 
-def _stream_of(t):
-    import torch
+_raw_stream = None
 
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+def _stream_of(t):
+    """The handle of the current stream on t's device: without the Stream
+    object of the public call (2 us of a small call's 7) where torch has the
+    direct one."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.device.index)
 
 
 def _rows(x):
@@ -426,9 +437,9 @@ def _matrix(v, name, rows, n, dtype, device):
 
 
 def _vector(v, name, size, dtype, device):
-    """Pointer of a contiguous vector of `size` entries, or None for None."""
+    """Pointer of a contiguous vector of `size` entries, 0 for None."""
     if v is None:
-        return None
+        return 0
     if v.dtype is not dtype or v.numel() != size or v.device != device or not v.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {size} entries on {device}")
     return v.data_ptr()
@@ -451,29 +462,33 @@ def signrot_quant_int8(x, sums: bool = False, out=None):
     ptr, ld = _matrix(x, "x", None, None, torch.bfloat16, device)
     t, n = x.shape
     if out is None:
-        out = (torch.empty((t, n), dtype=torch.int8, device=device),
-               torch.empty(t, dtype=torch.float32, device=device))
-        if sums:
-            out += (torch.empty(t, dtype=torch.int32, device=device),)
-    elif len(out) < (3 if sums else 2):
-        raise ValueError("out must hold (codes, scale[, sum])")
-    codes, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
-    check(lib().signrot_quant_int8(ptr, t, n, ld, codes, ldc, _vector(out[1], "scale", t, torch.float32, device),
-                                   _vector(out[2], "sum", t, torch.int32, device) if sums else None, _stream_of(x)),
+        codes, scale = torch.empty((t, n), dtype=torch.int8, device=device), torch.empty(t, device=device,
+                                                                                         dtype=torch.float32)
+        out = (codes, scale, torch.empty(t, dtype=torch.int32, device=device)) if sums else (codes, scale)
+        qptr, ldc, sptr = codes.data_ptr(), n, scale.data_ptr()
+    else:
+        out = tuple(out[:3 if sums else 2])
+        if len(out) < (3 if sums else 2):
+            raise ValueError("out must hold (codes, scale[, sum])")
+        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
+        sptr = _vector(out[1], "scale", t, torch.float32, device)
+    check(lib().signrot_quant_int8(ptr, t, n, ld, qptr, ldc, sptr,
+                                   _vector(out[2], "sum", t, torch.int32, device) if sums else 0, _stream_of(x)),
           "signrot_quant_int8")
-    return tuple(out[:3 if sums else 2])
+    return out
 
 
 def _product_out(out, dtype, t, rows, device):
+    """(out, its type, pointer, row stride), allocated when the caller gave none."""
     import torch
 
     if out is None:
         out = torch.empty((t, rows), dtype=torch.bfloat16 if dtype is None else dtype, device=device)
-    elif dtype is not None and out.dtype is not dtype:
+        return out, _type_of(out.dtype, "out"), out.data_ptr(), rows
+    if dtype is not None and out.dtype is not dtype:
         raise ValueError(f"out is {out.dtype}, dtype {dtype}")
-    kind = _type_of(out.dtype, "out")
     ptr, ldo = _matrix(out, "out", t, rows, out.dtype, device)
-    return out, kind, ptr, ldo
+    return out, _type_of(out.dtype, "out"), ptr, ldo
 
 
 def _workspace(size, device):
@@ -481,7 +496,7 @@ def _workspace(size, device):
     import torch
 
     if size <= 0:
-        return None, 0, None
+        return 0, 0, None
     w = torch.empty(size, dtype=torch.uint8, device=device)
     return w.data_ptr(), size, w
 
@@ -554,6 +569,8 @@ def int4_w8_linear_kernel_name(codes, w) -> str | None:
 
 
 class _ResidualNormArgs(ctypes.Structure):
+    """signrot_residual_norm_args."""
+
     _fields_ = [(name, kind) for names, kind in (
         (("tokens", "n"), ctypes.c_int64), (("h",), ctypes.c_void_p), (("ldh",), ctypes.c_int64),
         (("y",), ctypes.c_void_p), (("ldy",), ctypes.c_int64), (("h_out",), ctypes.c_void_p),
@@ -566,10 +583,16 @@ class _ResidualNormArgs(ctypes.Structure):
         (("post_norm", "pre_norm", "h_type", "param_type"), ctypes.c_int32)) for name in names]
 
 
+# the same struct packed in one call (None is no pointer: 0)
+_pack_norm_args = struct.Struct("@" + "".join(
+    {ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f", ctypes.c_int32: "i"}[kind]
+    for _, kind in _ResidualNormArgs._fields_)).pack
+
+
 def _modulation(v, name, t, n, index, dtype, device):
     """(pointer, stride, rows) of a gate or modulation: [n] shared by all rows, or [m, n]."""
     if v is None:
-        return None, 0, None
+        return 0, 0, None
     if v.dim() == 1:
         return _vector(v, name, n, dtype, device), 0, None
     ptr, step = _matrix(v, name, None, n, dtype, device)
@@ -579,14 +602,15 @@ def _modulation(v, name, t, n, index, dtype, device):
 
 
 def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
-                   mod_scale, mod_shift, mod_index, h_out, u, codes, code_scale, where):
+                   mod_scale, mod_shift, mod_index, h_out, out, codes, where):
+    """Checks, allocates what the caller did not give and launches; `codes`: out is (codes, scale), not u."""
     import torch
 
     device = _on_gpu(h, "h")
     h_type = _type_of(h.dtype, "h")
-    t, n = h.shape if h.dim() == 2 else (0, 0)
     hptr, ldh = _matrix(h, "h", None, None, h.dtype, device)
-    yptr, ldy = (None, 0) if y is None else _matrix(y, "y", t, n, torch.bfloat16, device)
+    t, n = h.shape
+    yptr, ldy = (0, 0) if y is None else _matrix(y, "y", t, n, torch.bfloat16, device)
     post_norm = norm if post_norm is None else post_norm
     if norm not in _NORMS or post_norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}")
@@ -596,25 +620,43 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
             param = v.dtype
             break
     p_type = _type_of(param, "the norm's parameters")
-    gptr, ldg, grows = _modulation(gate, "gate", t, n, mod_index, param, device)
-    mptr, ldm, mrows = _modulation(mod_scale, "mod_scale", t, n, mod_index, param, device)
-    cptr, ldm2, crows = _modulation(mod_shift, "mod_shift", t, n, mod_index, param, device)
-    if mptr is None:
-        ldm = ldm2
-    elif cptr is not None and ldm != ldm2:
-        raise ValueError("mod_scale and mod_shift must have the same row stride")
-    per_row = [r for r in (grows, mrows, crows) if r is not None]
-    hoptr, ldho = (None, 0) if h_out is None else _matrix(h_out, "h_out", t, n, h.dtype, device)
-    uptr, ldu = (None, 0) if u is None else _matrix(u, "u", t, n, torch.bfloat16, device)
-    qptr, ldc = (None, 0) if codes is None else _matrix(codes, "codes", t, n, torch.int8, device)
-    args = _ResidualNormArgs(
-        t, n, hptr, ldh, yptr, ldy, hoptr, ldho, uptr, ldu, qptr, ldc,
-        _vector(code_scale, "scale", t, torch.float32, device),
+    gptr, mptr, cptr, ldg, ldm, mod_rows = 0, 0, 0, 0, 0, 0
+    if gate is not None or mod_scale is not None or mod_shift is not None:
+        gptr, ldg, grows = _modulation(gate, "gate", t, n, mod_index, param, device)
+        mptr, ldm, mrows = _modulation(mod_scale, "mod_scale", t, n, mod_index, param, device)
+        cptr, ldm2, crows = _modulation(mod_shift, "mod_shift", t, n, mod_index, param, device)
+        if not mptr:
+            ldm = ldm2
+        elif cptr and ldm != ldm2:
+            raise ValueError("mod_scale and mod_shift must have the same row stride")
+        mod_rows = min((r for r in (grows, mrows, crows) if r is not None), default=0)
+    if h_out is None:
+        h_out = torch.empty((t, n), dtype=h.dtype, device=device)
+        hoptr, ldho = h_out.data_ptr(), n
+    else:
+        hoptr, ldho = _matrix(h_out, "h_out", t, n, h.dtype, device)
+    uptr, ldu, qptr, ldc, sptr = 0, 0, 0, 0, 0
+    if not codes:
+        if out is None:
+            out = torch.empty((t, n), dtype=torch.bfloat16, device=device)
+            uptr, ldu = out.data_ptr(), n
+        else:
+            uptr, ldu = _matrix(out, "u", t, n, torch.bfloat16, device)
+    elif out is None:
+        out = (torch.empty((t, n), dtype=torch.int8, device=device),
+               torch.empty(t, dtype=torch.float32, device=device))
+        qptr, ldc, sptr = out[0].data_ptr(), n, out[1].data_ptr()
+    else:
+        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
+        sptr = _vector(out[1], "scale", t, torch.float32, device)
+    args = _pack_norm_args(
+        t, n, hptr, ldh, yptr, ldy, hoptr, ldho, uptr, ldu, qptr, ldc, sptr,
         _vector(post_weight, "post_weight", n, param, device), _vector(post_bias, "post_bias", n, param, device),
         gptr, ldg, _vector(weight, "weight", n, param, device), _vector(bias, "bias", n, param, device),
-        mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, device), min(per_row) if per_row else 0,
+        mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, device), mod_rows,
         alpha, beta, eps if post_eps is None else post_eps, eps, _NORMS[post_norm], _NORMS[norm], h_type, p_type)
-    check(lib().signrot_residual_norm(ctypes.addressof(args), _stream_of(h)), where)
+    check(lib().signrot_residual_norm(args, _stream_of(h)), where)
+    return h_out, out
 
 
 def signrot_residual_norm(h, y=None, norm: str = "rms", post_norm: str | None = None, eps: float = 1e-6,
@@ -632,15 +674,8 @@ def signrot_residual_norm(h, y=None, norm: str = "rms", post_norm: str | None = 
     per token, or one per sequence picked by mod_index (int32 [T]); all of
     them bf16, or all f32.  Returns (h' of h's type, u bf16).  h_out may be h,
     to update the stream in place; `out` may pass u's tensor."""
-    import torch
-
-    if h_out is None:
-        h_out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    if out is None:
-        out = torch.empty(h.shape, dtype=torch.bfloat16, device=h.device)
-    _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
-                   mod_scale, mod_shift, mod_index, h_out, out, None, None, "signrot_residual_norm")
-    return h_out, out
+    return _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight,
+                          bias, mod_scale, mod_shift, mod_index, h_out, out, False, "signrot_residual_norm")
 
 
 def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: str | None = None, eps: float = 1e-6,
@@ -650,16 +685,10 @@ def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: st
     """signrot_residual_norm with u quantized as signrot_quant_int8 does, from
     its binary32 values: returns (h', codes int8 [T, n], scale f32 [T]).
     `out` may pass (codes, scale)."""
-    import torch
-
-    if h_out is None:
-        h_out = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    if out is None:
-        out = (torch.empty(h.shape, dtype=torch.int8, device=h.device),
-               torch.empty(h.shape[0], dtype=torch.float32, device=h.device))
-    _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
-                   mod_scale, mod_shift, mod_index, h_out, None, out[0], out[1], "signrot_residual_norm")
-    return h_out, out[0], out[1]
+    h_out, (codes, scale) = _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha,
+                                           beta, weight, bias, mod_scale, mod_shift, mod_index, h_out, out, True,
+                                           "signrot_residual_norm")
+    return h_out, codes, scale
 
 
 def signrot_stream_ceiling(x, out=None):

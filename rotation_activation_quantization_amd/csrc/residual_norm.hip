@@ -15,94 +15,313 @@ namespace {
 
 using NormArgs = signrot_residual_norm_args;
 
-constexpr int kThreads = 256;
+// Row of the modulations that token t takes.
+__device__ __forceinline__ int64_t modulation_row(const NormArgs& a, int64_t t) {
+  if (!a.mod_index) return t;
+  const int64_t i = a.mod_index[t];
+  return i < 0 ? 0 : (i >= a.mod_rows ? a.mod_rows - 1 : i);
+}
+
+// Rows of whole 16-byte chunks: one work-group per row, the row in registers
+// (V chunks of eight values a thread).  y and h are read once, h' and u
+// written once; the statistics are one or two reductions each (a LayerNorm's
+// centred sum of squares follows its mean, so that it cannot cancel).
+template <int V, bool HB>
+__global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
+  __shared__ float sh[4][16];
+  __shared__ uint32_t sh_top[16];
+  const int n = static_cast<int>(a.n);
+  const float inv_n = 1.f / static_cast<float>(n);
+  const int pb = a.param_type == SIGNROT_BF16;
+  const int chunks = n >> 3, step = blockDim.x;
+  const int tid = threadIdx.x;
+
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const int64_t r = modulation_row(a, t);
+    const int64_t gate_at = a.ldg ? r * a.ldg : 0, mod_at = a.ldm ? r * a.ldm : 0;
+    // the rows as they are stored; zeros beyond the last chunk
+    row::u32x4_t hw[V][HB ? 1 : 2], yw[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tid + v * step;
+      yw[v] = row::u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < (HB ? 1 : 2); ++i) hw[v][i] = row::u32x4_t{0, 0, 0, 0};
+      if (c < chunks) {
+        if (a.y) yw[v] = reinterpret_cast<const row::u32x4_t*>(static_cast<const uint16_t*>(a.y) + t * a.ldy)[c];
+        const uint8_t* hr = static_cast<const uint8_t*>(a.h) + t * a.ldh * (HB ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < (HB ? 1 : 2); ++i)
+          hw[v][i] = reinterpret_cast<const row::u32x4_t*>(hr)[(HB ? 1 : 2) * c + i];
+      }
+    }
+    // mean and 1 / sqrt(var + eps) of the row whose chunk v is get(v)
+    auto stats = [&](auto get, int kind, float eps, float* sh1, float* sh2, float& mean, float& inv) {
+      mean = 0.f;
+      inv = 1.f;
+      if (kind == SIGNROT_NORM_NONE) return;
+      if (kind == SIGNROT_NORM_LAYER) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float x[8];
+          get(v, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s += x[e];
+        }
+        mean = row::block_reduce(s, sh1) * inv_n;
+      }
+      float q = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (tid + v * step >= chunks) continue;
+        float x[8];
+        get(v, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = x[e] - mean;
+          q = fmaf(d, d, q);
+        }
+      }
+      inv = 1.f / sqrtf(row::block_reduce(q, sh2) * inv_n + eps);
+    };
+    // x = (x - mean) inv w + b on the chunk from element j on
+    auto affine = [&](float (&x)[8], int kind, float mean, float inv, const void* w, const void* b, int j) {
+      if (kind == SIGNROT_NORM_NONE) return;
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (x[e] - mean) * inv;
+      if (w) {
+        row::load8(w, j, pb, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= p[e];
+      }
+      if (b) {
+        row::load8(b, j, pb, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += p[e];
+      }
+    };
+
+    float mean, inv, h[V][8];
+    if (a.y)
+      stats([&](int v, float (&x)[8]) { row::widen_bf16(yw[v], x); }, a.post_norm, a.eps_post, sh[0], sh[1], mean, inv);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tid + v * step;
+      if (HB) {
+        row::widen_bf16(hw[v][0], h[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] = __uint_as_float(hw[v][HB ? 0 : e >> 2][e & 3]);
+      }
+      if (c >= chunks) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] *= a.beta;
+      if (a.y) {
+        float y[8];
+        row::widen_bf16(yw[v], y);
+        affine(y, a.post_norm, mean, inv, a.post_weight, a.post_bias, 8 * c);
+        if (a.gate) {
+          float p[8];
+          row::load8(a.gate, gate_at + 8 * c, pb, p);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] *= p[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] = fmaf(a.alpha, y[e], h[v][e]);
+      }
+      if (a.h_out) {
+        if (HB) {
+          row::u32x4_t w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = row::pack_bf16(h[v][2 * e], h[v][2 * e + 1]);
+          *reinterpret_cast<row::u32x4_t*>(static_cast<uint16_t*>(a.h_out) + t * a.ldho + 8 * c) = w;
+        } else {
+          float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.h_out) + t * a.ldho + 8 * c);
+          p[0] = make_float4(h[v][0], h[v][1], h[v][2], h[v][3]);
+          p[1] = make_float4(h[v][4], h[v][5], h[v][6], h[v][7]);
+        }
+      }
+    }
+    if (a.u || a.codes) {
+      stats(
+          [&](int v, float (&x)[8]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = h[v][e];
+          },
+          a.pre_norm, a.eps_pre, sh[2], sh[3], mean, inv);
+      uint32_t top = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = tid + v * step;
+        if (c >= chunks) continue;
+        affine(h[v], a.pre_norm, mean, inv, a.pre_weight, a.pre_bias, 8 * c);
+        float p[8];
+        if (a.mod_scale) {
+          row::load8(a.mod_scale, mod_at + 8 * c, pb, p);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[v][e] *= 1.f + p[e];
+        }
+        if (a.mod_shift) {
+          row::load8(a.mod_shift, mod_at + 8 * c, pb, p);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[v][e] += p[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = row::join(top, row::abs_bits(h[v][e]));
+        if (a.u) {
+          row::u32x4_t w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = row::pack_bf16(h[v][2 * e], h[v][2 * e + 1]);
+          *reinterpret_cast<row::u32x4_t*>(static_cast<uint16_t*>(a.u) + t * a.ldu + 8 * c) = w;
+        }
+      }
+      if (a.codes) {
+        const float m = __uint_as_float(row::block_reduce(top, sh_top));
+        const row::Codes code(m);
+        if (tid == 0) a.code_scale[t] = row::scale_of(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int c = tid + v * step;
+          if (c >= chunks) continue;
+          row::u32x2_t q;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            q[e] = row::pack_codes(code.bits(h[v][4 * e]), code.bits(h[v][4 * e + 1]), code.bits(h[v][4 * e + 2]),
+                                   code.bits(h[v][4 * e + 3]));
+          *reinterpret_cast<row::u32x2_t*>(a.codes + t * a.ldc + 8 * c) = q;
+        }
+      }
+    }
+    if (t + gridDim.x < a.tokens) __syncthreads();  // the reductions' words are used again
+  }
+}
 
 // Any width, stride and alignment: one work-group per row, every pass
 // recomputes the row's values from memory (the row is in cache after the
 // first).  Thread i owns the elements i, i + 256, ... in every pass, so h_out
 // may be h.
-__global__ __launch_bounds__(kThreads) void residual_norm_any_kernel(NormArgs a) {
-  __shared__ float sh[kThreads / 64];
-  __shared__ uint32_t shm[kThreads / 64];
+constexpr int kAnyThreads = 256;
+__global__ __launch_bounds__(kAnyThreads) void residual_norm_any_kernel(NormArgs a) {
+  __shared__ float sh[4][16];
+  __shared__ uint32_t sh_top[16];
   const int n = static_cast<int>(a.n);
   const float inv_n = 1.f / static_cast<float>(n);
   const int hb = a.h_type == SIGNROT_BF16, pb = a.param_type == SIGNROT_BF16;
   const int tid = threadIdx.x;
+
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-  int64_t r = t;
-  if (a.mod_index) {
-    const int64_t i = a.mod_index[t];
-    r = i < 0 ? 0 : (i >= a.mod_rows ? a.mod_rows - 1 : i);
-  }
-  const int64_t gate_at = a.ldg ? r * a.ldg : 0, mod_at = a.ldm ? r * a.ldm : 0;
-  const int64_t h_at = t * a.ldh, y_at = t * a.ldy;
+    const int64_t r = modulation_row(a, t);
+    const int64_t gate_at = a.ldg ? r * a.ldg : 0, mod_at = a.ldm ? r * a.ldm : 0;
+    const int64_t h_at = t * a.ldh, y_at = t * a.ldy;
 
-  // mean and 1 / sqrt(var + eps) of the n values of f
-  auto stats = [&](auto f, int kind, float eps, float& mean, float& inv) {
-    mean = 0.f;
-    inv = 1.f;
-    if (kind == SIGNROT_NORM_NONE) return;
-    if (kind == SIGNROT_NORM_LAYER) {
-      float s = 0.f;
-      for (int j = tid; j < n; j += kThreads) s += f(j);
-      mean = row::block_reduce(s, sh) * inv_n;
-    }
-    float q = 0.f;
-    for (int j = tid; j < n; j += kThreads) {
-      const float d = f(j) - mean;
-      q = fmaf(d, d, q);
-    }
-    inv = 1.f / sqrtf(row::block_reduce(q, sh) * inv_n + eps);
-  };
-  auto affine = [&](float v, int kind, float mean, float inv, const void* w, const void* b, int j) {
-    if (kind == SIGNROT_NORM_NONE) return v;
-    v = (v - mean) * inv;
-    if (w) v *= row::load_elem(w, j, pb);
-    if (b) v += row::load_elem(b, j, pb);
-    return v;
-  };
+    // mean and 1 / sqrt(var + eps) of the n values of f
+    auto stats = [&](auto f, int kind, float eps, float* sh1, float* sh2, float& mean, float& inv) {
+      mean = 0.f;
+      inv = 1.f;
+      if (kind == SIGNROT_NORM_NONE) return;
+      if (kind == SIGNROT_NORM_LAYER) {
+        float s = 0.f;
+        for (int j = tid; j < n; j += kAnyThreads) s += f(j);
+        mean = row::block_reduce(s, sh1) * inv_n;
+      }
+      float q = 0.f;
+      for (int j = tid; j < n; j += kAnyThreads) {
+        const float d = f(j) - mean;
+        q = fmaf(d, d, q);
+      }
+      inv = 1.f / sqrtf(row::block_reduce(q, sh2) * inv_n + eps);
+    };
+    auto affine = [&](float v, int kind, float mean, float inv, const void* w, const void* b, int j) {
+      if (kind == SIGNROT_NORM_NONE) return v;
+      v = (v - mean) * inv;
+      if (w) v *= row::load_elem(w, j, pb);
+      if (b) v += row::load_elem(b, j, pb);
+      return v;
+    };
 
-  float mean_y = 0.f, inv_y = 1.f, mean_h, inv_h;
-  if (a.y)
-    stats([&](int j) { return row::load_elem(a.y, y_at + j, 1); }, a.post_norm, a.eps_post, mean_y, inv_y);
-  auto stream = [&](int j) {
-    float v = a.beta * row::load_elem(a.h, h_at + j, hb);
-    if (a.y) {
-      float b = affine(row::load_elem(a.y, y_at + j, 1), a.post_norm, mean_y, inv_y, a.post_weight, a.post_bias, j);
-      if (a.gate) b *= row::load_elem(a.gate, gate_at + j, pb);
-      v = fmaf(a.alpha, b, v);
+    float mean_y = 0.f, inv_y = 1.f, mean_h, inv_h;
+    if (a.y)
+      stats([&](int j) { return row::load_elem(a.y, y_at + j, 1); }, a.post_norm, a.eps_post, sh[0], sh[1], mean_y,
+            inv_y);
+    auto stream = [&](int j) {
+      float v = a.beta * row::load_elem(a.h, h_at + j, hb);
+      if (a.y) {
+        float b = affine(row::load_elem(a.y, y_at + j, 1), a.post_norm, mean_y, inv_y, a.post_weight, a.post_bias, j);
+        if (a.gate) b *= row::load_elem(a.gate, gate_at + j, pb);
+        v = fmaf(a.alpha, b, v);
+      }
+      return v;
+    };
+    stats(stream, a.pre_norm, a.eps_pre, sh[2], sh[3], mean_h, inv_h);
+    auto out = [&](float v, int j) {
+      v = affine(v, a.pre_norm, mean_h, inv_h, a.pre_weight, a.pre_bias, j);
+      if (a.mod_scale) v *= 1.f + row::load_elem(a.mod_scale, mod_at + j, pb);
+      if (a.mod_shift) v += row::load_elem(a.mod_shift, mod_at + j, pb);
+      return v;
+    };
+    float top = 0.f;
+    if (a.codes) {
+      uint32_t m = 0;
+      for (int j = tid; j < n; j += kAnyThreads) m = row::join(m, row::abs_bits(out(stream(j), j)));
+      top = __uint_as_float(row::block_reduce(m, sh_top));
+      if (tid == 0) a.code_scale[t] = row::scale_of(top);
     }
-    return v;
-  };
-  stats(stream, a.pre_norm, a.eps_pre, mean_h, inv_h);
-  auto out = [&](float v, int j) {
-    v = affine(v, a.pre_norm, mean_h, inv_h, a.pre_weight, a.pre_bias, j);
-    if (a.mod_scale) v *= 1.f + row::load_elem(a.mod_scale, mod_at + j, pb);
-    if (a.mod_shift) v += row::load_elem(a.mod_shift, mod_at + j, pb);
-    return v;
-  };
-  float top = 0.f;
-  if (a.codes) {
-    uint32_t m = 0;
-    for (int j = tid; j < n; j += kThreads) m = row::add(m, row::abs_bits(out(stream(j), j)));
-    top = __uint_as_float(row::block_reduce(m, shm));
-    if (tid == 0) a.code_scale[t] = row::scale_of(top);
+    const row::Codes code(top);
+    for (int j = tid; j < n; j += kAnyThreads) {
+      const float v = stream(j);
+      const float u = out(v, j);
+      if (a.h_out) row::store_elem(a.h_out, t * a.ldho + j, v, hb);
+      if (a.u) row::store_elem(a.u, t * a.ldu + j, u, 1);
+      if (a.codes) a.codes[t * a.ldc + j] = static_cast<int8_t>(code.bits(u));
+    }
+    if (t + gridDim.x < a.tokens) __syncthreads();  // the reductions' words are used again
   }
-  for (int j = tid; j < n; j += kThreads) {
-    const float v = stream(j);
-    const float u = out(v, j);
-    if (a.h_out) row::store_elem(a.h_out, t * a.ldho + j, v, hb);
-    if (a.u) row::store_elem(a.u, t * a.ldu + j, u, 1);
-    if (a.codes) a.codes[t * a.ldc + j] = static_cast<int8_t>(row::code_of(u, top));
-  }
-  }
+}
+
+// Every row of every tensor starts on a 16-byte boundary (8 for the codes)
+// and n is a multiple of eight.
+bool aligned_rows(const NormArgs& a) {
+  const int64_t hs = a.h_type == SIGNROT_BF16 ? 2 : 4, ps = a.param_type == SIGNROT_BF16 ? 2 : 4;
+  uintptr_t at = 0;
+  for (const void* p : {a.h, a.y, static_cast<const void*>(a.h_out), static_cast<const void*>(a.u), a.post_weight,
+                        a.post_bias, a.gate, a.pre_weight, a.pre_bias, a.mod_scale, a.mod_shift})
+    at |= reinterpret_cast<uintptr_t>(p);
+  int64_t ld = a.ldh * hs;
+  if (a.y) ld |= a.ldy * 2;
+  if (a.h_out) ld |= a.ldho * hs;
+  if (a.u) ld |= a.ldu * 2;
+  if (a.gate) ld |= a.ldg * ps;
+  if (a.mod_scale || a.mod_shift) ld |= a.ldm * ps;
+  const bool codes = !a.codes || ((reinterpret_cast<uintptr_t>(a.codes) | static_cast<uintptr_t>(a.ldc)) & 7u) == 0;
+  return a.n % 8 == 0 && (at & 15u) == 0 && (ld & 15) == 0 && codes;
+}
+
+template <int V>
+void run_rows(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
+  if (a.h_type == SIGNROT_BF16)
+    residual_norm_rows_kernel<V, true><<<grid, block, 0, s>>>(a);
+  else
+    residual_norm_rows_kernel<V, false><<<grid, block, 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(a.tokens < row::kMaxBlocks ? a.tokens : row::kMaxBlocks);
-  residual_norm_any_kernel<<<dim3(blocks), dim3(kThreads), 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>(a.tokens < row::kMaxBlocks ? a.tokens : row::kMaxBlocks));
+  const int chunks = static_cast<int>(a.n / 8);
+  if (!aligned_rows(a) || chunks > 4 * 1024) {
+    residual_norm_any_kernel<<<grid, dim3(kAnyThreads), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int v = row::chunks_per_thread(chunks, a.tokens);
+  const dim3 block(static_cast<unsigned>(row::threads_for(chunks, v)));
+  switch (v) {
+    case 1: run_rows<1>(a, grid, block, s); break;
+    case 2: run_rows<2>(a, grid, block, s); break;
+    default: run_rows<4>(a, grid, block, s); break;
+  }
   return hipGetLastError();
 }
 
