@@ -8,6 +8,7 @@
 // The weights are the MFMA's A operand and the tokens its B operand, so that a
 // lane's four results are consecutive output channels of one token.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -19,6 +20,8 @@ namespace signrot {
 namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int32_t)))) int32_t i32x4_t;
+
+constexpr int kCus = 256;  // of an MI355X: the plans do not depend on the device asked
 
 // Eight packed INT4 codes (code 2i in the low nibble of byte i) as eight
 // bytes in channel order.
@@ -51,24 +54,33 @@ __device__ __forceinline__ void tile_at(int p, int tiles_m, int tiles_n, int& tm
   tn = r / gm;
 }
 
-constexpr int kStep = 64;  // k per step, one MFMA deep
+constexpr int kDeep = 64;  // k of one MFMA
 
-// WK x WT waves of FK x FT 16 x 16 results each, a ring of S steps.
-template <bool A4, int WK, int WT, int FK, int FT, int S>
+// WK x WT waves of FK x FT 16 x 16 results each, a ring of S steps of KU
+// MFMAs' depth.
+template <bool A4, int WK, int WT, int FK, int FT, int KU, int S>
 struct Tile {
+  static constexpr int kStep = KU * kDeep;                // k per step
   static constexpr int kWaves = WK * WT;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kBN = 16 * WK * FK;                // channels
   static constexpr int kBM = 16 * WT * FT;                // tokens
-  static constexpr int kTokRow = A4 ? kStep / 2 : kStep;  // bytes of a token row and step
-  static constexpr int kWStage = kBN * kStep;
-  static constexpr int kTStage = kBM * kTokRow;
-  static constexpr int kWLoads = kWStage / 1024 / kWaves;  // LDS loads per wave and step
-  static constexpr int kTLoads = kTStage / 1024 / kWaves;
+  static constexpr int kTokRow = A4 ? kDeep / 2 : kDeep;  // bytes of a token row and MFMA
+  // LDS bytes of one MFMA's depth, its 1 KiB loads, and the loads per wave and step
+  static constexpr int kWDeep = kBN * kDeep, kTDeep = kBM * kTokRow;
+  static constexpr int kWBlocks = kWDeep / 1024, kTBlocks = kTDeep / 1024;
+  static constexpr int kWLoads = KU * kWBlocks / kWaves, kTLoads = KU * kTBlocks / kWaves;
   static constexpr int kLoads = kWLoads + kTLoads;
-  static_assert(kWLoads * 1024 * kWaves == kWStage && kTLoads * 1024 * kWaves == kTStage, "whole loads per wave");
+  static constexpr int kWStage = KU * kWDeep, kTStage = KU * kTDeep;
+  static constexpr int kPart = 256 * FK * FT * kWaves;  // int32 of a tile's partial sums
+  // work-groups to a CU: as many as its LDS holds, at most eight waves
+  static constexpr int kLds = S * (kWStage + kTStage);
+  static constexpr int kFit = 160 * 1024 / kLds < 8 / kWaves ? 160 * 1024 / kLds : 8 / kWaves;
+  static_assert(kWLoads * kWaves == KU * kWBlocks && kTLoads * kWaves == KU * kTBlocks, "whole loads per wave");
+  static_assert(kWBlocks * 1024 == kWDeep && kTBlocks * 1024 == kTDeep, "whole loads");
   static_assert(FK % 4 == 0, "a lane's channels come in sixteens");
-  static_assert(S >= 4 && S * (kWStage + kTStage) <= 160 * 1024, "ring");
+  static_assert(KU == 1 || KU % 2 == 0, "the token operands alternate");
+  static_assert(S >= 4 && kFit > 0, "ring");
 };
 
 // Both operands stream global -> LDS (16 bytes a lane, no registers) through a
@@ -98,10 +110,10 @@ struct Tile {
 // Slot 16 f + i of a 64-channel group holds channel 16 (i / 4) + 4 f + i % 4:
 // the four 16 x 16 results f = 0 .. 3 then leave a lane sixteen consecutive
 // channels of a token, stored as whole vectors.
-template <bool A4, int WK, int WT, int FK, int FT, int S>
-__device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_n) {
-  using C = Tile<A4, WK, WT, FK, FT, S>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S * (C::kWStage + C::kTStage)];
+template <bool A4, int WK, int WT, int FK, int FT, int KU, int S, bool SPLIT>
+__device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_n, int splits) {
+  using C = Tile<A4, WK, WT, FK, FT, KU, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
   uint8_t* const lds_w = lds;
   uint8_t* const lds_t = lds + S * C::kWStage;
   const int lane = threadIdx.x & 63;
@@ -109,36 +121,55 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   const int wk = wid % WK, wt = wid / WK;
   const int g = lane >> 4, i = lane & 15;
 
-  // Consecutive block ids go to different XCDs: each XCD takes one contiguous
-  // range of the tiles, its work-groups (gridDim / 8 of them) the tiles of that
-  // range in turn.  A grid that is not a multiple of eight is one tile each.
+  // Item p is part p / tiles of tile p % tiles.  Consecutive block ids go to
+  // different XCDs: each XCD takes one contiguous range of the items, its
+  // work-groups (gridDim / 8 of them) the items of that range in turn.  A grid
+  // that is not a multiple of eight is one item each.
+  const int tiles = tiles_m * tiles_n;
   int p, end, stride;
   {
-    const int tiles = tiles_m * tiles_n;
-    const int q = tiles >> 3, rem = tiles & 7;
+    const int items = tiles * splits;
+    const int q = items >> 3, rem = items & 7;
     const int x = blockIdx.x & 7;
     const int start = x < rem ? x * (q + 1) : rem * (q + 1) + (x - rem) * q;
     p = start + (blockIdx.x >> 3);
     end = start + q + (x < rem ? 1 : 0);
-    stride = (gridDim.x & 7) ? tiles : gridDim.x >> 3;
+    stride = (gridDim.x & 7) ? items : gridDim.x >> 3;
   }
-  const int last = (a.n + kStep - 1) / kStep - 1;
-  const int tail = a.n - last * kStep;  // k of step 0
+  const int steps = (a.n + C::kStep - 1) / C::kStep;
+  const int tail = a.n - (steps - 1) * C::kStep;  // k of step 0
+  // part j of a row: steps first(j) .. first(j + 1) - 1
+  auto first = [&](int j) { return static_cast<int>(static_cast<int64_t>(steps) * j / splits); };
 
-  // What is loaded next: step ik of tile src_p.  Rows beyond the tensor are
+  // What is loaded next: step ik of item src_p.  Rows beyond the tensor are
   // clamped (their results are not stored).
+  // Load l of a wave is block kLoads * wave + l of the step's, counted through
+  // the depths: sixteen rows of weights or tokens (32 of packed codes).
   const int chunk_w = (lane & 3) ^ (2 * (lane >> 5));  // logical chunk of the lane's slot: row lane / 4 of 16
   const int chunk_t = A4 ? (g & 1) : chunk_w;
-  const uint32_t cut_w = 16 * chunk_w >= tail ? -16 * chunk_w : 0;
-  const uint32_t cut_t = (A4 ? 32 : 16) * chunk_t >= tail ? -16 * chunk_t : 0;
-  int src_p = p, ik = 0;
+  auto depth_w = [&](int l) { return (C::kWLoads * wid + l) / C::kWBlocks; };
+  auto depth_t = [&](int l) { return (C::kTLoads * wid + l) / C::kTBlocks; };
+  // what a chunk beyond n is moved back by in the short step: to chunk 0
+  auto cut_w = [&](int l) {
+    const int k = kDeep * depth_w(l) + 16 * chunk_w;
+    return k >= tail ? static_cast<uint32_t>(k) : 0u;
+  };
+  auto cut_t = [&](int l) {
+    const int k = kDeep * depth_t(l) + (A4 ? 32 : 16) * chunk_t;
+    return k >= tail ? static_cast<uint32_t>(A4 ? k / 2 : k) : 0u;
+  };
+  int src_p = p, ik, ik_end;
   const int8_t* base_w;
   const uint8_t* base_t;
   uint32_t size_w, size_t_, off_w[C::kWLoads], off_t[C::kTLoads];
   auto set_source = [&]() {
+    const int part = SPLIT ? src_p / tiles : 0;
+    ik = __builtin_amdgcn_readfirstlane(first(part));
+    ik_end = __builtin_amdgcn_readfirstlane(first(part + 1));
     int tm, tn;
-    tile_at(src_p, tiles_m, tiles_n, tm, tn);
+    tile_at(src_p - part * tiles, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+    const bool cut = ik == 0 && tail < C::kStep;
     const int rows_w = min(C::kBN, a.R - n0), rows_t = min(C::kBM, a.T - m0);
     base_w = a.w + static_cast<int64_t>(n0) * a.ldw;
     base_t = a.a + static_cast<int64_t>(m0) * a.lda;
@@ -146,59 +177,62 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     size_t_ = static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n);
 #pragma unroll
     for (int l = 0; l < C::kWLoads; ++l) {
-      const int slot = 16 * (C::kWLoads * wid + l) + (lane >> 2);
+      const int slot = 16 * ((C::kWLoads * wid + l) % C::kWBlocks) + (lane >> 2);
       const int at = slot & 15;
       const int ch = (slot & ~63) + 16 * (at >> 2) + 4 * ((slot >> 4) & 3) + (at & 3);
-      off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + 16 * chunk_w + cut_w;
+      off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + kDeep * depth_w(l) +
+                 16 * chunk_w - (cut ? cut_w(l) : 0);
     }
 #pragma unroll
     for (int l = 0; l < C::kTLoads; ++l) {
-      const int r =
-          A4 ? 32 * (C::kTLoads * wid + l) + 16 * (lane >> 5) + i : 16 * (C::kTLoads * wid + l) + (lane >> 2);
-      off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda) + 16 * chunk_t + cut_t;
+      const int block = (C::kTLoads * wid + l) % C::kTBlocks;
+      const int r = A4 ? 32 * block + 16 * (lane >> 5) + i : 16 * block + (lane >> 2);
+      off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda) + C::kTokRow * depth_t(l) +
+                 16 * chunk_t - (cut ? cut_t(l) : 0);
     }
   };
   int wr_w = 0, wr_t = 0;  // ring position that is filled
-  int ks = last;           // 64 k-block of step ik
+  int ks;                  // k of step ik, in steps
   auto issue = [&](int l) {
     if (l < C::kWLoads) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           wave::buffer_rsrc(base_w, size_w),
           (__attribute__((address_space(3))) void*)(lds_w + wr_w + 1024 * (C::kWLoads * wid + l)), 16,
-          off_w[l], kStep * ks, 0, 0);
+          off_w[l], C::kStep * ks, 0, 0);
     } else {
       const int j = l - C::kWLoads;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           wave::buffer_rsrc(base_t, size_t_),
           (__attribute__((address_space(3))) void*)(lds_t + wr_t + 1024 * (C::kTLoads * wid + j)), 16,
-          off_t[j], C::kTokRow * ks, 0, 0);
+          off_t[j], KU * C::kTokRow * ks, 0, 0);
     }
   };
-  // Past the last tile the loads go on with that tile's: every step issues the
+  auto block_of = [&](int step) { return __builtin_amdgcn_readfirstlane(step == 0 ? steps - 1 : step - 1); };
+  // Past the last item the loads go on with that item's: every step issues the
   // same number, so the vmcnt threshold is exact.
   auto issued = [&]() {
     wr_w = wr_w == (S - 1) * C::kWStage ? 0 : wr_w + C::kWStage;
     wr_t = wr_t == (S - 1) * C::kTStage ? 0 : wr_t + C::kTStage;
-    if (ik == 0 && tail < kStep) {
+    if (ik == 0 && tail < C::kStep) {
 #pragma unroll
-      for (int l = 0; l < C::kWLoads; ++l) off_w[l] -= cut_w;
+      for (int l = 0; l < C::kWLoads; ++l) off_w[l] += cut_w(l);
 #pragma unroll
-      for (int l = 0; l < C::kTLoads; ++l) off_t[l] -= cut_t;
+      for (int l = 0; l < C::kTLoads; ++l) off_t[l] += cut_t(l);
     }
-    ik = __builtin_amdgcn_readfirstlane(ik == last ? 0 : ik + 1);
-    if (ik == 0) {
+    ik = __builtin_amdgcn_readfirstlane(ik + 1);
+    if (ik == ik_end) {
       src_p = src_p + stride < end ? src_p + stride : src_p;
       set_source();
     }
-    ks = __builtin_amdgcn_readfirstlane(ik == 0 ? last : ik - 1);
+    ks = block_of(ik);
   };
 
-  const int read_w = (64 * wk * FK / 4) * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
+  const int read_w = (64 * wk * FK / 4) * kDeep + i * kDeep + 16 * (g ^ (2 * (i >> 3)));
   const int read_t = A4 ? 512 * (wt * FT) + 256 * (g >> 1) + 16 * i + 8 * (g & 1)
-                        : 16 * wt * FT * kStep + i * kStep + 16 * (g ^ (2 * (i >> 3)));
+                        : 16 * wt * FT * kDeep + i * kDeep + 16 * (g ^ (2 * (i >> 3)));
   int rd_w = 0, rd_t = 0;  // ring position that is multiplied
   auto weight = [&](int at, int f) {
-    return *reinterpret_cast<const i32x4_t*>(lds_w + at + read_w + 16 * kStep * f);
+    return *reinterpret_cast<const i32x4_t*>(lds_w + at + read_w + 16 * kDeep * f);
   };
 
   i32x4_t acc[FK][FT];
@@ -209,7 +243,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     if (A4)
       code[j] = *reinterpret_cast<const wave::u32x2_t*>(s + 512 * j);
     else
-      dst = *reinterpret_cast<const i32x4_t*>(s + 16 * kStep * j);
+      dst = *reinterpret_cast<const i32x4_t*>(s + 16 * kDeep * j);
   };
   auto widen = [&](int j, i32x4_t& dst) {
     uint32_t w0, w1, w2, w3;
@@ -220,6 +254,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   };
 
   set_source();
+  ks = block_of(ik);
   for (int s = 0; s < S - 1; ++s) {
 #pragma unroll
     for (int l = 0; l < C::kLoads; ++l) issue(l);
@@ -236,18 +271,17 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     if (A4) widen(j, tok[0][j]);
   }
 
-  auto step = [&](i32x4_t (&now)[FT], i32x4_t (&next)[FT]) {
-    const int nx_w = rd_w == (S - 1) * C::kWStage ? 0 : rd_w + C::kWStage;
-    const int nx_t = rd_t == (S - 1) * C::kTStage ? 0 : rd_t + C::kTStage;
+  // MFMA depth u of a step
+  auto deep = [&](int u, int nx_w, int nx_t, i32x4_t (&now)[FT], i32x4_t (&next)[FT]) {
 #pragma unroll
     for (int f = 0; f < FK; ++f) {
       // The reads follow the block's first MFMA: the wait before that one is
       // then for reads a whole block old.
       acc[f][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[f], now[0], acc[f][0], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      // two reads ahead, the last two from the next step
-      wf[f + 2] = f + 2 < FK ? weight(rd_w, f + 2) : weight(nx_w, f + 2 - FK);
-      // the next step's tokens: packed codes are read over the first half of
+      // two reads ahead, the last two from the next depth or step
+      wf[f + 2] = f + 2 < FK ? weight(rd_w + u * C::kWDeep, f + 2) : weight(nx_w, f + 2 - FK);
+      // the next depth's tokens: packed codes are read over the first half of
       // the blocks and widened, between the MFMAs, over the second
       constexpr int kOver = A4 ? FK / 2 : FK;
       if (f < kOver) {
@@ -257,8 +291,11 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
 #pragma unroll
         for (int j = (f - kOver) * FT / kOver; j < (f - kOver + 1) * FT / kOver; ++j) widen(j, next[j]);
       }
+      constexpr int kBlocks = KU * FK;
+      const int b = u * FK + f;
 #pragma unroll
-      for (int l = f * C::kLoads / FK; l < (f + 1) * C::kLoads / FK; ++l) issue(l);
+      for (int l = 0; l < C::kLoads; ++l)
+        if (l >= b * C::kLoads / kBlocks && l < (b + 1) * C::kLoads / kBlocks) issue(l);
 #pragma unroll
       for (int j = 1; j < FT; ++j)
         acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[f], now[j], acc[f][j], 0, 0, 0);
@@ -266,6 +303,25 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     }
     wf[0] = wf[FK];
     wf[1] = wf[FK + 1];
+  };
+  // zeros in place of the k beyond n: depth u of the short step
+  auto mask = [&](int u, i32x4_t (&t)[FT]) {
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+      if (kDeep * u + 16 * g >= tail) t[j] = i32x4_t{0, 0, 0, 0};
+  };
+  // A step begins with tok[0] and, of odd depth, ends with the next one's in tok[1].
+  auto step = [&](i32x4_t (&t0)[FT], i32x4_t (&t1)[FT], bool cut) {
+    const int nx_w = rd_w == (S - 1) * C::kWStage ? 0 : rd_w + C::kWStage;
+    const int nx_t = rd_t == (S - 1) * C::kTStage ? 0 : rd_t + C::kTStage;
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      i32x4_t(&now)[FT] = u & 1 ? t1 : t0;
+      i32x4_t(&next)[FT] = u & 1 ? t0 : t1;
+      if (cut) mask(u, now);
+      deep(u, u + 1 < KU ? rd_w + (u + 1) * C::kWDeep : nx_w, u + 1 < KU ? rd_t + (u + 1) * C::kTDeep : nx_t, now,
+           next);
+    }
     rd_w = nx_w;
     rd_t = nx_t;
     issued();
@@ -280,19 +336,36 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     for (int f = 0; f < FK; ++f)
 #pragma unroll
       for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
-    if (tail < kStep) {
+    const int part = SPLIT ? p / tiles : 0;
+    const int count = first(part + 1) - first(part);
+    bool cut = part == 0 && tail < C::kStep;  // the item begins with the short step
+    if (KU % 2 == 0) {
+      for (int kt = 0; kt < count; ++kt) {
+        step(tok[0], tok[1], cut);
+        cut = false;
+      }
+    } else {
+      if (cut) mask(0, tok[0]);
+      for (int kt = 1; kt < count; kt += 2) {
+        step(tok[0], tok[1], false);
+        step(tok[1], tok[0], false);
+      }
+      if (count & 1) {
+        step(tok[0], tok[1], false);
 #pragma unroll
-      for (int j = 0; j < FT; ++j)
-        if (16 * g >= tail) tok[0][j] = i32x4_t{0, 0, 0, 0};
+        for (int j = 0; j < FT; ++j) tok[0][j] = tok[1][j];
+      }
     }
-    for (int kt = 0; kt < last; kt += 2) {
-      step(tok[0], tok[1]);
-      step(tok[1], tok[0]);
-    }
-    if ((last & 1) == 0) {
-      step(tok[0], tok[1]);
+
+    if (SPLIT) {
+      // partial sums in operand order, [part][tile][wave][f][j][lane]
+      i32x4_t* const out = reinterpret_cast<i32x4_t*>(a.partial) +
+                           (static_cast<int64_t>(p) * C::kPart + 256 * FK * FT * wid) / 4 + lane;
 #pragma unroll
-      for (int j = 0; j < FT; ++j) tok[0][j] = tok[1][j];
+      for (int f = 0; f < FK; ++f)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) out[64 * (FT * f + j)] = acc[f][j];
+      continue;
     }
 
     // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.
@@ -352,20 +425,309 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   wave::wait_vmcnt<0>();
 }
 
-template <bool A4, int WK, int WT, int FK, int FT, int S>
-__global__ __launch_bounds__(64 * WK * WT) __attribute__((amdgpu_waves_per_eu(WK * WT / 4)))
-void w8_tile_kernel(W8Args a, int tiles_m, int tiles_n) {
-  w8_tile<A4, WK, WT, FK, FT, S>(a, tiles_m, tiles_n);
+template <bool A4, int WK, int WT, int FK, int FT, int KU, int S, bool SPLIT>
+__global__ __launch_bounds__(64 * WK * WT) __attribute__((
+    amdgpu_waves_per_eu(Tile<A4, WK, WT, FK, FT, KU, S>::kWaves * Tile<A4, WK, WT, FK, FT, KU, S>::kFit / 4)))
+void w8_tile_kernel(W8Args a, int tiles_m, int tiles_n, int splits) {
+  w8_tile<A4, WK, WT, FK, FT, KU, S, SPLIT>(a, tiles_m, tiles_n, SPLIT ? splits : 1);
 }
 
-template <bool A4, int WK, int WT, int FK, int FT, int S>
-void run_tile(const W8Args& a, hipStream_t s) {
-  using C = Tile<A4, WK, WT, FK, FT, S>;
-  const int tiles_m = (a.T + C::kBM - 1) / C::kBM, tiles_n = (a.R + C::kBN - 1) / C::kBN;
+// Sums the parts of a tile's results and finishes them: a thread takes one
+// lane's four channels of a 16 x 16 result.
+template <bool A4, int WK, int WT, int FK, int FT, int KU, int S>
+__global__ __launch_bounds__(256) void w8_join_kernel(W8Args a, int tiles_m, int tiles_n, int splits) {
+  using C = Tile<A4, WK, WT, FK, FT, KU, S>;
   const int tiles = tiles_m * tiles_n;
-  const int cus = device_cu_count() & ~7;
-  w8_tile_kernel<A4, WK, WT, FK, FT, S><<<dim3(static_cast<unsigned>(cus > 0 && tiles > cus ? cus : tiles)),
-                                          dim3(C::kThreads), 0, s>>>(a, tiles_m, tiles_n);
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // i32x4 of a part
+  const int tile = static_cast<int>(e / (C::kPart / 4));
+  const int at = static_cast<int>(e - static_cast<int64_t>(tile) * (C::kPart / 4));
+  const int lane = at & 63, j = (at >> 6) % FT, f = (at >> 6) / FT % FK, wid = (at >> 6) / (FT * FK);
+  int tm, tn;
+  tile_at(tile, tiles_m, tiles_n, tm, tn);
+  const int t = tm * C::kBM + 16 * ((wid / WK) * FT + j) + (lane & 15);
+  const int k = tn * C::kBN + 16 * (wid % WK) * FK + 64 * (f >> 2) + 16 * (lane >> 4) + 4 * (f & 3);
+  if (t >= a.T || k >= a.R) return;
+  const i32x4_t* src = reinterpret_cast<const i32x4_t*>(a.partial) + e;
+  const int64_t pitch = static_cast<int64_t>(tiles) * (C::kPart / 4);
+  i32x4_t sum = src[0];
+  for (int s = 1; s < splits; ++s) sum += src[s * pitch];
+  float o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) o[c] = finish(a, t, min(k + c, a.R - 1), sum[c]);
+  const int64_t to = static_cast<int64_t>(t) * a.ldo + k;
+  if (k + 4 <= a.R && a.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
+    if (a.out_bf16)
+      *reinterpret_cast<wave::u32x2_t*>(static_cast<uint16_t*>(a.out) + to) =
+          wave::u32x2_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3])};
+    else
+      *reinterpret_cast<wave::f32x4_t*>(static_cast<float*>(a.out) + to) = wave::f32x4_t{o[0], o[1], o[2], o[3]};
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (k + c < a.R) row::store_elem(a.out, to + c, o[c], a.out_bf16);
+  }
+}
+
+template <bool A4, int WK, int WT, int FK, int FT, int KU, int S>
+hipError_t run_tile(const W8Args& a, int splits, hipStream_t s) {
+  using C = Tile<A4, WK, WT, FK, FT, KU, S>;
+  const int tiles_m = (a.T + C::kBM - 1) / C::kBM, tiles_n = (a.R + C::kBN - 1) / C::kBN;
+  const int items = tiles_m * tiles_n * splits;
+  const int most = (device_cu_count() & ~7) * C::kFit;
+  const dim3 grid(static_cast<unsigned>(most > 0 && items > most ? most : items)), block(C::kThreads);
+  if (splits == 1) {
+    w8_tile_kernel<A4, WK, WT, FK, FT, KU, S, false><<<grid, block, 0, s>>>(a, tiles_m, tiles_n, 1);
+    return hipGetLastError();
+  }
+  w8_tile_kernel<A4, WK, WT, FK, FT, KU, S, true><<<grid, block, 0, s>>>(a, tiles_m, tiles_n, splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  w8_join_kernel<A4, WK, WT, FK, FT, KU, S>
+      <<<dim3(static_cast<unsigned>(tiles_m * tiles_n * (C::kPart / 1024))), dim3(256), 0, s>>>(a, tiles_m, tiles_n,
+                                                                                              splits);
+  return hipGetLastError();
+}
+
+// The tiles there are, and what they cost: microseconds for 128 of k with one
+// work-group on a CU and with two side by side, and for a tile's start and
+// stores, fitted to 300 timings of 25 shapes (40 x 4096 x 4096 to 8192 x 1024 x
+// 1024; 10 % rms).  Taking the least estimate lands on the fastest of the timed
+// choices, or within 6 % of it, at every one of those shapes.  Both operands of
+// the smaller tiles come a whole 128-byte line a row and step (KU = 2): 512 x
+// 4096 x 4096 took 19.8 us with 64 bytes a step, 13.9 with 128.
+struct TileCost {
+  int bm, bn, step, fit;
+  double one, two, tile;
+};
+constexpr TileCost kTiles8[] = {{256, 256, 64, 1, 1.40, 0, 3.6},   // 4 x 2 waves of 64 channels x 128 tokens
+                                {128, 128, 128, 1, 0.474, 0, 1.8},  // 2 x 2 waves of 64 x 64
+                                {64, 128, 128, 1, 0.287, 0, 1.5},   // 2 x 2 waves of 64 x 32
+                                {64, 64, 128, 2, 0.193, 0.352, 1.7},  // 1 x 4 waves of 64 x 16
+                                {64, 64, 256, 1, 0.182, 0, 1.5}};   // the same, 256 of k a step
+constexpr TileCost kTiles4[] = {{256, 256, 64, 1, 1.48, 0, 4.9},   // 2 x 4 waves of 128 x 64: codes are widened twice
+                                {128, 128, 128, 1, 0.539, 0, 2.0},  // 2 x 4 waves of 64 x 32
+                                {128, 64, 128, 1, 0.313, 0, 1.3},   // 1 x 4 waves of 64 x 32
+                                {64, 64, 128, 2, 0.236, 0.373, 1.7},
+                                {64, 64, 256, 1, 0.190, 0, 1.6}};
+
+struct Plan {
+  int kind, splits;
+};
+
+// The least estimate over the tiles and over parts of the row joined by a
+// second kernel (3.2 us, and 3.3 TB/s over the partial sums).
+Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
+  Plan best{0, 1};
+  double least = 1e30;
+  const double bytes = static_cast<double>(R) * n + (a4 ? 0.5 : 1.0) * T * n + 2.0 * T * R;
+  for (int c = 0; c < 5; ++c) {
+    const TileCost& t = a4 ? kTiles4[c] : kTiles8[c];
+    const double tiles = static_cast<double>((T + t.bm - 1) / t.bm) * static_cast<double>((R + t.bn - 1) / t.bn);
+    for (const int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (splits > (n + t.step - 1) / t.step || tiles * splits > 4 * kCus)) break;
+      const double per_cu = ceil(tiles * splits / kCus);
+      const double k = n / 128.0 / splits;
+      double us = t.fit == 1 ? per_cu * (k * t.one + t.tile)
+                             : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
+      us = fmax(us, bytes / 7e6);
+      if (splits > 1) us += 3.2 + tiles * splits * t.bm * t.bn * 4 / 3.3e6;
+      if (us < least) {
+        least = us;
+        best = {c, splits};
+      }
+    }
+  }
+  return best;
+}
+
+// ---- few tokens ---------------------------------------------------------------
+//
+// The weights are read once and bound the time.  A work-group takes sixteen
+// channels and all tokens (FT groups of sixteen); its waves share the row:
+// wave w takes the 128-byte units w, w + waves, ... of k, so that the
+// work-group reads sixteen rows side by side.  Each wave has a ring of D units
+// of its own in LDS and waits for its own loads only; the partial sums meet in
+// LDS at the end.
+//
+// The loads go through LDS, and not straight into the operand registers,
+// because a lane (g, i) holds 16 bytes of row i: sixteen neighbouring lanes
+// would read sixteen rows, 64 cache accesses an instruction instead of eight
+// whole lines, and with many in flight a line's second half came back from L2
+// again (1.3 M requests for 0.9 M lines at 16 x 14336 x 4096).
+//
+// LDS rows of 128 bytes: chunk c of row r sits at chunk c ^ h(r),
+// h(r) = (r & 7) ^ ((r >> 3) & 1); of 64 bytes (packed codes): c ^ 2 ((r >> 3) & 1).
+// Either way the sixteen lanes a 16-byte read serves at a time cover the 64
+// banks once.
+constexpr int kUnit = 128;
+
+template <bool A4, int FK, int FT, int D>
+struct Few {
+  static constexpr int kTokRow = A4 ? kUnit / 2 : kUnit;
+  static constexpr int kWBytes = 16 * FK * kUnit;
+  static constexpr int kTBytes = 16 * FT * kTokRow;
+  static constexpr int kWLoads = kWBytes / 1024, kTLoads = kTBytes / 1024;
+  static constexpr int kLoads = kWLoads + kTLoads;
+  static constexpr int kRing = D * (kWBytes + kTBytes);  // bytes of a wave
+  static constexpr int kPart = 1024 * FK * FT;                // bytes of a wave's partial sums
+};
+
+template <bool A4, int FK, int FT, int D>
+__device__ __forceinline__ void w8_few(const W8Args& a, uint8_t* lds) {
+  using C = Few<A4, FK, FT, D>;
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int g = lane >> 4, i = lane & 15;
+  const int n0 = 16 * FK * blockIdx.x;
+  const int units = (a.n + kUnit - 1) / kUnit;
+  const int tail = a.n - (units - 1) * kUnit;  // k of the row's last unit
+  const int count = units > wid ? (units - wid - 1) / waves + 1 : 0;
+  uint8_t* const ring_w = lds + wid * C::kRing;
+  uint8_t* const ring_t = ring_w + D * C::kWBytes;
+  int32_t* const part = reinterpret_cast<int32_t*>(lds + waves * C::kRing);
+
+  // rows and tokens beyond the tensors are clamped (their results are not stored)
+  const int rows_w = min(16 * FK, a.R - n0);
+  const __amdgpu_buffer_rsrc_t src_w =
+      wave::buffer_rsrc(a.w + static_cast<int64_t>(n0) * a.ldw,
+                        static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + a.n);
+  const __amdgpu_buffer_rsrc_t src_t = wave::buffer_rsrc(
+      a.a, static_cast<uint32_t>(a.T - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n));
+  auto h = [](int r) { return (r & 7) ^ ((r >> 3) & 1); };
+  // sources of the lane: load l of the weights fills rows 8 l .. 8 l + 7
+  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
+  int chunk_w[C::kWLoads], chunk_t[C::kTLoads];
+#pragma unroll
+  for (int l = 0; l < C::kWLoads; ++l) {
+    const int r = 8 * l + (lane >> 3);
+    chunk_w[l] = (lane & 7) ^ h(r & 15);
+    off_w[l] = static_cast<uint32_t>(min(r, rows_w - 1)) * static_cast<uint32_t>(a.ldw);
+  }
+#pragma unroll
+  for (int l = 0; l < C::kTLoads; ++l) {
+    const int r = A4 ? 16 * l + (lane >> 2) : 8 * l + (lane >> 3);
+    chunk_t[l] = A4 ? (lane & 3) ^ (2 * (lane >> 5)) : (lane & 7) ^ h(r & 15);
+    off_t[l] = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(a.lda);
+  }
+  // unit x of this wave into ring slot x % D; in the row's last unit the
+  // chunks beyond n are read as chunk 0
+  auto issue = [&](int x) {
+    const int u = wid + x * waves;
+    const int left = u == units - 1 ? tail : kUnit;
+    const int slot = x % D;
+#pragma unroll
+    for (int l = 0; l < C::kWLoads; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          src_w, (__attribute__((address_space(3))) void*)(ring_w + slot * C::kWBytes + 1024 * l), 16,
+          off_w[l] + (16 * chunk_w[l] < left ? 16 * chunk_w[l] : 0), kUnit * u, 0, 0);
+#pragma unroll
+    for (int l = 0; l < C::kTLoads; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          src_t, (__attribute__((address_space(3))) void*)(ring_t + slot * C::kTBytes + 1024 * l), 16,
+          off_t[l] + ((A4 ? 32 : 16) * chunk_t[l] < left ? 16 * chunk_t[l] : 0), C::kTokRow * u, 0, 0);
+  };
+
+  i32x4_t acc[FK][FT];
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
+  for (int x = 0; x < min(D, count); ++x) issue(x);
+  for (int x = 0; x < count; ++x) {
+    if (x + D <= count)
+      wave::wait_vmcnt<(D - 1) * C::kLoads>();
+    else
+      wave::wait_vmcnt<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* const sw = ring_w + (x % D) * C::kWBytes;
+    const uint8_t* const st = ring_t + (x % D) * C::kTBytes;
+    // lane (g, i): chunks 2 g and 2 g + 1 of row i
+    i32x4_t w[2][FK], tok[2][FT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int f = 0; f < FK; ++f)
+        w[s][f] = *reinterpret_cast<const i32x4_t*>(sw + 2048 * f + kUnit * i + 16 * ((2 * g + s) ^ h(i)));
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      if (A4) {
+        const i32x4_t c = *reinterpret_cast<const i32x4_t*>(st + 1024 * j + 64 * i + 16 * (g ^ (2 * (i >> 3))));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t b[4];
+          widen8(static_cast<uint32_t>(c[2 * s]), b[0], b[1]);
+          widen8(static_cast<uint32_t>(c[2 * s + 1]), b[2], b[3]);
+          tok[s][j] = i32x4_t{static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]),
+                              static_cast<int>(b[3])};
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          tok[s][j] = *reinterpret_cast<const i32x4_t*>(st + 2048 * j + kUnit * i + 16 * ((2 * g + s) ^ h(i)));
+      }
+    }
+    if (wid + x * waves == units - 1 && tail < kUnit) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int f = 0; f < FK; ++f)
+          if (16 * (2 * g + s) >= tail) w[s][f] = i32x4_t{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int f = 0; f < FK; ++f)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+          acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][f], tok[s][j], acc[f][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (x + D < count) issue(x + D);
+  }
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+      *reinterpret_cast<i32x4_t*>(part + 4 * (((wid * FK + f) * FT + j) * 64 + lane)) = acc[f][j];
+  __syncthreads();
+  // result e: channel e % 4 + 4 (e / 64 % 4) of group e / 256 / FT, token e / 4 % 16 of group e / 256 % FT
+  for (int e = threadIdx.x; e < 256 * FK * FT; e += blockDim.x) {
+    const int k = n0 + 16 * ((e >> 8) / FT) + (e & 3) + 4 * ((e >> 6) & 3);
+    const int t = 16 * ((e >> 8) % FT) + ((e >> 2) & 15);
+    if (k >= a.R || t >= a.T) continue;
+    int32_t sum = part[e];
+    for (int v = 1; v < waves; ++v) sum += part[256 * FK * FT * v + e];
+    row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, sum), a.out_bf16);
+  }
+}
+
+template <bool A4, int FK, int FT, int D>
+__global__ __launch_bounds__(512) void w8_few_kernel(W8Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
+  w8_few<A4, FK, FT, D>(a, few_lds);
+}
+
+template <bool A4, int FK, int FT, int D>
+hipError_t run_few_as(const W8Args& a, hipStream_t s) {
+  using C = Few<A4, FK, FT, D>;
+  const int groups = (a.R + 16 * FK - 1) / (16 * FK), units = (a.n + kUnit - 1) / kUnit;
+  int waves = 8;
+  while (waves > 2 && (groups * waves > 8 * kCus || units < waves)) waves /= 2;
+  w8_few_kernel<A4, FK, FT, D><<<dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(64 * waves)),
+                             static_cast<unsigned>(waves * (C::kRing + C::kPart)), s>>>(a);
+  return hipGetLastError();
+}
+
+// Thirty-two channels to a work-group where that leaves one to two of them a
+// CU: 16 x 28672 x 8192 43.5 us and 1 x 4096 x 14336 13.8 us against 48.1 and
+// 15.3 with sixteen; fewer channels need the work-groups (16 x 14336 x 4096 has
+// 256 of sixteen), and 1 x 8192 x 28672 ran 45.0 us with sixteen, 48.9 with
+// thirty-two.
+template <bool A4>
+hipError_t run_few(const W8Args& a, hipStream_t s) {
+  if (a.R >= 8192 && a.R <= 16384)
+    return a.T <= 16 ? run_few_as<A4, 2, 1, 3>(a, s) : run_few_as<A4, 2, 2, 2>(a, s);
+  return a.T <= 16 ? run_few_as<A4, 1, 1, 3>(a, s) : run_few_as<A4, 1, 2, 2>(a, s);
 }
 
 // Rows that start on 16-byte boundaries and end on one.
@@ -460,13 +822,58 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
   }
 }
 
+hipError_t run_tiles(const W8Args& a, hipStream_t s) {
+  const Plan p = tile_plan(a.T, a.n, a.R, a.a4 != 0);
+  if (a.a4) {
+    switch (p.kind) {
+      case 0: return run_tile<true, 2, 4, 8, 4, 1, 4>(a, p.splits, s);
+      case 1: return run_tile<true, 2, 4, 4, 2, 2, 5>(a, p.splits, s);
+      case 2: return run_tile<true, 1, 4, 4, 2, 2, 5>(a, p.splits, s);
+      case 3: return run_tile<true, 1, 4, 4, 1, 2, 5>(a, p.splits, s);
+      default: return run_tile<true, 1, 4, 4, 1, 4, 5>(a, p.splits, s);
+    }
+  }
+  switch (p.kind) {
+    case 0: return run_tile<false, 4, 2, 4, 8, 1, 4>(a, p.splits, s);
+    case 1: return run_tile<false, 2, 2, 4, 4, 2, 5>(a, p.splits, s);
+    case 2: return run_tile<false, 2, 2, 4, 2, 2, 5>(a, p.splits, s);
+    case 3: return run_tile<false, 1, 4, 4, 1, 2, 5>(a, p.splits, s);
+    default: return run_tile<false, 1, 4, 4, 1, 4, 5>(a, p.splits, s);
+  }
+}
+
+// Up to 32 tokens: 32 x 14336 x 4096 16.9 us, 32 x 4096 x 4096 7.1 us, the best
+// tile 17.3 and 10.5.
+bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24); }
+
 }  // namespace
 
-int64_t w8_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t w8_workspace(int64_t tokens, int64_t n, int64_t rows, bool a4) {
+  if (tokens == 0 || rows == 0 || takes_few(tokens, rows)) return 0;
+  const Plan p = tile_plan(tokens, n, rows, a4);
+  const TileCost& t = a4 ? kTiles4[p.kind] : kTiles8[p.kind];
+  if (p.splits == 1) return 0;
+  return ((tokens + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn) * p.splits * t.bm * t.bn * 4;
+}
 
-const char* w8_name(const W8Args& a) { return aligned_rows(a) && a.T > 64 ? "w8_tile" : "w8_any"; }
+const char* w8_name(const W8Args& a) {
+  if (!aligned_rows(a)) return "w8_any";
+  if (takes_few(a.T, a.R)) return "w8_few";
+  const Plan p = tile_plan(a.T, a.n, a.R, a.a4 != 0);
+  static const char* const names8[5][2] = {{"w8_tile_256x256", "w8_tile_256x256_split"},
+                                           {"w8_tile_128x128", "w8_tile_128x128_split"},
+                                           {"w8_tile_64x128", "w8_tile_64x128_split"},
+                                           {"w8_tile_64x64", "w8_tile_64x64_split"},
+                                           {"w8_tile_64x64_deep", "w8_tile_64x64_deep_split"}};
+  static const char* const names4[2] = {"w8_tile_128x64", "w8_tile_128x64_split"};
+  return a.a4 && p.kind == 2 ? names4[p.splits > 1] : names8[p.kind][p.splits > 1];
+}
 
 hipError_t launch_w8(const W8Args& all, hipStream_t s) {
+  if (aligned_rows(all)) {
+    if (takes_few(all.T, all.R)) return all.a4 ? run_few<true>(all, s) : run_few<false>(all, s);
+    return run_tiles(all, s);
+  }
   // a launch holds fewer than 2^32 threads in one dimension: token ranges of at most 2^22 tiles
   const int64_t tiles_n = (static_cast<int64_t>(all.R) + kAnyTile - 1) / kAnyTile;
   if (tiles_n > (int64_t{1} << 22)) return hipErrorInvalidConfiguration;
@@ -478,13 +885,6 @@ hipError_t launch_w8(const W8Args& all, hipStream_t s) {
     a.scale += t;
     if (a.a4) a.zero += t;
     a.out = static_cast<uint8_t*>(a.out) + t * a.ldo * (a.out_bf16 ? 2 : 4);
-    if (aligned_rows(a) && a.T > 64) {
-      if (a.a4)
-        run_tile<true, 2, 4, 8, 4, 4>(a, s);
-      else
-        run_tile<false, 4, 2, 4, 8, 4>(a, s);
-      continue;
-    }
     const dim3 grid(static_cast<unsigned>(((a.T + kAnyTile - 1) / kAnyTile) * tiles_n)), block(256);
     if (a.a4)
       w8_any_kernel<true><<<grid, block, 0, s>>>(a);
