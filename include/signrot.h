@@ -369,14 +369,15 @@ int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld
  *   bias     device, [rows] float, or NULL.
  *   out      device, [tokens][ldo] of out_type, ldo >= rows.
  *   workspace, workspace_bytes
- *            device scratch of at least signrot_int8_linear_workspace(tokens,
- *            n, rows) bytes, 16-byte aligned; NULL when that is 0.  Its
- *            contents are unspecified before and after the call; it must not
- *            be used by anything else until the call's work has ended.
+ *            device scratch of at least signrot_int8_linear_workspace bytes
+ *            (for the same operands), 16-byte aligned; NULL when that is 0.
+ *            Its contents are unspecified before and after the call; it must
+ *            not be used by anything else until the call's work has ended.
  *
  * 1 <= n <= 131071 (an int32 sum cannot overflow); any alignment and stride
- * of codes, w and out (16-byte aligned rows with n a multiple of 16 take the
- * faster kernels).  tokens == 0 or rows == 0 is a no-op.  Negative or
+ * of codes, w and out.  Rows that are not 16-byte aligned with n a multiple of
+ * 16 (32 of packed INT4 codes) cost more; large ones are laid out anew in the
+ * workspace first.  tokens == 0 or rows == 0 is a no-op.  Negative or
  * over-large sizes (>= 2^31), a leading dimension below its row, an unknown
  * out_type, a workspace that is too small or a null pointer ->
  * SIGNROT_EINVAL.  No allocation.  Asynchronous.
@@ -408,10 +409,13 @@ int signrot_int4_w8_linear(const uint8_t* codes, const float* scale, const float
                            const float* bias, int64_t rows, void* out, int64_t ldo, int out_type, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
-/* Scratch bytes the two products need for a shape (0: none, the pointer may
- * be NULL), or -1 when the sizes are invalid.  Host-only. */
-int64_t signrot_int8_linear_workspace(int64_t tokens, int64_t n, int64_t rows);
-int64_t signrot_int4_w8_linear_workspace(int64_t tokens, int64_t n, int64_t rows);
+/* Scratch bytes the two products need for these operands (0: none, the pointer
+ * may be NULL), or -1 when the sizes are invalid.  They depend on the sizes and
+ * on the alignment of the pointers and strides.  Host-only. */
+int64_t signrot_int8_linear_workspace(const int8_t* codes, int64_t ldc, int64_t tokens, int64_t n, const int8_t* w,
+                                      int64_t ldw, int64_t rows);
+int64_t signrot_int4_w8_linear_workspace(const uint8_t* codes, int64_t tokens, int64_t n, const int8_t* w, int64_t ldw,
+                                         int64_t rows);
 
 /* Which kernel the two products would launch for these operands (a static
  * string), or NULL when the sizes are invalid.  Host-only. */

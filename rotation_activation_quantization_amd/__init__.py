@@ -73,9 +73,10 @@ def lib() -> ctypes.CDLL:
     L.signrot_int4_w8_linear.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp, vp, i64, vp, i64, ctypes.c_int, vp,
                                          i64, vp]
     L.signrot_int4_w8_linear.restype = ctypes.c_int
-    for name in ("signrot_int8_linear_workspace", "signrot_int4_w8_linear_workspace"):
-        getattr(L, name).argtypes = [i64, i64, i64]
-        getattr(L, name).restype = i64
+    L.signrot_int8_linear_workspace.argtypes = [vp, i64, i64, i64, vp, i64, i64]
+    L.signrot_int8_linear_workspace.restype = i64
+    L.signrot_int4_w8_linear_workspace.argtypes = [vp, i64, i64, vp, i64, i64]
+    L.signrot_int4_w8_linear_workspace.restype = i64
     L.signrot_int8_linear_kernel_name.argtypes = [vp, i64, i64, i64, vp, i64, i64]
     L.signrot_int8_linear_kernel_name.restype = ctypes.c_char_p
     L.signrot_int4_w8_linear_kernel_name.argtypes = [vp, i64, i64, vp, i64, i64]
@@ -451,21 +452,32 @@ def _on_gpu(v, name):
     return v.device
 
 
+def _empty_codes(t, n, device):
+    """int8 [T, n] in rows of whole 16-byte chunks, which the products read as they are."""
+    import torch
+
+    if n % 16 == 0:
+        return torch.empty((t, n), dtype=torch.int8, device=device), n
+    pitch = (n + 15) // 16 * 16
+    return torch.empty((t, pitch), dtype=torch.int8, device=device)[:, :n], pitch
+
+
 def signrot_quant_int8(x, sums: bool = False, out=None):
     """bf16 [T, n] -> (codes int8 [T, n], scale f32 [T][, sum int32 [T]]): per
     row scale = max|x| / 127 and codes = rint(127 x / max|x|); sum holds the
-    code sums.  On a weight [rows, n] the rows are the output channels.  `out`
-    may pass preallocated (codes, scale[, sum])."""
+    code sums.  On a weight [rows, n] the rows are the output channels.  The
+    codes' rows start on 16-byte boundaries (a view of wider rows where n is no
+    multiple of 16).  `out` may pass preallocated (codes, scale[, sum])."""
     import torch
 
     device = _on_gpu(x, "x")
     ptr, ld = _matrix(x, "x", None, None, torch.bfloat16, device)
     t, n = x.shape
     if out is None:
-        codes, scale = torch.empty((t, n), dtype=torch.int8, device=device), torch.empty(t, device=device,
-                                                                                         dtype=torch.float32)
+        codes, ldc = _empty_codes(t, n, device)
+        scale = torch.empty(t, dtype=torch.float32, device=device)
         out = (codes, scale, torch.empty(t, dtype=torch.int32, device=device)) if sums else (codes, scale)
-        qptr, ldc, sptr = codes.data_ptr(), n, scale.data_ptr()
+        qptr, sptr = codes.data_ptr(), scale.data_ptr()
     else:
         out = tuple(out[:3 if sums else 2])
         if len(out) < (3 if sums else 2):
@@ -518,7 +530,7 @@ def signrot_int8_linear(codes, scale, w, w_scale, bias=None, dtype=None, out=Non
     bptr = _vector(bias, "bias", rows, torch.float32, device)
     out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
     L = lib()
-    ws, size, _owner = _workspace(L.signrot_int8_linear_workspace(t, n, rows), device)
+    ws, size, _owner = _workspace(L.signrot_int8_linear_workspace(aptr, lda, t, n, wptr, ldw, rows), device)
     check(L.signrot_int8_linear(aptr, lda, sptr, t, n, wptr, ldw, vptr, bptr, rows, optr, ldo, kind, ws, size,
                                 _stream_of(codes)), "signrot_int8_linear")
     return out
@@ -544,8 +556,9 @@ def signrot_int4_w8_linear(codes, scale, zero, w, w_scale, w_sum, bias=None, dty
     bptr = _vector(bias, "bias", rows, torch.float32, device)
     out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
     L = lib()
-    ws, size, _owner = _workspace(L.signrot_int4_w8_linear_workspace(t, n, rows), device)
-    check(L.signrot_int4_w8_linear(codes.data_ptr(), sptr, zptr, t, n, wptr, ldw, vptr, uptr, bptr, rows, optr, ldo,
+    aptr = codes.data_ptr()
+    ws, size, _owner = _workspace(L.signrot_int4_w8_linear_workspace(aptr, t, n, wptr, ldw, rows), device)
+    check(L.signrot_int4_w8_linear(aptr, sptr, zptr, t, n, wptr, ldw, vptr, uptr, bptr, rows, optr, ldo,
                                    kind, ws, size, _stream_of(codes)), "signrot_int4_w8_linear")
     return out
 
@@ -643,9 +656,9 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
         else:
             uptr, ldu = _matrix(out, "u", t, n, torch.bfloat16, device)
     elif out is None:
-        out = (torch.empty((t, n), dtype=torch.int8, device=device),
-               torch.empty(t, dtype=torch.float32, device=device))
-        qptr, ldc, sptr = out[0].data_ptr(), n, out[1].data_ptr()
+        q, ldc = _empty_codes(t, n, device)
+        out = (q, torch.empty(t, dtype=torch.float32, device=device))
+        qptr, sptr = q.data_ptr(), out[1].data_ptr()
     else:
         qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
         sptr = _vector(out[1], "scale", t, torch.float32, device)

@@ -665,16 +665,16 @@ int w8_linear(W8Args& a, int64_t tokens, int64_t n, int64_t rows, int out_type, 
   if (odd(a.scale) || odd(a.zero) || odd(a.w_scale) || odd(a.w_sum) || odd(a.bias) ||
       (out_type == SIGNROT_F32 ? odd(a.out) : (reinterpret_cast<uintptr_t>(a.out) & 1u) != 0))
     return fail_einval("a pointer is not aligned to its type");
-  const int64_t need = w8_workspace(tokens, n, rows, a.a4 != 0);
+  a.out_bf16 = out_type == SIGNROT_BF16;
+  a.T = static_cast<int>(tokens);
+  a.R = static_cast<int>(rows);
+  a.n = static_cast<int>(n);
+  const int64_t need = w8_workspace(a);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return fail_einval("workspace too small");
     if (!aligned16(workspace)) return fail_einval("workspace must be 16-byte aligned");
   }
   a.partial = static_cast<int32_t*>(workspace);
-  a.out_bf16 = out_type == SIGNROT_BF16;
-  a.T = static_cast<int>(tokens);
-  a.R = static_cast<int>(rows);
-  a.n = static_cast<int>(n);
   const hipError_t e = launch_w8(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, where);
   return SIGNROT_OK;
@@ -720,19 +720,12 @@ int signrot_int4_w8_linear(const uint8_t* codes, const float* scale, const float
   return w8_linear(a, tokens, n, rows, out_type, workspace, workspace_bytes, stream, "int4_w8_linear launch");
 }
 
-int64_t signrot_int8_linear_workspace(int64_t tokens, int64_t n, int64_t rows) {
-  return w8_sizes(tokens, n, rows, false) == SIGNROT_OK ? w8_workspace(tokens, n, rows, false) : -1;
-}
-
-int64_t signrot_int4_w8_linear_workspace(int64_t tokens, int64_t n, int64_t rows) {
-  return w8_sizes(tokens, n, rows, true) == SIGNROT_OK ? w8_workspace(tokens, n, rows, true) : -1;
-}
-
 namespace {
-const char* w8_kernel_name(const uint8_t* codes, int64_t lda, int64_t tokens, int64_t n, const int8_t* w, int64_t ldw,
-                           int64_t rows, bool a4) {
-  if (w8_sizes(tokens, n, rows, a4) != SIGNROT_OK || lda < (a4 ? n / 2 : n) || ldw < n) return nullptr;
-  W8Args a;
+// The operands of a host-only question; false when the sizes are invalid.
+bool w8_operands(W8Args& a, const uint8_t* codes, int64_t lda, int64_t tokens, int64_t n, const int8_t* w, int64_t ldw,
+                 int64_t rows, bool a4) {
+  g_last_error[0] = '\0';
+  if (w8_sizes(tokens, n, rows, a4) != SIGNROT_OK || lda < (a4 ? n / 2 : n) || ldw < n) return false;
   memset(&a, 0, sizeof(a));
   a.a4 = a4;
   a.a = codes;
@@ -742,18 +735,34 @@ const char* w8_kernel_name(const uint8_t* codes, int64_t lda, int64_t tokens, in
   a.T = static_cast<int>(tokens);
   a.R = static_cast<int>(rows);
   a.n = static_cast<int>(n);
-  return w8_name(a);
+  return true;
 }
 }  // namespace
 
+int64_t signrot_int8_linear_workspace(const int8_t* codes, int64_t ldc, int64_t tokens, int64_t n, const int8_t* w,
+                                      int64_t ldw, int64_t rows) {
+  W8Args a;
+  return w8_operands(a, reinterpret_cast<const uint8_t*>(codes), ldc, tokens, n, w, ldw, rows, false) ? w8_workspace(a)
+                                                                                                      : -1;
+}
+
+int64_t signrot_int4_w8_linear_workspace(const uint8_t* codes, int64_t tokens, int64_t n, const int8_t* w, int64_t ldw,
+                                         int64_t rows) {
+  W8Args a;
+  return w8_operands(a, codes, n / 2, tokens, n, w, ldw, rows, true) ? w8_workspace(a) : -1;
+}
+
 const char* signrot_int8_linear_kernel_name(const int8_t* codes, int64_t ldc, int64_t tokens, int64_t n,
                                             const int8_t* w, int64_t ldw, int64_t rows) {
-  return w8_kernel_name(reinterpret_cast<const uint8_t*>(codes), ldc, tokens, n, w, ldw, rows, false);
+  W8Args a;
+  return w8_operands(a, reinterpret_cast<const uint8_t*>(codes), ldc, tokens, n, w, ldw, rows, false) ? w8_name(a)
+                                                                                                      : nullptr;
 }
 
 const char* signrot_int4_w8_linear_kernel_name(const uint8_t* codes, int64_t tokens, int64_t n, const int8_t* w,
                                                int64_t ldw, int64_t rows) {
-  return w8_kernel_name(codes, n / 2, tokens, n, w, ldw, rows, true);
+  W8Args a;
+  return w8_operands(a, codes, n / 2, tokens, n, w, ldw, rows, true) ? w8_name(a) : nullptr;
 }
 
 int signrot_residual_norm(const signrot_residual_norm_args* args, void* stream) {

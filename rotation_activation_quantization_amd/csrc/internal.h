@@ -162,6 +162,7 @@ struct W8Args {
   void* out;             // [T][ldo]
   int64_t ldo;
   int32_t* partial;      // workspace
+  int row_bytes;         // bytes of a token row that may be read, set by launch_w8
   int out_bf16;
   int a4;
   int T;
@@ -169,7 +170,7 @@ struct W8Args {
   int n;
 };
 constexpr int kW8MaxN = 131071;  // 128 * 128 * n stays below 2^31
-int64_t w8_workspace(int64_t tokens, int64_t n, int64_t rows, bool a4);
+int64_t w8_workspace(const W8Args& a);
 const char* w8_name(const W8Args& a);
 hipError_t launch_w8(const W8Args& a, hipStream_t s);
 

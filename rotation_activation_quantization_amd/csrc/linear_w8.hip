@@ -174,7 +174,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     base_w = a.w + static_cast<int64_t>(n0) * a.ldw;
     base_t = a.a + static_cast<int64_t>(m0) * a.lda;
     size_w = static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + a.n;
-    size_t_ = static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n);
+    size_t_ = static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + a.row_bytes;
 #pragma unroll
     for (int l = 0; l < C::kWLoads; ++l) {
       const int slot = 16 * ((C::kWLoads * wid + l) % C::kWBlocks) + (lane >> 2);
@@ -512,13 +512,13 @@ constexpr TileCost kTiles4[] = {{256, 256, 64, 1, 1.48, 0, 4.9},   // 2 x 4 wave
 
 struct Plan {
   int kind, splits;
+  double us;
 };
 
 // The least estimate over the tiles and over parts of the row joined by a
 // second kernel (3.2 us, and 3.3 TB/s over the partial sums).
 Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
-  Plan best{0, 1};
-  double least = 1e30;
+  Plan best{0, 1, 1e30};
   const double bytes = static_cast<double>(R) * n + (a4 ? 0.5 : 1.0) * T * n + 2.0 * T * R;
   for (int c = 0; c < 5; ++c) {
     const TileCost& t = a4 ? kTiles4[c] : kTiles8[c];
@@ -531,10 +531,7 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
                              : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
       us = fmax(us, bytes / 7e6);
       if (splits > 1) us += 3.2 + tiles * splits * t.bm * t.bn * 4 / 3.3e6;
-      if (us < least) {
-        least = us;
-        best = {c, splits};
-      }
+      if (us < best.us) best = {c, splits, us};
     }
   }
   return best;
@@ -560,6 +557,21 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
 // Either way the sixteen lanes a 16-byte read serves at a time cover the 64
 // banks once.
 constexpr int kUnit = 128;
+
+// The waves' partial sums [wave][FK][FT][64][4] joined and finished: result e is
+// channel e % 4 + 4 (e / 64 % 4) of group e / 256 / FT, token e / 4 % 16 of
+// group e / 256 % FT.
+template <int FK, int FT>
+__device__ __forceinline__ void few_finish(const W8Args& a, const int32_t* part, int n0, int waves) {
+  for (int e = threadIdx.x; e < 256 * FK * FT; e += blockDim.x) {
+    const int k = n0 + 16 * ((e >> 8) / FT) + (e & 3) + 4 * ((e >> 6) & 3);
+    const int t = 16 * ((e >> 8) % FT) + ((e >> 2) & 15);
+    if (k >= a.R || t >= a.T) continue;
+    int32_t sum = part[e];
+    for (int v = 1; v < waves; ++v) sum += part[256 * FK * FT * v + e];
+    row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, sum), a.out_bf16);
+  }
+}
 
 template <bool A4, int FK, int FT, int D>
 struct Few {
@@ -593,7 +605,7 @@ __device__ __forceinline__ void w8_few(const W8Args& a, uint8_t* lds) {
       wave::buffer_rsrc(a.w + static_cast<int64_t>(n0) * a.ldw,
                         static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + a.n);
   const __amdgpu_buffer_rsrc_t src_t = wave::buffer_rsrc(
-      a.a, static_cast<uint32_t>(a.T - 1) * static_cast<uint32_t>(a.lda) + (A4 ? a.n / 2 : a.n));
+      a.a, static_cast<uint32_t>(a.T - 1) * static_cast<uint32_t>(a.lda) + a.row_bytes);
   auto h = [](int r) { return (r & 7) ^ ((r >> 3) & 1); };
   // sources of the lane: load l of the weights fills rows 8 l .. 8 l + 7
   uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
@@ -690,15 +702,7 @@ __device__ __forceinline__ void w8_few(const W8Args& a, uint8_t* lds) {
     for (int j = 0; j < FT; ++j)
       *reinterpret_cast<i32x4_t*>(part + 4 * (((wid * FK + f) * FT + j) * 64 + lane)) = acc[f][j];
   __syncthreads();
-  // result e: channel e % 4 + 4 (e / 64 % 4) of group e / 256 / FT, token e / 4 % 16 of group e / 256 % FT
-  for (int e = threadIdx.x; e < 256 * FK * FT; e += blockDim.x) {
-    const int k = n0 + 16 * ((e >> 8) / FT) + (e & 3) + 4 * ((e >> 6) & 3);
-    const int t = 16 * ((e >> 8) % FT) + ((e >> 2) & 15);
-    if (k >= a.R || t >= a.T) continue;
-    int32_t sum = part[e];
-    for (int v = 1; v < waves; ++v) sum += part[256 * FK * FT * v + e];
-    row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, sum), a.out_bf16);
-  }
+  few_finish<FK, FT>(a, part, n0, waves);
 }
 
 template <bool A4, int FK, int FT, int D>
@@ -730,100 +734,306 @@ hipError_t run_few(const W8Args& a, hipStream_t s) {
   return a.T <= 16 ? run_few_as<A4, 1, 1, 3>(a, s) : run_few_as<A4, 1, 2, 2>(a, s);
 }
 
+constexpr int64_t kMaxPitch = 1 << 23;  // a tile's offsets stay below 2^32
+
 // Rows that start on 16-byte boundaries and end on one.
 bool aligned_rows(const W8Args& a) {
   return a.n % (a.a4 ? 32 : 16) == 0 && a.lda % 16 == 0 && a.ldw % 16 == 0 &&
-         ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w)) & 15u) == 0 &&
-         a.lda < (int64_t{1} << 23) && a.ldw < (int64_t{1} << 23);
+         ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w)) & 15u) == 0 && a.lda < kMaxPitch &&
+         a.ldw < kMaxPitch;
 }
 
-// ---- any shape, stride and alignment ----------------------------------------
-//
-// Tile 64 tokens x 64 channels, four waves of 32 x 32, k steps of 64.  Both
-// operands go through registers (16 bytes a thread, loads of any alignment,
-// the row's last bytes one at a time) into a double-buffered LDS tile kept in
-// operand order: 16-row group, 16-byte chunk, row.
-constexpr int kAnyTile = 64;
+// Up to 32 tokens: 32 x 14336 x 4096 16.9 us, 32 x 4096 x 4096 7.1 us, the best
+// tile 17.3 and 10.5.
+bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24); }
 
-// 16 operand bytes from channel j0 on of a row with n channels, zeros beyond.
+// ---- any stride and alignment -------------------------------------------------
+//
+// Rows that are not made of whole, aligned 16-byte chunks cannot go straight to
+// LDS.
+
+// The 16 operand bytes (8 of packed codes) from channel j0 on of a row with n
+// channels, in two halves so that loads stay in flight: the load, at any
+// alignment, moved back where it would pass the row's end, and the shift that
+// undoes the move and leaves zeros beyond n.  Rows shorter than a chunk are
+// read byte by byte.
 template <bool A4>
 __device__ __forceinline__ i32x4_t any_load(const uint8_t* p, int j0, int n) {
-  uint32_t w[4] = {0, 0, 0, 0};
-  if (A4) {
-    uint32_t c[2] = {0, 0};
-    const int left = (n - j0) / 2;
-    if (left >= 8) {
-      memcpy(c, p + j0 / 2, 8);
-    } else {
-      for (int i = 0; i < left; ++i) c[i >> 2] |= static_cast<uint32_t>(p[j0 / 2 + i]) << (8 * (i & 3));
-    }
-    widen8(c[0], w[0], w[1]);
-    widen8(c[1], w[2], w[3]);
-  } else {
-    const int left = n - j0;
-    if (left >= 16) {
-      memcpy(w, p + j0, 16);
-    } else {
+  constexpr int kBytes = A4 ? 8 : 16;
+  const int bytes = A4 ? n / 2 : n;
+  i32x4_t w = {0, 0, 0, 0};
+  if (bytes >= kBytes) {  // the same for all lanes
+    memcpy(&w, p + min(A4 ? j0 / 2 : j0, bytes - kBytes), kBytes);
+  } else if (j0 == 0) {
+    uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < left) w[i >> 2] |= static_cast<uint32_t>(p[j0 + i]) << (8 * (i & 3));
-    }
+    for (int i = 0; i < kBytes; ++i)
+      if (i < bytes) b[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+    w = i32x4_t{static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
   }
-  return i32x4_t{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+  return w;
+}
+template <bool A4>
+__device__ __forceinline__ i32x4_t any_shift(const i32x4_t& w, int j0, int n) {
+  constexpr int kBytes = A4 ? 8 : 16;
+  const int bytes = A4 ? n / 2 : n;
+  const int by = max((A4 ? j0 / 2 : j0) - max(bytes - kBytes, 0), 0);  // bytes moved back
+  uint64_t lo = static_cast<uint32_t>(w[0]) | static_cast<uint64_t>(static_cast<uint32_t>(w[1])) << 32;
+  uint64_t hi = static_cast<uint32_t>(w[2]) | static_cast<uint64_t>(static_cast<uint32_t>(w[3])) << 32;
+  if (by >= 16) {
+    lo = hi = 0;
+  } else if (by >= 8) {
+    lo = hi >> (8 * (by - 8));
+    hi = 0;
+  } else if (by > 0) {
+    lo = lo >> (8 * by) | hi << (64 - 8 * by);
+    hi >>= 8 * by;
+  }
+  return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi), static_cast<int>(hi >> 32)};
+}
+template <bool A4>
+__device__ __forceinline__ i32x4_t any_operand(const i32x4_t& c) {
+  if (!A4) return c;
+  uint32_t b[4];
+  widen8(static_cast<uint32_t>(c[0]), b[0], b[1]);
+  widen8(static_cast<uint32_t>(c[1]), b[2], b[3]);
+  return i32x4_t{static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
 }
 
-template <bool A4>
-__global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
-  __shared__ i32x4_t lds[2][2][kAnyTile * 4];  // [buffer][weights, tokens]
+// Tile of WK x WT waves of FK x FT 16 x 16 results, steps of KU * 64 k.  Step s
+// multiplies from one LDS buffer while the registers with step s + 1 are written
+// to the other and filled with step s + 2 (three sets, for deeper loads, were no
+// faster).
+// LDS as in w8_tile: for each depth rows of 64 bytes, chunk c of row r at chunk
+// c ^ 2 ((r >> 3) & 1).
+template <bool A4, int WK, int WT, int FK, int FT, int KU>
+struct AnyTile {
+  static constexpr int kThreads = 64 * WK * WT;
+  static constexpr int kBN = 16 * WK * FK, kBM = 16 * WT * FT;
+  static constexpr int kStep = 64 * KU;
+  static constexpr int kWSlots = kBN * 4 * KU, kTSlots = kBM * 4 * KU;  // 16-byte chunks of a step
+  static constexpr int kWPer = kWSlots / kThreads, kTPer = kTSlots / kThreads;
+  static_assert(kWPer * kThreads == kWSlots && kTPer * kThreads == kTSlots, "whole chunks per thread");
+};
+
+template <bool A4, int WK, int WT, int FK, int FT, int KU>
+__global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
+  using C = AnyTile<A4, WK, WT, FK, FT, KU>;
+  __shared__ i32x4_t lds[2][C::kWSlots + C::kTSlots];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-  const int tiles_n = (a.R + kAnyTile - 1) / kAnyTile;
-  const int m0 = static_cast<int>(blockIdx.x / tiles_n) * kAnyTile;
-  const int n0 = static_cast<int>(blockIdx.x % tiles_n) * kAnyTile;
-  // thread -> tile row tid / 4, chunk tid % 4; rows clamped (not stored)
-  const int r = tid >> 2, c = tid & 3;
-  const uint8_t* pw = reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(min(n0 + r, a.R - 1)) * a.ldw;
-  const uint8_t* pt = a.a + static_cast<int64_t>(min(m0 + r, a.T - 1)) * a.lda;
-  const int slot = (r >> 4) * 64 + c * 16 + (r & 15);
-  const int steps = (a.n + 63) / 64;
-  const int wk = 2 * (wid & 1), wt = 2 * (wid >> 1);  // first 16-row group of channels and of tokens
-  i32x4_t acc[2][2] = {};
-  i32x4_t vw = any_load<false>(pw, 16 * c, a.n), vt = any_load<A4>(pt, 16 * c, a.n);
-  for (int s = 0; s < steps; ++s) {
-    const int b = s & 1;
-    lds[b][0][slot] = vw;
-    lds[b][1][slot] = vt;
-    __syncthreads();
-    if (s + 1 < steps) {
-      vw = any_load<false>(pw, 64 * (s + 1) + 16 * c, a.n);
-      vt = any_load<A4>(pt, 64 * (s + 1) + 16 * c, a.n);
-    }
-    i32x4_t fw[2], ft[2];
+  const int tiles_n = (a.R + C::kBN - 1) / C::kBN;
+  const int m0 = static_cast<int>(blockIdx.x / tiles_n) * C::kBM;
+  const int n0 = static_cast<int>(blockIdx.x % tiles_n) * C::kBN;
+  const int wk = wid % WK, wt = wid / WK;
+  const int steps = (a.n + C::kStep - 1) / C::kStep;
+
+  // chunk x of a thread: KU * 4 neighbouring threads share a row; rows clamped (not stored)
+  const uint8_t* pw[C::kWPer];
+  const uint8_t* pt[C::kTPer];
+  int kw[C::kWPer], kt[C::kTPer], sw[C::kWPer], st[C::kTPer];
+  auto slot = [](int r, int c, int rows) { return ((c >> 2) * rows + r) * 4 + ((c & 3) ^ (2 * ((r >> 3) & 1))); };
+  const int at = 4 * (lane & 15) + ((lane >> 4) ^ (2 * ((lane >> 3) & 1)));  // the lane's chunk of a 16-row group
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fw[i] = lds[b][0][(wk + i) * 64 + lane];
-      ft[i] = lds[b][1][(wt + i) * 64 + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], ft[j], acc[i][j], 0, 0, 0);
+  for (int x = 0; x < C::kWPer; ++x) {
+    const int e = tid + x * C::kThreads, r = e / (4 * KU), c = e % (4 * KU);
+    pw[x] = reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(min(n0 + r, a.R - 1)) * a.ldw;
+    kw[x] = 16 * c;
+    sw[x] = slot(r, c, C::kBN);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int t = m0 + 16 * (wt + j) + (lane & 15);
+  for (int x = 0; x < C::kTPer; ++x) {
+    const int e = tid + x * C::kThreads, r = e / (4 * KU), c = e % (4 * KU);
+    pt[x] = a.a + static_cast<int64_t>(min(m0 + r, a.T - 1)) * a.lda;
+    kt[x] = 16 * c;
+    st[x] = C::kWSlots + slot(r, c, C::kBM);
+  }
+  i32x4_t vw[C::kWPer], vt[C::kTPer];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int x = 0; x < C::kWPer; ++x) vw[x] = any_load<false>(pw[x], C::kStep * s + kw[x], a.n);
+#pragma unroll
+    for (int x = 0; x < C::kTPer; ++x) vt[x] = any_load<A4>(pt[x], C::kStep * s + kt[x], a.n);
+  };
+  auto store = [&](int s) {
+    if (s == steps - 1) {
+#pragma unroll
+      for (int x = 0; x < C::kWPer; ++x) vw[x] = any_shift<false>(vw[x], C::kStep * s + kw[x], a.n);
+#pragma unroll
+      for (int x = 0; x < C::kTPer; ++x) vt[x] = any_shift<A4>(vt[x], C::kStep * s + kt[x], a.n);
+    }
+#pragma unroll
+    for (int x = 0; x < C::kWPer; ++x) lds[s & 1][sw[x]] = vw[x];
+#pragma unroll
+    for (int x = 0; x < C::kTPer; ++x) lds[s & 1][st[x]] = any_operand<A4>(vt[x]);
+  };
+  i32x4_t acc[FK][FT];
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
+
+  load(0);
+  store(0);
+  if (steps > 1) load(1);
+  __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    const int buf = s & 1;
+    i32x4_t fw[KU][FK], ft[KU][FT];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+#pragma unroll
+      for (int f = 0; f < FK; ++f) fw[u][f] = lds[buf][(u * C::kBN + 16 * (wk * FK + f)) * 4 + at];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) ft[u][j] = lds[buf][C::kWSlots + (u * C::kBM + 16 * (wt * FT + j)) * 4 + at];
+    }
+    if (s + 1 < steps) {
+      store(s + 1);
+      if (s + 2 < steps) load(s + 2);
+    }
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+#pragma unroll
+      for (int f = 0; f < FK; ++f)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+          acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][f], ft[u][j], acc[f][j], 0, 0, 0);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int t = m0 + 16 * (wt * FT + j) + (lane & 15);
     if (t >= a.T) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int f = 0; f < FK; ++f)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int k = n0 + 16 * (wk + i) + 4 * (lane >> 4) + e;
-        if (k < a.R) row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, acc[i][j][e]), a.out_bf16);
+        const int k = n0 + 16 * (wk * FK + f) + 4 * (lane >> 4) + e;
+        if (k < a.R)
+          row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, acc[f][j][e]), a.out_bf16);
       }
   }
 }
 
-hipError_t run_tiles(const W8Args& a, hipStream_t s) {
-  const Plan p = tile_plan(a.T, a.n, a.R, a.a4 != 0);
+constexpr double kAnyOne = 0.62, kAnyTwo = 0.73;  // as in TileCost, for its 64 x 64 tile
+
+template <bool A4>
+hipError_t run_any(const W8Args& a, hipStream_t s) {
+  using C = AnyTile<A4, 2, 2, 2, 2, 2>;
+  const int tiles = ((a.T + C::kBM - 1) / C::kBM) * ((a.R + C::kBN - 1) / C::kBN);
+  w8_any_kernel<A4, 2, 2, 2, 2, 2>
+      <<<dim3(static_cast<unsigned>(tiles)), dim3(static_cast<unsigned>(C::kThreads)), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Few tokens: as w8_few, with both operands straight to registers, a lane (g, i)
+// reading 16 bytes (g) of row i for each 64 k.
+template <bool A4, int FT>
+__global__ __launch_bounds__(1024) void w8_few_any_kernel(W8Args a) {
+  extern __shared__ __attribute__((aligned(16))) int32_t few_part[];  // [wave][FT][64][4]
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int g = lane >> 4, i = lane & 15;
+  const int n0 = 16 * blockIdx.x;
+  const uint8_t* const pw =
+      reinterpret_cast<const uint8_t*>(a.w) + static_cast<int64_t>(min(n0 + i, a.R - 1)) * a.ldw;
+  const uint8_t* pt[FT];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) pt[j] = a.a + static_cast<int64_t>(min(16 * j + i, a.T - 1)) * a.lda;
+  i32x4_t acc[FT];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
+  auto unit = [&](int k0, bool last) {
+    i32x4_t w[2], tok[2][FT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int k = k0 + 64 * s + 16 * g;
+      w[s] = any_load<false>(pw, k, a.n);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) tok[s][j] = any_load<A4>(pt[j], k, a.n);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (last) w[s] = any_shift<false>(w[s], k0 + 64 * s + 16 * g, a.n);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        if (last) tok[s][j] = any_shift<A4>(tok[s][j], k0 + 64 * s + 16 * g, a.n);
+        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], any_operand<A4>(tok[s][j]), acc[j], 0, 0, 0);
+      }
+    }
+  };
+  int k0 = kUnit * wid;
+  for (; k0 + kUnit <= a.n; k0 += kUnit * waves) unit(k0, false);
+  if (k0 < a.n) unit(k0, true);
+#pragma unroll
+  for (int j = 0; j < FT; ++j)
+    *reinterpret_cast<i32x4_t*>(few_part + 4 * ((wid * FT + j) * 64 + lane)) = acc[j];
+  __syncthreads();
+  few_finish<1, FT>(a, few_part, n0, waves);
+}
+
+template <bool A4>
+hipError_t run_few_any(const W8Args& a, hipStream_t s) {
+  const int groups = (a.R + 15) / 16;
+  int waves = 16;
+  while (waves > 4 && (groups * waves > 32 * kCus || (a.n + kUnit - 1) / kUnit < waves)) waves /= 2;
+  const dim3 grid(static_cast<unsigned>(groups)), block(static_cast<unsigned>(64 * waves));
+  if (a.T <= 16)
+    w8_few_any_kernel<A4, 1><<<grid, block, static_cast<unsigned>(1024 * waves), s>>>(a);
+  else
+    w8_few_any_kernel<A4, 2><<<grid, block, static_cast<unsigned>(2048 * waves), s>>>(a);
+  return hipGetLastError();
+}
+
+// Many tokens: the rows are laid out anew in the workspace, in whole chunks with
+// zeros beyond n, and the tile kernels run on those.  One launch for both
+// operands: rows 0 .. rows_w - 1 are the weights', the rest the codes'.
+struct PackArgs {
+  const uint8_t* src[2];
+  uint8_t* dst[2];
+  int64_t ld[2];
+  int bytes[2], chunks[2];
+  int64_t rows[2];
+};
+__global__ __launch_bounds__(256) void w8_pack_kernel(PackArgs a) {
+  for (int64_t row = blockIdx.x; row < a.rows[0] + a.rows[1]; row += gridDim.x) {
+    const int x = row < a.rows[0] ? 0 : 1;
+    const int64_t r = x ? row - a.rows[0] : row;
+    const uint8_t* const src = a.src[x] + r * a.ld[x];
+    i32x4_t* const dst = reinterpret_cast<i32x4_t*>(a.dst[x]) + r * a.chunks[x];
+    for (int c = threadIdx.x; c < a.chunks[x]; c += blockDim.x) {
+      i32x4_t v = any_load<false>(src, 16 * c, a.bytes[x]);
+      if (16 * c + 16 > a.bytes[x]) v = any_shift<false>(v, 16 * c, a.bytes[x]);
+      dst[c] = v;
+    }
+  }
+}
+
+hipError_t run_pack(const PackArgs& a, hipStream_t s) {
+  const int64_t rows = a.rows[0] + a.rows[1];
+  const int waves = (a.chunks[0] + 63) / 64;
+  w8_pack_kernel<<<dim3(static_cast<unsigned>(rows < 64 * kCus ? rows : 64 * kCus)),
+                   dim3(static_cast<unsigned>(64 * (waves < 4 ? waves : 4))), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Where the operands of a product that packs lie in its workspace: the weights,
+// the codes unless their rows are aligned already, then the partial sums.
+struct Packed {
+  int n;          // k of the packed rows
+  bool codes;     // the codes are packed too
+  int64_t w_bytes, t_bytes;
+};
+Packed packing(const W8Args& a) {
+  Packed p;
+  p.n = a.a4 ? (a.n + 31) / 32 * 32 : (a.n + 15) / 16 * 16;
+  p.codes = a.lda % 16 != 0 || (reinterpret_cast<uintptr_t>(a.a) & 15u) != 0 || a.lda >= kMaxPitch;
+  p.w_bytes = static_cast<int64_t>(a.R) * p.n;
+  p.t_bytes = p.codes ? static_cast<int64_t>(a.T) * (a.a4 ? p.n / 2 : p.n) : 0;
+  return p;
+}
+
+hipError_t run_tiles(const W8Args& a, const Plan& p, hipStream_t s) {
   if (a.a4) {
     switch (p.kind) {
       case 0: return run_tile<true, 2, 4, 8, 4, 1, 4>(a, p.splits, s);
@@ -842,58 +1052,89 @@ hipError_t run_tiles(const W8Args& a, hipStream_t s) {
   }
 }
 
-// Up to 32 tokens: 32 x 14336 x 4096 16.9 us, 32 x 4096 x 4096 7.1 us, the best
-// tile 17.3 and 10.5.
-bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24); }
+// The way a product takes.
+struct Way {
+  enum { kFew, kFewAny, kAny, kTiles, kPackTiles } kind;
+  Plan plan;  // kTiles, kPackTiles
+};
+Way way_of(const W8Args& a) {
+  const bool aligned = aligned_rows(a);
+  if (takes_few(a.T, a.R)) return {aligned ? Way::kFew : Way::kFewAny, {0, 1, 0}};
+  if (aligned) return {Way::kTiles, tile_plan(a.T, a.n, a.R, a.a4 != 0)};
+  const Packed k = packing(a);
+  Plan p = tile_plan(a.T, k.n, a.R, a.a4 != 0);
+  // packing: a launch and the workspace, and 4 TB/s over what it reads and writes
+  p.us += 5.0 + 2.0 * (k.w_bytes + k.t_bytes) / 4e6;
+  const double tiles = static_cast<double>((a.T + int64_t{63}) / 64) * static_cast<double>((a.R + int64_t{63}) / 64);
+  const double per_cu = ceil(tiles / kCus), deep = a.n / 128.0;
+  const double any =
+      floor(per_cu / 2) * (deep * kAnyTwo + 1.5) + fmod(per_cu, 2) * (deep * kAnyOne + 1.5);
+  if (any < p.us && tiles < (1 << 22)) return {Way::kAny, {0, 1, any}};
+  return {Way::kPackTiles, p};
+}
 
 }  // namespace
 
-int64_t w8_workspace(int64_t tokens, int64_t n, int64_t rows, bool a4) {
-  if (tokens == 0 || rows == 0 || takes_few(tokens, rows)) return 0;
-  const Plan p = tile_plan(tokens, n, rows, a4);
-  const TileCost& t = a4 ? kTiles4[p.kind] : kTiles8[p.kind];
-  if (p.splits == 1) return 0;
-  return ((tokens + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn) * p.splits * t.bm * t.bn * 4;
+int64_t w8_workspace(const W8Args& a) {
+  if (a.T == 0 || a.R == 0) return 0;
+  const Way way = way_of(a);
+  int64_t bytes = 0;
+  if (way.kind == Way::kPackTiles) {
+    const Packed k = packing(a);
+    bytes = k.w_bytes + k.t_bytes;
+  }
+  if (way.plan.splits > 1) {
+    const TileCost& t = a.a4 ? kTiles4[way.plan.kind] : kTiles8[way.plan.kind];
+    bytes += ((static_cast<int64_t>(a.T) + t.bm - 1) / t.bm) * ((static_cast<int64_t>(a.R) + t.bn - 1) / t.bn) *
+             way.plan.splits * t.bm * t.bn * 4;
+  }
+  return bytes;
 }
 
 const char* w8_name(const W8Args& a) {
-  if (!aligned_rows(a)) return "w8_any";
-  if (takes_few(a.T, a.R)) return "w8_few";
-  const Plan p = tile_plan(a.T, a.n, a.R, a.a4 != 0);
-  static const char* const names8[5][2] = {{"w8_tile_256x256", "w8_tile_256x256_split"},
-                                           {"w8_tile_128x128", "w8_tile_128x128_split"},
-                                           {"w8_tile_64x128", "w8_tile_64x128_split"},
-                                           {"w8_tile_64x64", "w8_tile_64x64_split"},
-                                           {"w8_tile_64x64_deep", "w8_tile_64x64_deep_split"}};
-  static const char* const names4[2] = {"w8_tile_128x64", "w8_tile_128x64_split"};
-  return a.a4 && p.kind == 2 ? names4[p.splits > 1] : names8[p.kind][p.splits > 1];
+  if (a.T == 0 || a.R == 0) return "none";
+  const Way way = way_of(a);
+  static const char* const names[2][6] = {{"w8_tile_256x256", "w8_tile_128x128", "w8_tile_64x128", "w8_tile_64x64",
+                                           "w8_tile_64x64_deep", "w8_tile_128x64"},
+                                          {"w8_pack_tile_256x256", "w8_pack_tile_128x128", "w8_pack_tile_64x128",
+                                           "w8_pack_tile_64x64", "w8_pack_tile_64x64_deep", "w8_pack_tile_128x64"}};
+  switch (way.kind) {
+    case Way::kFew: return "w8_few";
+    case Way::kFewAny: return "w8_few_any";
+    case Way::kAny: return "w8_any";
+    default: return names[way.kind == Way::kPackTiles][a.a4 && way.plan.kind == 2 ? 5 : way.plan.kind];
+  }
 }
 
 hipError_t launch_w8(const W8Args& all, hipStream_t s) {
-  if (aligned_rows(all)) {
-    if (takes_few(all.T, all.R)) return all.a4 ? run_few<true>(all, s) : run_few<false>(all, s);
-    return run_tiles(all, s);
+  W8Args a = all;
+  a.row_bytes = a.a4 ? a.n / 2 : a.n;
+  const Way way = way_of(a);
+  switch (way.kind) {
+    case Way::kFew: return a.a4 ? run_few<true>(a, s) : run_few<false>(a, s);
+    case Way::kFewAny: return a.a4 ? run_few_any<true>(a, s) : run_few_any<false>(a, s);
+    case Way::kAny: return a.a4 ? run_any<true>(a, s) : run_any<false>(a, s);
+    case Way::kTiles: return run_tiles(a, way.plan, s);
+    case Way::kPackTiles: break;
   }
-  // a launch holds fewer than 2^32 threads in one dimension: token ranges of at most 2^22 tiles
-  const int64_t tiles_n = (static_cast<int64_t>(all.R) + kAnyTile - 1) / kAnyTile;
-  if (tiles_n > (int64_t{1} << 22)) return hipErrorInvalidConfiguration;
-  const int64_t step = ((int64_t{1} << 22) / tiles_n) * kAnyTile;
-  for (int64_t t = 0; t < all.T; t += step) {
-    W8Args a = all;
-    a.T = static_cast<int>(step < all.T - t ? step : all.T - t);
-    a.a += t * a.lda;
-    a.scale += t;
-    if (a.a4) a.zero += t;
-    a.out = static_cast<uint8_t*>(a.out) + t * a.ldo * (a.out_bf16 ? 2 : 4);
-    const dim3 grid(static_cast<unsigned>(((a.T + kAnyTile - 1) / kAnyTile) * tiles_n)), block(256);
-    if (a.a4)
-      w8_any_kernel<true><<<grid, block, 0, s>>>(a);
-    else
-      w8_any_kernel<false><<<grid, block, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const Packed k = packing(a);
+  uint8_t* const at = reinterpret_cast<uint8_t*>(a.partial);
+  const int pitch = a.a4 ? k.n / 2 : k.n;
+  const PackArgs pack = {{reinterpret_cast<const uint8_t*>(a.w), a.a}, {at, at + k.w_bytes},   {a.ldw, a.lda},
+                         {a.n, a.row_bytes},                           {k.n / 16, pitch / 16}, {a.R, k.codes ? a.T : 0}};
+  const hipError_t e = run_pack(pack, s);
+  if (e != hipSuccess) return e;
+  a.w = reinterpret_cast<const int8_t*>(at);
+  a.ldw = a.n = k.n;
+  if (k.codes) {
+    a.a = at + k.w_bytes;
+    a.lda = pitch;
   }
-  return hipSuccess;
+  // aligned codes are read to the end of their last 16-byte chunk, which lies in
+  // the page of its first byte; whatever is there meets weights of zero
+  a.row_bytes = pitch;
+  a.partial = reinterpret_cast<int32_t*>(at + k.w_bytes + k.t_bytes);
+  return run_tiles(a, way.plan, s);
 }
 
 }  // namespace signrot

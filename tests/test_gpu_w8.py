@@ -237,6 +237,50 @@ def test_int4_w8_linear_strides_offsets_and_guards(t):
         assert (buf[:, rows:] == GUARD).all()
 
 
+@pytest.mark.parametrize("t,n,rows", [(1030, 4099, 2050), (2100, 2047, 2304), (4100, 1023, 1100)])
+def test_large_unaligned_rows_are_laid_out_anew(t, n, rows):
+    """Both operands unaligned; codes in aligned rows that end inside a chunk, with
+    other bytes after them, unaligned weights; packed INT4 codes."""
+    codes, s, z, w, v, b = operands(t, n, rows, 6, False)
+    ref = B.w8_linear(codes.astype(np.float64), s, None, w, v, b)
+    dw = dev(w)
+    for c in (dev(codes), strided(codes, (n + 15) // 16 * 16)):
+        name = R.int8_linear_kernel_name(c, dw)
+        assert name.startswith("w8_pack_tile"), name
+        check_product(R.int8_linear(c, dev(s), dw, dev(v), bias=dev(b), dtype=torch.float32), ref, s, v,
+                      torch.float32, f"int8_linear {t} x {n} x {rows} [{name}]")
+    n4 = n + 1 + 2 * (n % 4 == 3)  # even, and no multiple of four bytes of codes
+    codes, s, z, w, v, b = operands(t, n4, rows, 7, True)
+    ref = B.w8_linear(B.unpack_int4(codes), s, z, w, v, b)
+    c, dw = dev(codes), dev(w)
+    name = R.int4_w8_linear_kernel_name(c, dw)
+    assert name.startswith("w8_pack_tile"), name
+    got = R.int4_w8_linear(c, dev(s), dev(z), dw, dev(v), dev(w.sum(axis=1, dtype=np.int32)), bias=dev(b),
+                           dtype=torch.float32)
+    check_product(got, ref, s, v, torch.float32, f"int4_w8_linear {t} x {n4} x {rows} [{name}]")
+
+
+@pytest.mark.parametrize("t,n,rows,kind", [
+    (64, 14336, 512, "tile_64x64"), (70, 4096, 4096, "tile_64x64"), (512, 4096, 4096, "tile_64x128"),
+    (1024, 4096, 2048, "tile_64x128"), (2048, 4096, 4096, "tile_128x128"), (4096, 2048, 4096, "tile_256x256"),
+    (2048, 14336, 4096, "tile_256x256"), (64, 28672, 2048, "tile_64x64")])
+def test_every_tile_and_split_against_the_definition(t, n, rows, kind):
+    """Shapes at which the plan takes each of its tiles, some with the row split."""
+    codes, s, _, w, v, _ = operands(t, n, rows, 8, False)
+    ref = B.w8_linear(codes.astype(np.float64), s, None, w, v, None)
+    c, dw = dev(codes), dev(w)
+    name = R.int8_linear_kernel_name(c, dw)
+    assert kind in name, name
+    check_product(R.int8_linear(c, dev(s), dw, dev(v), dtype=torch.float32), ref, s, v, torch.float32,
+                  f"int8_linear {t} x {n} x {rows} [{name}]")
+    codes, s, z, w, v, _ = operands(t, n, rows, 9, True)
+    ref = B.w8_linear(B.unpack_int4(codes), s, z, w, v, None)
+    c, dw = dev(codes), dev(w)
+    got = R.int4_w8_linear(c, dev(s), dev(z), dw, dev(v), dev(w.sum(axis=1, dtype=np.int32)), dtype=torch.float32)
+    check_product(got, ref, s, v, torch.float32,
+                  f"int4_w8_linear {t} x {n} x {rows} [{R.int4_w8_linear_kernel_name(c, dw)}]")
+
+
 def test_products_over_four_gib_offsets():
     """An output whose last rows lie beyond 2^31 and 2^32 bytes."""
     t, n, rows = 140000, 64, 8192

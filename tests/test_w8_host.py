@@ -59,17 +59,31 @@ def test_int4_w8_linear_argument_errors(L):
 @pytest.mark.parametrize("t,n,rows", [(1, 14336, 4096), (16, 4096, 14336), (70, 4096, 512), (200, 11008, 4096),
                                       (8192, 4096, 14336), (613, 1111, 777)])
 def test_workspace_sizes_are_checked(L, t, n, rows):
-    need = L.signrot_int8_linear_workspace(t, n, rows)
+    need = L.signrot_int8_linear_workspace(FAKE, n, t, n, FAKE, n, rows)
     assert need >= 0
     if need:
         args = (FAKE, n, FAKE, t, n, FAKE, n, FAKE, None, rows, FAKE, rows, 1)
         assert L.signrot_int8_linear(*args, None, 0, None) == R.SIGNROT_EINVAL
         assert L.signrot_int8_linear(*args, FAKE, need - 1, None) == R.SIGNROT_EINVAL
         assert L.signrot_int8_linear(*args, FAKE + 4, need, None) == R.SIGNROT_EINVAL
-    assert L.signrot_int8_linear_workspace(t, 0, rows) == -1
-    assert L.signrot_int8_linear_workspace(-1, n, rows) == -1
-    assert L.signrot_int4_w8_linear_workspace(t, 3, rows) == -1
-    assert L.signrot_int4_w8_linear_workspace(t, 64, rows) >= 0
+    assert L.signrot_int8_linear_workspace(FAKE, n, t, 0, FAKE, n, rows) == -1
+    assert L.signrot_int8_linear_workspace(FAKE, n, -1, n, FAKE, n, rows) == -1
+    assert L.signrot_int8_linear_workspace(FAKE, n, t, n, FAKE, n - 1, rows) == -1
+    assert L.signrot_int4_w8_linear_workspace(FAKE, t, 3, FAKE, 3, rows) == -1
+    assert L.signrot_int4_w8_linear_workspace(FAKE, t, 64, FAKE, 64, rows) >= 0
+
+
+def test_workspace_holds_the_rows_that_are_laid_out_anew(L):
+    """Large unaligned weights and, if they are unaligned too, codes are packed into the workspace."""
+    t, n, rows = 4096, 4096, 8192
+    aligned = L.signrot_int8_linear_workspace(FAKE, n, t, n, FAKE, n, rows)
+    assert L.signrot_int8_linear_workspace(FAKE, n, t, n, FAKE + 1, n, rows) == aligned + rows * n
+    assert L.signrot_int8_linear_workspace(FAKE + 1, n, t, n, FAKE, n, rows) == aligned + (t + rows) * n
+    assert L.signrot_int8_linear_workspace(FAKE, 5001, t, 5001, FAKE, 5001, rows) >= (t + rows) * 5008
+    assert L.signrot_int4_w8_linear_workspace(FAKE, t, 5002, FAKE, 5002, rows) >= t * 2512 + rows * 5024
+    # small ones and few tokens are not
+    assert L.signrot_int8_linear_workspace(FAKE, 1111, 613, 1111, FAKE, 1111, 777) == 0
+    assert L.signrot_int8_linear_workspace(FAKE, 5001, 32, 5001, FAKE, 5001, rows) == 0
 
 
 def test_kernel_names_are_host_only(L):
