@@ -419,37 +419,40 @@ def _type_of(dtype, what):
     raise ValueError(f"{what} must be bfloat16 or float32, not {dtype}")
 
 
-def _matrix(v, name, rows, n, dtype, device):
-    """(pointer, row stride) of a [rows, n] tensor with contiguous rows; None sizes are free."""
-    if v.dtype is not dtype or v.dim() != 2 or v.device != device:
-        raise ValueError(f"{name} must be a 2-D {dtype} tensor on {device}")
+def _matrix(v, name, rows, n, dtype, gpu):
+    """(pointer, row stride) of a [rows, n] tensor with contiguous rows on GPU
+    number `gpu`; None sizes are free."""
     shape = v.shape
-    if (rows is not None and shape[0] != rows) or (n is not None and shape[1] != n):
+    if v.dtype is not dtype or len(shape) != 2 or v.get_device() != gpu:
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor on GPU {gpu}")
+    t, m = shape
+    if (rows is not None and t != rows) or (n is not None and m != n):
         raise ValueError(f"{name} has shape {tuple(shape)}, not [{'*' if rows is None else rows}, "
                          f"{'*' if n is None else n}]")
     step, unit = v.stride()
-    if unit != 1 and shape[1] > 1:
+    if unit != 1 and m > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    if shape[0] <= 1:
-        step = shape[1]
-    elif step < shape[1]:
+    if t <= 1:
+        step = max(step, m)
+    elif step < m:
         raise ValueError(f"{name} rows overlap")
     return v.data_ptr(), step
 
 
-def _vector(v, name, size, dtype, device):
+def _vector(v, name, size, dtype, gpu):
     """Pointer of a contiguous vector of `size` entries, 0 for None."""
     if v is None:
         return 0
-    if v.dtype is not dtype or v.numel() != size or v.device != device or not v.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {size} entries on {device}")
+    if v.dtype is not dtype or v.numel() != size or v.get_device() != gpu or not v.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {size} entries on GPU {gpu}")
     return v.data_ptr()
 
 
 def _on_gpu(v, name):
+    """(device, its number) of a GPU tensor."""
     if not v.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return v.device
+    return v.device, v.get_device()
 
 
 def _empty_codes(t, n, device):
@@ -457,9 +460,9 @@ def _empty_codes(t, n, device):
     import torch
 
     if n % 16 == 0:
-        return torch.empty((t, n), dtype=torch.int8, device=device), n
+        return torch.empty(t, n, dtype=torch.int8, device=device), n
     pitch = (n + 15) // 16 * 16
-    return torch.empty((t, pitch), dtype=torch.int8, device=device)[:, :n], pitch
+    return torch.empty(t, pitch, dtype=torch.int8, device=device)[:, :n], pitch
 
 
 def signrot_quant_int8(x, sums: bool = False, out=None):
@@ -470,8 +473,8 @@ def signrot_quant_int8(x, sums: bool = False, out=None):
     multiple of 16).  `out` may pass preallocated (codes, scale[, sum])."""
     import torch
 
-    device = _on_gpu(x, "x")
-    ptr, ld = _matrix(x, "x", None, None, torch.bfloat16, device)
+    device, gpu = _on_gpu(x, "x")
+    ptr, ld = _matrix(x, "x", None, None, torch.bfloat16, gpu)
     t, n = x.shape
     if out is None:
         codes, ldc = _empty_codes(t, n, device)
@@ -482,24 +485,24 @@ def signrot_quant_int8(x, sums: bool = False, out=None):
         out = tuple(out[:3 if sums else 2])
         if len(out) < (3 if sums else 2):
             raise ValueError("out must hold (codes, scale[, sum])")
-        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
-        sptr = _vector(out[1], "scale", t, torch.float32, device)
+        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, gpu)
+        sptr = _vector(out[1], "scale", t, torch.float32, gpu)
     check(lib().signrot_quant_int8(ptr, t, n, ld, qptr, ldc, sptr,
-                                   _vector(out[2], "sum", t, torch.int32, device) if sums else 0, _stream_of(x)),
+                                   _vector(out[2], "sum", t, torch.int32, gpu) if sums else 0, _stream_of(x)),
           "signrot_quant_int8")
     return out
 
 
-def _product_out(out, dtype, t, rows, device):
+def _product_out(out, dtype, t, rows, device, gpu):
     """(out, its type, pointer, row stride), allocated when the caller gave none."""
     import torch
 
     if out is None:
-        out = torch.empty((t, rows), dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+        out = torch.empty(t, rows, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
         return out, _type_of(out.dtype, "out"), out.data_ptr(), rows
     if dtype is not None and out.dtype is not dtype:
         raise ValueError(f"out is {out.dtype}, dtype {dtype}")
-    ptr, ldo = _matrix(out, "out", t, rows, out.dtype, device)
+    ptr, ldo = _matrix(out, "out", t, rows, out.dtype, gpu)
     return out, _type_of(out.dtype, "out"), ptr, ldo
 
 
@@ -520,15 +523,15 @@ def signrot_int8_linear(codes, scale, w, w_scale, bias=None, dtype=None, out=Non
     exact in int32.  `out` may pass the result's tensor."""
     import torch
 
-    device = _on_gpu(codes, "codes")
-    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, device)
+    device, gpu = _on_gpu(codes, "codes")
+    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, gpu)
     t, n = codes.shape
-    wptr, ldw = _matrix(w, "w", None, n, torch.int8, device)
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, gpu)
     rows = w.shape[0]
-    sptr = _vector(scale, "scale", t, torch.float32, device)
-    vptr = _vector(w_scale, "w_scale", rows, torch.float32, device)
-    bptr = _vector(bias, "bias", rows, torch.float32, device)
-    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
+    sptr = _vector(scale, "scale", t, torch.float32, gpu)
+    vptr = _vector(w_scale, "w_scale", rows, torch.float32, gpu)
+    bptr = _vector(bias, "bias", rows, torch.float32, gpu)
+    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device, gpu)
     L = lib()
     ws, size, _owner = _workspace(L.signrot_int8_linear_workspace(aptr, lda, t, n, wptr, ldw, rows), device)
     check(L.signrot_int8_linear(aptr, lda, sptr, t, n, wptr, ldw, vptr, bptr, rows, optr, ldo, kind, ws, size,
@@ -543,18 +546,18 @@ def signrot_int4_w8_linear(codes, scale, zero, w, w_scale, w_sum, bias=None, dty
     [T, rows] of `dtype` (bfloat16, the default, or float32)."""
     import torch
 
-    device = _on_gpu(codes, "codes")
+    device, gpu = _on_gpu(codes, "codes")
     if codes.dtype is not torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous 2-D uint8 tensor")
     t, n = codes.shape[0], codes.shape[1] * 2
-    wptr, ldw = _matrix(w, "w", None, n, torch.int8, device)
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, gpu)
     rows = w.shape[0]
-    sptr = _vector(scale, "scale", t, torch.float32, device)
-    zptr = _vector(zero, "zero", t, torch.float32, device)
-    vptr = _vector(w_scale, "w_scale", rows, torch.float32, device)
-    uptr = _vector(w_sum, "w_sum", rows, torch.int32, device)
-    bptr = _vector(bias, "bias", rows, torch.float32, device)
-    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device)
+    sptr = _vector(scale, "scale", t, torch.float32, gpu)
+    zptr = _vector(zero, "zero", t, torch.float32, gpu)
+    vptr = _vector(w_scale, "w_scale", rows, torch.float32, gpu)
+    uptr = _vector(w_sum, "w_sum", rows, torch.int32, gpu)
+    bptr = _vector(bias, "bias", rows, torch.float32, gpu)
+    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device, gpu)
     L = lib()
     aptr = codes.data_ptr()
     ws, size, _owner = _workspace(L.signrot_int4_w8_linear_workspace(aptr, t, n, wptr, ldw, rows), device)
@@ -566,8 +569,8 @@ def signrot_int4_w8_linear(codes, scale, zero, w, w_scale, w_sum, bias=None, dty
 def int8_linear_kernel_name(codes, w) -> str | None:
     import torch
 
-    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, codes.device)
-    wptr, ldw = _matrix(w, "w", None, codes.shape[1], torch.int8, codes.device)
+    aptr, lda = _matrix(codes, "codes", None, None, torch.int8, codes.get_device())
+    wptr, ldw = _matrix(w, "w", None, codes.shape[1], torch.int8, codes.get_device())
     r = lib().signrot_int8_linear_kernel_name(aptr, lda, codes.shape[0], codes.shape[1], wptr, ldw, w.shape[0])
     return r.decode() if r else None
 
@@ -576,7 +579,7 @@ def int4_w8_linear_kernel_name(codes, w) -> str | None:
     import torch
 
     n = codes.shape[1] * 2
-    wptr, ldw = _matrix(w, "w", None, n, torch.int8, codes.device)
+    wptr, ldw = _matrix(w, "w", None, n, torch.int8, codes.get_device())
     r = lib().signrot_int4_w8_linear_kernel_name(codes.data_ptr(), codes.shape[0], n, wptr, ldw, w.shape[0])
     return r.decode() if r else None
 
@@ -602,13 +605,13 @@ _pack_norm_args = struct.Struct("@" + "".join(
     for _, kind in _ResidualNormArgs._fields_)).pack
 
 
-def _modulation(v, name, t, n, index, dtype, device):
+def _modulation(v, name, t, n, index, dtype, gpu):
     """(pointer, stride, rows) of a gate or modulation: [n] shared by all rows, or [m, n]."""
     if v is None:
         return 0, 0, None
     if v.dim() == 1:
-        return _vector(v, name, n, dtype, device), 0, None
-    ptr, step = _matrix(v, name, None, n, dtype, device)
+        return _vector(v, name, n, dtype, gpu), 0, None
+    ptr, step = _matrix(v, name, None, n, dtype, gpu)
     if v.shape[0] < (1 if index is not None else t):
         raise ValueError(f"{name} has {v.shape[0]} rows for {t} tokens")
     return ptr, step, v.shape[0]
@@ -619,11 +622,11 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
     """Checks, allocates what the caller did not give and launches; `codes`: out is (codes, scale), not u."""
     import torch
 
-    device = _on_gpu(h, "h")
+    device, gpu = _on_gpu(h, "h")
     h_type = _type_of(h.dtype, "h")
-    hptr, ldh = _matrix(h, "h", None, None, h.dtype, device)
+    hptr, ldh = _matrix(h, "h", None, None, h.dtype, gpu)
     t, n = h.shape
-    yptr, ldy = (0, 0) if y is None else _matrix(y, "y", t, n, torch.bfloat16, device)
+    yptr, ldy = (0, 0) if y is None else _matrix(y, "y", t, n, torch.bfloat16, gpu)
     post_norm = norm if post_norm is None else post_norm
     if norm not in _NORMS or post_norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}")
@@ -635,38 +638,38 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
     p_type = _type_of(param, "the norm's parameters")
     gptr, mptr, cptr, ldg, ldm, mod_rows = 0, 0, 0, 0, 0, 0
     if gate is not None or mod_scale is not None or mod_shift is not None:
-        gptr, ldg, grows = _modulation(gate, "gate", t, n, mod_index, param, device)
-        mptr, ldm, mrows = _modulation(mod_scale, "mod_scale", t, n, mod_index, param, device)
-        cptr, ldm2, crows = _modulation(mod_shift, "mod_shift", t, n, mod_index, param, device)
+        gptr, ldg, grows = _modulation(gate, "gate", t, n, mod_index, param, gpu)
+        mptr, ldm, mrows = _modulation(mod_scale, "mod_scale", t, n, mod_index, param, gpu)
+        cptr, ldm2, crows = _modulation(mod_shift, "mod_shift", t, n, mod_index, param, gpu)
         if not mptr:
             ldm = ldm2
         elif cptr and ldm != ldm2:
             raise ValueError("mod_scale and mod_shift must have the same row stride")
         mod_rows = min((r for r in (grows, mrows, crows) if r is not None), default=0)
     if h_out is None:
-        h_out = torch.empty((t, n), dtype=h.dtype, device=device)
+        h_out = torch.empty(t, n, dtype=h.dtype, device=device)
         hoptr, ldho = h_out.data_ptr(), n
     else:
-        hoptr, ldho = _matrix(h_out, "h_out", t, n, h.dtype, device)
+        hoptr, ldho = _matrix(h_out, "h_out", t, n, h.dtype, gpu)
     uptr, ldu, qptr, ldc, sptr = 0, 0, 0, 0, 0
     if not codes:
         if out is None:
-            out = torch.empty((t, n), dtype=torch.bfloat16, device=device)
+            out = torch.empty(t, n, dtype=torch.bfloat16, device=device)
             uptr, ldu = out.data_ptr(), n
         else:
-            uptr, ldu = _matrix(out, "u", t, n, torch.bfloat16, device)
+            uptr, ldu = _matrix(out, "u", t, n, torch.bfloat16, gpu)
     elif out is None:
         q, ldc = _empty_codes(t, n, device)
         out = (q, torch.empty(t, dtype=torch.float32, device=device))
         qptr, sptr = q.data_ptr(), out[1].data_ptr()
     else:
-        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, device)
-        sptr = _vector(out[1], "scale", t, torch.float32, device)
+        qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, gpu)
+        sptr = _vector(out[1], "scale", t, torch.float32, gpu)
     args = _pack_norm_args(
         t, n, hptr, ldh, yptr, ldy, hoptr, ldho, uptr, ldu, qptr, ldc, sptr,
-        _vector(post_weight, "post_weight", n, param, device), _vector(post_bias, "post_bias", n, param, device),
-        gptr, ldg, _vector(weight, "weight", n, param, device), _vector(bias, "bias", n, param, device),
-        mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, device), mod_rows,
+        _vector(post_weight, "post_weight", n, param, gpu), _vector(post_bias, "post_bias", n, param, gpu),
+        gptr, ldg, _vector(weight, "weight", n, param, gpu), _vector(bias, "bias", n, param, gpu),
+        mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, gpu), mod_rows,
         alpha, beta, eps if post_eps is None else post_eps, eps, _NORMS[post_norm], _NORMS[norm], h_type, p_type)
     check(lib().signrot_residual_norm(args, _stream_of(h)), where)
     return h_out, out
