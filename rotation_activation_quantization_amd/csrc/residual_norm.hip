@@ -22,18 +22,18 @@ __device__ __forceinline__ int64_t modulation_row(const NormArgs& a, int64_t t) 
   return i < 0 ? 0 : (i >= a.mod_rows ? a.mod_rows - 1 : i);
 }
 
-// Rows of whole 16-byte chunks: one work-group per row, the row in registers
-// (V chunks of eight values a thread).  y and h are read once, h' and u
+// One work-group per row, the row in registers (V chunks of eight values a
+// thread).  y and h are read once, h' and u
 // written once; the statistics are one or two reductions each (a LayerNorm's
 // centred sum of squares follows its mean, so that it cannot cancel).
-template <int V, bool HB>
+template <int V, bool HB, bool WHOLE>
 __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
   __shared__ float sh[4][16];
   __shared__ uint32_t sh_top[16];
   const int n = static_cast<int>(a.n);
   const float inv_n = 1.f / static_cast<float>(n);
   const int pb = a.param_type == SIGNROT_BF16;
-  const int chunks = n >> 3, step = blockDim.x;
+  const int chunks = (n + 7) >> 3, step = blockDim.x;
   const int tid = threadIdx.x;
 
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
@@ -48,11 +48,11 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < (HB ? 1 : 2); ++i) hw[v][i] = row::u32x4_t{0, 0, 0, 0};
       if (c < chunks) {
-        if (a.y) yw[v] = reinterpret_cast<const row::u32x4_t*>(static_cast<const uint16_t*>(a.y) + t * a.ldy)[c];
-        const uint8_t* hr = static_cast<const uint8_t*>(a.h) + t * a.ldh * (HB ? 2 : 4);
+        const int at = row::Chunk<WHOLE>(c, n).at;
+        if (a.y) yw[v] = row::load_as<WHOLE, row::u32x4_t>(static_cast<const uint16_t*>(a.y) + t * a.ldy + at);
+        const uint8_t* const hr = static_cast<const uint8_t*>(a.h) + (t * a.ldh + at) * (HB ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < (HB ? 1 : 2); ++i)
-          hw[v][i] = reinterpret_cast<const row::u32x4_t*>(hr)[(HB ? 1 : 2) * c + i];
+        for (int i = 0; i < (HB ? 1 : 2); ++i) hw[v][i] = row::load_as<WHOLE, row::u32x4_t>(hr + 16 * i);
       }
     }
     // mean and 1 / sqrt(var + eps) of the row whose chunk v is get(v)
@@ -66,20 +66,23 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
         for (int v = 0; v < V; ++v) {
           float x[8];
           get(v, x);
+          const row::Chunk<WHOLE> k(tid + v * step, n);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s += x[e];
+          for (int e = 0; e < 8; ++e) s += WHOLE || k.own(e) ? x[e] : 0.f;
         }
         mean = row::block_reduce(s, sh1) * inv_n;
       }
       float q = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (tid + v * step >= chunks) continue;
+        const int c = tid + v * step;
+        if (c >= chunks) continue;
         float x[8];
         get(v, x);
+        const row::Chunk<WHOLE> k(c, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float d = x[e] - mean;
+          const float d = WHOLE || k.own(e) ? x[e] - mean : 0.f;
           q = fmaf(d, d, q);
         }
       }
@@ -92,12 +95,12 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = (x[e] - mean) * inv;
       if (w) {
-        row::load8(w, j, pb, p);
+        row::load8<WHOLE>(w, j, pb, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= p[e];
       }
       if (b) {
-        row::load8(b, j, pb, p);
+        row::load8<WHOLE>(b, j, pb, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += p[e];
       }
@@ -116,15 +119,16 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
         for (int e = 0; e < 8; ++e) h[v][e] = __uint_as_float(hw[v][HB ? 0 : e >> 2][e & 3]);
       }
       if (c >= chunks) continue;
+      const row::Chunk<WHOLE> k(c, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[v][e] *= a.beta;
       if (a.y) {
         float y[8];
         row::widen_bf16(yw[v], y);
-        affine(y, a.post_norm, mean, inv, a.post_weight, a.post_bias, 8 * c);
+        affine(y, a.post_norm, mean, inv, a.post_weight, a.post_bias, k.at);
         if (a.gate) {
           float p[8];
-          row::load8(a.gate, gate_at + 8 * c, pb, p);
+          row::load8<WHOLE>(a.gate, gate_at + k.at, pb, p);
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] *= p[e];
         }
@@ -132,15 +136,24 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
         for (int e = 0; e < 8; ++e) h[v][e] = fmaf(a.alpha, y[e], h[v][e]);
       }
       if (a.h_out) {
-        if (HB) {
+        uint8_t* const out = static_cast<uint8_t*>(a.h_out) + (t * a.ldho + k.at) * (HB ? 2 : 4);
+        if (!WHOLE && k.dup > 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k.own(e)) row::store_elem(out, e, h[v][e], HB);
+        } else if (HB) {
           row::u32x4_t w;
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = row::pack_bf16(h[v][2 * e], h[v][2 * e + 1]);
-          *reinterpret_cast<row::u32x4_t*>(static_cast<uint16_t*>(a.h_out) + t * a.ldho + 8 * c) = w;
+          row::store_as<WHOLE>(out, w);
         } else {
-          float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.h_out) + t * a.ldho + 8 * c);
-          p[0] = make_float4(h[v][0], h[v][1], h[v][2], h[v][3]);
-          p[1] = make_float4(h[v][4], h[v][5], h[v][6], h[v][7]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            row::u32x4_t w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(h[v][4 * i + e]);
+            row::store_as<WHOLE>(out + 16 * i, w);
+          }
         }
       }
     }
@@ -156,25 +169,34 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
       for (int v = 0; v < V; ++v) {
         const int c = tid + v * step;
         if (c >= chunks) continue;
-        affine(h[v], a.pre_norm, mean, inv, a.pre_weight, a.pre_bias, 8 * c);
+        const row::Chunk<WHOLE> k(c, n);
+        affine(h[v], a.pre_norm, mean, inv, a.pre_weight, a.pre_bias, k.at);
         float p[8];
         if (a.mod_scale) {
-          row::load8(a.mod_scale, mod_at + 8 * c, pb, p);
+          row::load8<WHOLE>(a.mod_scale, mod_at + k.at, pb, p);
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[v][e] *= 1.f + p[e];
         }
         if (a.mod_shift) {
-          row::load8(a.mod_shift, mod_at + 8 * c, pb, p);
+          row::load8<WHOLE>(a.mod_shift, mod_at + k.at, pb, p);
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[v][e] += p[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = row::join(top, row::abs_bits(h[v][e]));
+        for (int e = 0; e < 8; ++e)
+          if (WHOLE || k.own(e)) top = row::join(top, row::abs_bits(h[v][e]));
         if (a.u) {
-          row::u32x4_t w;
+          uint16_t* const out = static_cast<uint16_t*>(a.u) + t * a.ldu + k.at;
+          if (!WHOLE && k.dup > 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = row::pack_bf16(h[v][2 * e], h[v][2 * e + 1]);
-          *reinterpret_cast<row::u32x4_t*>(static_cast<uint16_t*>(a.u) + t * a.ldu + 8 * c) = w;
+            for (int e = 0; e < 8; ++e)
+              if (k.own(e)) out[e] = row::f32_bf16(h[v][e]);
+          } else {
+            row::u32x4_t w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = row::pack_bf16(h[v][2 * e], h[v][2 * e + 1]);
+            row::store_as<WHOLE>(out, w);
+          }
         }
       }
       if (a.codes) {
@@ -190,7 +212,15 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
           for (int e = 0; e < 2; ++e)
             q[e] = row::pack_codes(code.bits(h[v][4 * e]), code.bits(h[v][4 * e + 1]), code.bits(h[v][4 * e + 2]),
                                    code.bits(h[v][4 * e + 3]));
-          *reinterpret_cast<row::u32x2_t*>(a.codes + t * a.ldc + 8 * c) = q;
+          const row::Chunk<WHOLE> k(c, n);
+          int8_t* const out = a.codes + t * a.ldc + k.at;
+          if (!WHOLE && k.dup > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (k.own(e)) out[e] = static_cast<int8_t>(q[e >> 2] >> (8 * (e & 3)));
+          } else {
+            row::store_as<WHOLE>(out, q);
+          }
         }
       }
     }
@@ -198,9 +228,9 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
   }
 }
 
-// Any width, stride and alignment: one work-group per row, every pass
-// recomputes the row's values from memory (the row is in cache after the
-// first).  Thread i owns the elements i, i + 256, ... in every pass, so h_out
+// Rows of fewer than eight values or more than 32768: one work-group per row,
+// every pass recomputes the row's values from memory (the row is in cache after
+// the first).  Thread i owns the elements i, i + 256, ... in every pass, so h_out
 // may be h.
 constexpr int kAnyThreads = 256;
 __global__ __launch_bounds__(kAnyThreads) void residual_norm_any_kernel(NormArgs a) {
@@ -298,30 +328,36 @@ bool aligned_rows(const NormArgs& a) {
   return a.n % 8 == 0 && (at & 15u) == 0 && (ld & 15) == 0 && codes;
 }
 
-template <int V>
-void run_rows(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
+template <int V, bool WHOLE>
+void run_rows_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
   if (a.h_type == SIGNROT_BF16)
-    residual_norm_rows_kernel<V, true><<<grid, block, 0, s>>>(a);
+    residual_norm_rows_kernel<V, true, WHOLE><<<grid, block, 0, s>>>(a);
   else
-    residual_norm_rows_kernel<V, false><<<grid, block, 0, s>>>(a);
+    residual_norm_rows_kernel<V, false, WHOLE><<<grid, block, 0, s>>>(a);
+}
+
+template <bool WHOLE>
+void run_rows(const NormArgs& a, dim3 grid, hipStream_t s) {
+  const int chunks = static_cast<int>((a.n + 7) / 8);
+  const int v = row::chunks_per_thread(chunks, a.tokens);
+  const dim3 block(static_cast<unsigned>(row::threads_for(chunks, v)));
+  switch (v) {
+    case 1: run_rows_as<1, WHOLE>(a, grid, block, s); break;
+    case 2: run_rows_as<2, WHOLE>(a, grid, block, s); break;
+    default: run_rows_as<4, WHOLE>(a, grid, block, s); break;
+  }
 }
 
 }  // namespace
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.tokens < row::kMaxBlocks ? a.tokens : row::kMaxBlocks));
-  const int chunks = static_cast<int>(a.n / 8);
-  if (!aligned_rows(a) || chunks > 4 * 1024) {
+  if (a.n < 8 || a.n > 4 * 8 * 1024)
     residual_norm_any_kernel<<<grid, dim3(kAnyThreads), 0, s>>>(a);
-    return hipGetLastError();
-  }
-  const int v = row::chunks_per_thread(chunks, a.tokens);
-  const dim3 block(static_cast<unsigned>(row::threads_for(chunks, v)));
-  switch (v) {
-    case 1: run_rows<1>(a, grid, block, s); break;
-    case 2: run_rows<2>(a, grid, block, s); break;
-    default: run_rows<4>(a, grid, block, s); break;
-  }
+  else if (aligned_rows(a))
+    run_rows<true>(a, grid, s);
+  else
+    run_rows<false>(a, grid, s);
   return hipGetLastError();
 }
 

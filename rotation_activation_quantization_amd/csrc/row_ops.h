@@ -43,16 +43,51 @@ __device__ __forceinline__ void widen_bf16(const u32x4_t& w, float (&v)[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-// Eight consecutive elements from j on (16-byte aligned).
+// Sixteen or eight bytes at an aligned address, or at any (the hardware takes
+// those; the compiler has to be told).
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ T load_as(const void* p) {
+  if (ALIGNED) return *static_cast<const T*>(p);
+  T v;
+  __builtin_memcpy(&v, p, sizeof(T));
+  return v;
+}
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ void store_as(void* p, const T& v) {
+  if (ALIGNED)
+    *static_cast<T*>(p) = v;
+  else
+    __builtin_memcpy(p, &v, sizeof(T));
+}
+
+// Eight consecutive elements from j on.
+template <bool ALIGNED>
 __device__ __forceinline__ void load8(const void* p, int64_t j, int bf16, float (&v)[8]) {
   if (bf16) {
-    widen_bf16(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + j), v);
+    widen_bf16(load_as<ALIGNED, u32x4_t>(static_cast<const uint16_t*>(p) + j), v);
   } else {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + j);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4_t w = load_as<ALIGNED, u32x4_t>(static_cast<const float*>(p) + j + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * i + e] = __uint_as_float(w[e]);
+    }
   }
 }
+
+// The rows kernels hold a row as chunks of eight elements.  Rows of whole,
+// aligned chunks (WHOLE) are read and written as vectors.  In other rows (n >= 8)
+// the vectors lie at any address, and the last chunk is moved back to the row's
+// last eight elements: the first `dup` of them belong to the chunk before, are
+// left out of every sum and maximum, and are not stored again (the other
+// thread may have stored them already, over an input that is the output).
+template <bool WHOLE>
+struct Chunk {
+  int at;   // first element
+  int dup;  // elements of the chunk before
+  __device__ __forceinline__ Chunk(int c, int n) : at(WHOLE ? 8 * c : min(8 * c, n - 8)), dup(8 * c - at) {}
+  __device__ __forceinline__ bool own(int e) const { return WHOLE || e >= dup; }
+};
 
 // |x| as ordered bits: for finite values the order of the magnitudes, with
 // infinity above them and NaN above infinity, so a maximum over a row keeps
