@@ -377,8 +377,8 @@ int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld
  * 1 <= n <= 131071 (an int32 sum cannot overflow); any alignment and stride
  * of codes, w and out.  Rows that are not 16-byte aligned with n a multiple of
  * 16 (32 of packed INT4 codes) cost more; large ones are laid out anew in the
- * workspace first.  tokens == 0 or rows == 0 is a no-op.  Negative or
- * over-large sizes (>= 2^31), a leading dimension below its row, an unknown
+ * workspace first.  tokens == 0 or rows == 0 is a no-op.  Negative
+ * sizes, tokens or rows >= 2^30, a leading dimension below its row, an unknown
  * out_type, a workspace that is too small or a null pointer ->
  * SIGNROT_EINVAL.  No allocation.  Asynchronous.
  */

@@ -643,8 +643,8 @@ int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld
 namespace {
 // Sizes of the 8-bit products, shared by the calls and their host-only helpers.
 int w8_sizes(int64_t tokens, int64_t n, int64_t rows, bool a4) {
-  if (tokens < 0 || rows < 0 || tokens >= (int64_t{1} << 31) || rows >= (int64_t{1} << 31))
-    return fail_einval("tokens and rows must be in [0, 2^31)");
+  if (tokens < 0 || rows < 0 || tokens >= (int64_t{1} << 30) || rows >= (int64_t{1} << 30))
+    return fail_einval("tokens and rows must be in [0, 2^30)");  // the kernels round them up to tiles in int
   if (n < 1 || n > kW8MaxN) return fail_einval("n must be in [1, 131071]");
   if (a4 && (n & 1)) return fail_einval("n must be even");
   return SIGNROT_OK;

@@ -34,8 +34,7 @@ __device__ __forceinline__ void widen8(uint32_t c, uint32_t& r0, uint32_t& r1) {
 __device__ __forceinline__ float finish(const W8Args& a, int t, int k, int32_t acc) {
   float v = static_cast<float>(acc);
   if (a.a4) v = fmaf(-a.zero[t], static_cast<float>(a.w_sum[k]), v);
-  v = v * a.scale[t] * a.w_scale[k];
-  return a.bias ? v + a.bias[k] : v;
+  return fmaf(v * a.scale[t], a.w_scale[k], a.bias ? a.bias[k] : 0.f);
 }
 
 // ---- large tiles ------------------------------------------------------------
@@ -80,6 +79,16 @@ struct Tile {
   static_assert(kWBlocks * 1024 == kWDeep && kTBlocks * 1024 == kTDeep, "whole loads");
   static_assert(FK % 4 == 0, "a lane's channels come in sixteens");
   static_assert(KU == 1 || KU % 2 == 0, "the token operands alternate");
+  // The factors of a tile's results are there before its stores, since a load
+  // after a store waits for the store: in registers where those are free (512 x
+  // 4096 x 4096: 12.8 us, 13.9 loaded between the stores), else (64 x 128
+  // results a wave, where registers would spill: 421 us at 8192 x 4096 x 14336)
+  // in LDS, loaded with the tile's first step (395; 404 between the stores).
+  // Two copies, since waves enter the next tile on their own.
+  static constexpr bool kFactorsInLds = FK * FT >= 32;
+  static constexpr int kFactors = kFactorsInLds ? 3 * kBN + 2 * kBM : 0;  // w_scale, scale, w_sum, zero, bias
+  static_assert(!kFactorsInLds || (kBN == 256 && kBM == 256 && kWaves == 8 && kLds + 8 * kFactors <= 160 * 1024),
+                "a wave loads 64 channels or 64 tokens");
   static_assert(S >= 4 && kFit > 0, "ring");
 };
 
@@ -113,9 +122,10 @@ struct Tile {
 template <bool A4, int WK, int WT, int FK, int FT, int KU, int S, bool SPLIT>
 __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_n, int splits) {
   using C = Tile<A4, WK, WT, FK, FT, KU, S>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + (SPLIT ? 0 : 8 * C::kFactors)];
   uint8_t* const lds_w = lds;
   uint8_t* const lds_t = lds + S * C::kWStage;
+  float* const factors = reinterpret_cast<float*>(lds + C::kLds);
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wid % WK, wt = wid / WK;
@@ -331,7 +341,27 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
   };
 
   const bool wide = (a.ldo % 8 == 0) && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  int copy = 0;
   for (; p < end; p += stride) {
+    int tm, tn;
+    tile_at(SPLIT ? p % tiles : p, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+    if (C::kFactorsInLds && !SPLIT) {
+      // Landed after the tile's first step: its wait leaves only later loads,
+      // and its barrier comes after every wave's.
+      copy ^= 1;
+      const bool ch = wid < 4;
+      const int rows = ch ? min(C::kBN, a.R - n0) : min(C::kBM, a.T - m0);
+      const uint32_t at = 4 * min(64 * (wid & 3) + lane, rows - 1);
+      auto fill = [&](const void* src, int to) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wave::buffer_rsrc(static_cast<const uint32_t*>(src) + (ch ? n0 : m0), 4 * static_cast<uint32_t>(rows)),
+            (__attribute__((address_space(3))) void*)(factors + copy * C::kFactors + to + 64 * wid), 4, at, 0, 0, 0);
+      };
+      fill(ch ? static_cast<const void*>(a.w_scale) : static_cast<const void*>(a.scale), 0);
+      if (A4) fill(ch ? static_cast<const void*>(a.w_sum) : static_cast<const void*>(a.zero), C::kBN + C::kBM);
+      if (a.bias && ch) fill(a.bias, 2 * (C::kBN + C::kBM));
+    }
 #pragma unroll
     for (int f = 0; f < FK; ++f)
 #pragma unroll
@@ -368,10 +398,18 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
       continue;
     }
 
-    // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.
-    int tm, tn;
-    tile_at(p, tiles_m, tiles_n, tm, tn);
-    const int m0 = tm * C::kBM, n0 = tn * C::kBN;
+    // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.  The
+    // factors come before the stores: a load after a store waits for the store.
+    const float* const fac = factors + copy * C::kFactors;
+    float sc[FT], z[FT];
+    if (!C::kFactorsInLds) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int t = min(m0 + 16 * (wt * FT + j) + i, a.T - 1);
+        sc[j] = a.scale[t];
+        z[j] = A4 ? a.zero[t] : 0.f;
+      }
+    }
 #pragma unroll
     for (int q = 0; q < FK / 4; ++q) {
       const int k0 = n0 + 16 * wk * FK + 64 * q + 16 * g;
@@ -380,26 +418,30 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
       float v[16], b[16], ws[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int k = min(k0 + e, a.R - 1);
-        v[e] = a.w_scale[k];
-        ws[e] = A4 ? static_cast<float>(a.w_sum[k]) : 0.f;
+        const int k = C::kFactorsInLds ? k0 - n0 + e : min(k0 + e, a.R - 1);
+        v[e] = C::kFactorsInLds ? fac[k] : a.w_scale[k];
+        ws[e] = 0.f;
+        if (A4)
+          ws[e] = static_cast<float>(C::kFactorsInLds ? __float_as_int(fac[C::kBN + C::kBM + k]) : a.w_sum[k]);
         b[e] = 0.f;
       }
       if (a.bias) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) b[e] = a.bias[min(k0 + e, a.R - 1)];
+        for (int e = 0; e < 16; ++e)
+          b[e] = C::kFactorsInLds ? fac[2 * (C::kBN + C::kBM) + k0 - n0 + e] : a.bias[min(k0 + e, a.R - 1)];
       }
 #pragma unroll
       for (int j = 0; j < FT; ++j) {
         const int t = m0 + 16 * (wt * FT + j) + i;
         if (t >= a.T) continue;
-        const float sc = a.scale[t], z = A4 ? a.zero[t] : 0.f;
+        const float scale = C::kFactorsInLds ? fac[C::kBN + t - m0] : sc[j];
+        const float zero = !A4 ? 0.f : C::kFactorsInLds ? fac[2 * C::kBN + C::kBM + t - m0] : z[j];
         float o[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float x = static_cast<float>(acc[4 * q + (e >> 2)][j][e & 3]);
-          if (A4) x = fmaf(-z, ws[e], x);
-          o[e] = fmaf(x * sc, v[e], b[e]);
+          if (A4) x = fmaf(-zero, ws[e], x);
+          o[e] = fmaf(x * scale, v[e], b[e]);
         }
         const int64_t at = static_cast<int64_t>(t) * a.ldo + k0;
         if (whole && a.out_bf16) {
@@ -753,57 +795,73 @@ bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24)
 // LDS.
 
 // The 16 operand bytes (8 of packed codes) from channel j0 on of a row with n
-// channels, in two halves so that loads stay in flight: the load, at any
-// alignment, moved back where it would pass the row's end, and the shift that
-// undoes the move and leaves zeros beyond n.  Rows shorter than a chunk are
-// read byte by byte.
-template <bool A4>
-__device__ __forceinline__ i32x4_t any_load(const uint8_t* p, int j0, int n) {
-  constexpr int kBytes = A4 ? 8 : 16;
-  const int bytes = A4 ? n / 2 : n;
-  i32x4_t w = {0, 0, 0, 0};
-  if (bytes >= kBytes) {  // the same for all lanes
-    memcpy(&w, p + min(A4 ? j0 / 2 : j0, bytes - kBytes), kBytes);
-  } else if (j0 == 0) {
-    uint32_t b[4] = {0, 0, 0, 0};
+// channels, in two halves so that loads stay in flight: the dwords that hold
+// them, moved back where they would pass the row's end, and the shifts that
+// take the bytes out and leave zeros beyond n.  (A load at an odd address costs
+// several times an aligned one: 1 x 14338 x 4096 took 27 us with those, 17.6
+// us so.)  No
+// dword without a byte of the row is read.  TINY: rows shorter than a chunk, byte by byte.
+template <bool A4, bool TINY>
+struct AnyChunk {
+  static constexpr int kBytes = A4 ? 8 : 16, kWords = kBytes / 4;
+  uint32_t d[kWords + 1];
+
+  static __device__ __forceinline__ int offset(int j0, int n) {
+    return min(A4 ? j0 / 2 : j0, max((A4 ? n / 2 : n) - kBytes, 0));
+  }
+  __device__ __forceinline__ void load(const uint8_t* p, int j0, int n) {
+    if (TINY) {
 #pragma unroll
-    for (int i = 0; i < kBytes; ++i)
-      if (i < bytes) b[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-    w = i32x4_t{static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+      for (int i = 0; i <= kWords; ++i) d[i] = 0;
+      if (j0 == 0) {
+#pragma unroll
+        for (int i = 0; i < kBytes; ++i)
+          if (i < (A4 ? n / 2 : n)) d[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+      }
+      return;
+    }
+    p += offset(j0, n);
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint32_t* const q = reinterpret_cast<const uint32_t*>(p - odd);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) d[i] = q[i];
+    d[kWords] = q[odd ? kWords : kWords - 1];
   }
-  return w;
-}
-template <bool A4>
-__device__ __forceinline__ i32x4_t any_shift(const i32x4_t& w, int j0, int n) {
-  constexpr int kBytes = A4 ? 8 : 16;
-  const int bytes = A4 ? n / 2 : n;
-  const int by = max((A4 ? j0 / 2 : j0) - max(bytes - kBytes, 0), 0);  // bytes moved back
-  uint64_t lo = static_cast<uint32_t>(w[0]) | static_cast<uint64_t>(static_cast<uint32_t>(w[1])) << 32;
-  uint64_t hi = static_cast<uint32_t>(w[2]) | static_cast<uint64_t>(static_cast<uint32_t>(w[3])) << 32;
-  if (by >= 16) {
-    lo = hi = 0;
-  } else if (by >= 8) {
-    lo = hi >> (8 * (by - 8));
-    hi = 0;
-  } else if (by > 0) {
-    lo = lo >> (8 * by) | hi << (64 - 8 * by);
-    hi >>= 8 * by;
+  // The operand; `cut`: the chunk may pass the row's end.  Packed codes are widened.
+  __device__ __forceinline__ i32x4_t take(const uint8_t* p, int j0, int n, bool cut) const {
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint32_t odd = TINY ? 0 : (reinterpret_cast<uintptr_t>(p) + offset(j0, n)) & 3u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __builtin_amdgcn_alignbyte(d[i + 1], d[i], odd);
+    if (cut && !TINY) {
+      const int by = (A4 ? j0 / 2 : j0) - offset(j0, n);  // bytes moved back
+      uint64_t lo = w[0] | static_cast<uint64_t>(w[1]) << 32, hi = w[2] | static_cast<uint64_t>(w[3]) << 32;
+      if (by >= 16) {
+        lo = hi = 0;
+      } else if (by >= 8) {
+        lo = hi >> (8 * (by - 8));
+        hi = 0;
+      } else if (by > 0) {
+        lo = lo >> (8 * by) | hi << (64 - 8 * by);
+        hi >>= 8 * by;
+      }
+      w[0] = static_cast<uint32_t>(lo);
+      w[1] = static_cast<uint32_t>(lo >> 32);
+      w[2] = static_cast<uint32_t>(hi);
+      w[3] = static_cast<uint32_t>(hi >> 32);
+    }
+    if (A4) {
+      const uint32_t c0 = w[0], c1 = w[1];
+      widen8(c0, w[0], w[1]);
+      widen8(c1, w[2], w[3]);
+    }
+    return i32x4_t{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
   }
-  return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi), static_cast<int>(hi >> 32)};
-}
-template <bool A4>
-__device__ __forceinline__ i32x4_t any_operand(const i32x4_t& c) {
-  if (!A4) return c;
-  uint32_t b[4];
-  widen8(static_cast<uint32_t>(c[0]), b[0], b[1]);
-  widen8(static_cast<uint32_t>(c[1]), b[2], b[3]);
-  return i32x4_t{static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
-}
+};
 
 // Tile of WK x WT waves of FK x FT 16 x 16 results, steps of KU * 64 k.  Step s
 // multiplies from one LDS buffer while the registers with step s + 1 are written
-// to the other and filled with step s + 2 (three sets, for deeper loads, were no
-// faster).
+// to the other and filled with step s + 2 (three sets of registers were slower).
 // LDS as in w8_tile: for each depth rows of 64 bytes, chunk c of row r at chunk
 // c ^ 2 ((r >> 3) & 1).
 template <bool A4, int WK, int WT, int FK, int FT, int KU>
@@ -816,7 +874,35 @@ struct AnyTile {
   static_assert(kWPer * kThreads == kWSlots && kTPer * kThreads == kTSlots, "whole chunks per thread");
 };
 
-template <bool A4, int WK, int WT, int FK, int FT, int KU>
+// The factors of a lane's results: channels k + 16 f + e (e < 4), tokens t + 16 j.
+template <bool A4, int FK, int FT>
+struct Factors {
+  float v[FK][4], ws[FK][4], b[FK][4], sc[FT], z[FT];
+  __device__ __forceinline__ Factors(const W8Args& a, int k, int t) {
+#pragma unroll
+    for (int f = 0; f < FK; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = min(k + 16 * f + e, a.R - 1);
+        v[f][e] = a.w_scale[c];
+        ws[f][e] = A4 ? static_cast<float>(a.w_sum[c]) : 0.f;
+        b[f][e] = a.bias ? a.bias[c] : 0.f;
+      }
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      const int c = min(t + 16 * j, a.T - 1);
+      sc[j] = a.scale[c];
+      z[j] = A4 ? a.zero[c] : 0.f;
+    }
+  }
+  __device__ __forceinline__ float finish(int f, int e, int j, int32_t acc) const {
+    float x = static_cast<float>(acc);
+    if (A4) x = fmaf(-z[j], ws[f][e], x);
+    return fmaf(x * sc[j], v[f][e], b[f][e]);
+  }
+};
+
+template <bool A4, int WK, int WT, int FK, int FT, int KU, bool TINY>
 __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
   using C = AnyTile<A4, WK, WT, FK, FT, KU>;
   __shared__ i32x4_t lds[2][C::kWSlots + C::kTSlots];
@@ -847,24 +933,23 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
     kt[x] = 16 * c;
     st[x] = C::kWSlots + slot(r, c, C::kBM);
   }
-  i32x4_t vw[C::kWPer], vt[C::kTPer];
+  AnyChunk<false, TINY> vw[C::kWPer];
+  AnyChunk<A4, TINY> vt[C::kTPer];
+  // step 0 is the row's last, possibly short one
+  auto start = [&](int s) { return C::kStep * (s == 0 ? steps - 1 : s - 1); };
   auto load = [&](int s) {
+    const int k0 = start(s);
 #pragma unroll
-    for (int x = 0; x < C::kWPer; ++x) vw[x] = any_load<false>(pw[x], C::kStep * s + kw[x], a.n);
+    for (int x = 0; x < C::kWPer; ++x) vw[x].load(pw[x], k0 + kw[x], a.n);
 #pragma unroll
-    for (int x = 0; x < C::kTPer; ++x) vt[x] = any_load<A4>(pt[x], C::kStep * s + kt[x], a.n);
+    for (int x = 0; x < C::kTPer; ++x) vt[x].load(pt[x], k0 + kt[x], a.n);
   };
-  auto store = [&](int s) {
-    if (s == steps - 1) {
+  auto store = [&](int s, bool cut) {
+    const int k0 = start(s);
 #pragma unroll
-      for (int x = 0; x < C::kWPer; ++x) vw[x] = any_shift<false>(vw[x], C::kStep * s + kw[x], a.n);
+    for (int x = 0; x < C::kWPer; ++x) lds[s & 1][sw[x]] = vw[x].take(pw[x], k0 + kw[x], a.n, cut);
 #pragma unroll
-      for (int x = 0; x < C::kTPer; ++x) vt[x] = any_shift<A4>(vt[x], C::kStep * s + kt[x], a.n);
-    }
-#pragma unroll
-    for (int x = 0; x < C::kWPer; ++x) lds[s & 1][sw[x]] = vw[x];
-#pragma unroll
-    for (int x = 0; x < C::kTPer; ++x) lds[s & 1][st[x]] = any_operand<A4>(vt[x]);
+    for (int x = 0; x < C::kTPer; ++x) lds[s & 1][st[x]] = vt[x].take(pt[x], k0 + kt[x], a.n, cut);
   };
   i32x4_t acc[FK][FT];
 #pragma unroll
@@ -873,8 +958,8 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
     for (int j = 0; j < FT; ++j) acc[f][j] = i32x4_t{0, 0, 0, 0};
 
   load(0);
-  store(0);
-  if (steps > 1) load(1);
+  store(0, true);
+  load(min(1, steps - 1));
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
     const int buf = s & 1;
@@ -886,10 +971,8 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
 #pragma unroll
       for (int j = 0; j < FT; ++j) ft[u][j] = lds[buf][C::kWSlots + (u * C::kBM + 16 * (wt * FT + j)) * 4 + at];
     }
-    if (s + 1 < steps) {
-      store(s + 1);
-      if (s + 2 < steps) load(s + 2);
-    }
+    if (s + 1 < steps) store(s + 1, false);
+    load(min(s + 2, steps - 1));
 #pragma unroll
     for (int u = 0; u < KU; ++u)
 #pragma unroll
@@ -899,6 +982,8 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
           acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][f], ft[u][j], acc[f][j], 0, 0, 0);
     __syncthreads();
   }
+  // All factors first: a load after a store waits for the store.
+  Factors<A4, FK, FT> fac(a, n0 + 16 * wk * FK + 4 * (lane >> 4), m0 + 16 * wt * FT + (lane & 15));
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int t = m0 + 16 * (wt * FT + j) + (lane & 15);
@@ -909,7 +994,7 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
       for (int e = 0; e < 4; ++e) {
         const int k = n0 + 16 * (wk * FK + f) + 4 * (lane >> 4) + e;
         if (k < a.R)
-          row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, finish(a, t, k, acc[f][j][e]), a.out_bf16);
+          row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, fac.finish(f, e, j, acc[f][j][e]), a.out_bf16);
       }
   }
 }
@@ -920,14 +1005,17 @@ template <bool A4>
 hipError_t run_any(const W8Args& a, hipStream_t s) {
   using C = AnyTile<A4, 2, 2, 2, 2, 2>;
   const int tiles = ((a.T + C::kBM - 1) / C::kBM) * ((a.R + C::kBN - 1) / C::kBN);
-  w8_any_kernel<A4, 2, 2, 2, 2, 2>
-      <<<dim3(static_cast<unsigned>(tiles)), dim3(static_cast<unsigned>(C::kThreads)), 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>(tiles)), block(static_cast<unsigned>(C::kThreads));
+  if (a.n < 16)
+    w8_any_kernel<A4, 2, 2, 2, 2, 2, true><<<grid, block, 0, s>>>(a);
+  else
+    w8_any_kernel<A4, 2, 2, 2, 2, 2, false><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
 // Few tokens: as w8_few, with both operands straight to registers, a lane (g, i)
 // reading 16 bytes (g) of row i for each 64 k.
-template <bool A4, int FT>
+template <bool A4, int FT, bool TINY>
 __global__ __launch_bounds__(1024) void w8_few_any_kernel(W8Args a) {
   extern __shared__ __attribute__((aligned(16))) int32_t few_part[];  // [wave][FT][64][4]
   const int lane = threadIdx.x & 63;
@@ -943,23 +1031,23 @@ __global__ __launch_bounds__(1024) void w8_few_any_kernel(W8Args a) {
   i32x4_t acc[FT];
 #pragma unroll
   for (int j = 0; j < FT; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
-  auto unit = [&](int k0, bool last) {
-    i32x4_t w[2], tok[2][FT];
+  auto unit = [&](int k0, bool cut) {
+    AnyChunk<false, TINY> w[2];
+    AnyChunk<A4, TINY> tok[2][FT];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int k = k0 + 64 * s + 16 * g;
-      w[s] = any_load<false>(pw, k, a.n);
+      w[s].load(pw, k, a.n);
 #pragma unroll
-      for (int j = 0; j < FT; ++j) tok[s][j] = any_load<A4>(pt[j], k, a.n);
+      for (int j = 0; j < FT; ++j) tok[s][j].load(pt[j], k, a.n);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      if (last) w[s] = any_shift<false>(w[s], k0 + 64 * s + 16 * g, a.n);
+      const int k = k0 + 64 * s + 16 * g;
+      const i32x4_t ws = w[s].take(pw, k, a.n, cut);
 #pragma unroll
-      for (int j = 0; j < FT; ++j) {
-        if (last) tok[s][j] = any_shift<A4>(tok[s][j], k0 + 64 * s + 16 * g, a.n);
-        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], any_operand<A4>(tok[s][j]), acc[j], 0, 0, 0);
-      }
+      for (int j = 0; j < FT; ++j)
+        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ws, tok[s][j].take(pt[j], k, a.n, cut), acc[j], 0, 0, 0);
     }
   };
   int k0 = kUnit * wid;
@@ -978,10 +1066,17 @@ hipError_t run_few_any(const W8Args& a, hipStream_t s) {
   int waves = 16;
   while (waves > 4 && (groups * waves > 32 * kCus || (a.n + kUnit - 1) / kUnit < waves)) waves /= 2;
   const dim3 grid(static_cast<unsigned>(groups)), block(static_cast<unsigned>(64 * waves));
-  if (a.T <= 16)
-    w8_few_any_kernel<A4, 1><<<grid, block, static_cast<unsigned>(1024 * waves), s>>>(a);
-  else
-    w8_few_any_kernel<A4, 2><<<grid, block, static_cast<unsigned>(2048 * waves), s>>>(a);
+  const unsigned lds = static_cast<unsigned>(1024 * waves);
+  if (a.n < 16) {
+    if (a.T <= 16)
+      w8_few_any_kernel<A4, 1, true><<<grid, block, lds, s>>>(a);
+    else
+      w8_few_any_kernel<A4, 2, true><<<grid, block, 2 * lds, s>>>(a);
+  } else if (a.T <= 16) {
+    w8_few_any_kernel<A4, 1, false><<<grid, block, lds, s>>>(a);
+  } else {
+    w8_few_any_kernel<A4, 2, false><<<grid, block, 2 * lds, s>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -1002,9 +1097,9 @@ __global__ __launch_bounds__(256) void w8_pack_kernel(PackArgs a) {
     const uint8_t* const src = a.src[x] + r * a.ld[x];
     i32x4_t* const dst = reinterpret_cast<i32x4_t*>(a.dst[x]) + r * a.chunks[x];
     for (int c = threadIdx.x; c < a.chunks[x]; c += blockDim.x) {
-      i32x4_t v = any_load<false>(src, 16 * c, a.bytes[x]);
-      if (16 * c + 16 > a.bytes[x]) v = any_shift<false>(v, 16 * c, a.bytes[x]);
-      dst[c] = v;
+      AnyChunk<false, false> v;
+      v.load(src, 16 * c, a.bytes[x]);
+      dst[c] = v.take(src, 16 * c, a.bytes[x], 16 * c + 16 > a.bytes[x]);
     }
   }
 }
@@ -1069,7 +1164,7 @@ Way way_of(const W8Args& a) {
   const double per_cu = ceil(tiles / kCus), deep = a.n / 128.0;
   const double any =
       floor(per_cu / 2) * (deep * kAnyTwo + 1.5) + fmod(per_cu, 2) * (deep * kAnyOne + 1.5);
-  if (any < p.us && tiles < (1 << 22)) return {Way::kAny, {0, 1, any}};
+  if ((any < p.us && tiles < (1 << 22)) || a.n < 16) return {Way::kAny, {0, 1, any}};
   return {Way::kPackTiles, p};
 }
 
