@@ -447,8 +447,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
         if (whole && a.out_bf16) {
           uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            h[e] = row::f32_bf16(o[2 * e]) | static_cast<uint32_t>(row::f32_bf16(o[2 * e + 1])) << 16;
+          for (int e = 0; e < 8; ++e) h[e] = row::pack_bf16(o[2 * e], o[2 * e + 1]);
           wave::u32x4_t* out = reinterpret_cast<wave::u32x4_t*>(static_cast<uint16_t*>(a.out) + at);
           out[0] = wave::u32x4_t{h[0], h[1], h[2], h[3]};
           out[1] = wave::u32x4_t{h[4], h[5], h[6], h[7]};

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
         if (a.mod_scale) {
           row::load8<WHOLE>(a.mod_scale, mod_at + k.at, pb, p);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[v][e] *= 1.f + p[e];
+          for (int e = 0; e < 8; ++e) h[v][e] = fmaf(h[v][e], p[e], h[v][e]);
         }
         if (a.mod_shift) {
           row::load8<WHOLE>(a.mod_shift, mod_at + k.at, pb, p);

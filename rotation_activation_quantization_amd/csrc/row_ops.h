@@ -21,7 +21,9 @@ __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float(s
 // Round to nearest even through the hardware conversion (NaN stays NaN).
 __device__ __forceinline__ uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return f32_bf16(lo) | static_cast<uint32_t>(f32_bf16(hi)) << 16;
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
 }
 
 // Element j of a row of binary32 (bf16 == 0) or bf16 values.
