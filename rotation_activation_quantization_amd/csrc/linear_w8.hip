@@ -37,6 +37,33 @@ __device__ __forceinline__ float finish(const W8Args& a, int t, int k, int32_t a
   return fmaf(v * a.scale[t], a.w_scale[k], a.bias ? a.bias[k] : 0.f);
 }
 
+// Results of token t from channel k on: vectors at whatever address they have
+// (the output's rows need not be aligned; 2048 x 4096 x 4094 took 58.7 us with
+// single elements there, 40.0 so), single ones at the row's end.
+template <int N>
+__device__ __forceinline__ void store_results(const W8Args& a, int t, int k, const float (&o)[N], bool whole) {
+  const int64_t at = static_cast<int64_t>(t) * a.ldo + k;
+  if (whole && a.out_bf16) {
+    uint16_t* const out = static_cast<uint16_t*>(a.out) + at;
+    uint32_t h[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) h[e] = row::pack_bf16(o[2 * e], o[2 * e + 1]);
+    if (N == 4) row::store_as<false>(out, wave::u32x2_t{h[0], h[1]});
+#pragma unroll
+    for (int e = 0; e < N / 8; ++e)
+      row::store_as<false>(out + 8 * e, wave::u32x4_t{h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]});
+  } else if (whole) {
+    float* const out = static_cast<float*>(a.out) + at;
+#pragma unroll
+    for (int e = 0; e < N; e += 4)
+      row::store_as<false>(out + e, wave::f32x4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (k + e < a.R) row::store_elem(a.out, at + e, o[e], a.out_bf16);
+  }
+}
+
 // ---- large tiles ------------------------------------------------------------
 //
 // Tile p of the order -> (token tile, channel tile): token tiles fastest over
@@ -340,7 +367,6 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  const bool wide = (a.ldo % 8 == 0) && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   int copy = 0;
   for (; p < end; p += stride) {
     int tm, tn;
@@ -414,7 +440,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
     for (int q = 0; q < FK / 4; ++q) {
       const int k0 = n0 + 16 * wk * FK + 64 * q + 16 * g;
       if (k0 >= a.R) continue;
-      const bool whole = wide && k0 + 16 <= a.R;
+      const bool whole = k0 + 16 <= a.R;
       float v[16], b[16], ws[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -443,23 +469,7 @@ __device__ __forceinline__ void w8_tile(const W8Args& a, int tiles_m, int tiles_
           if (A4) x = fmaf(-zero, ws[e], x);
           o[e] = fmaf(x * scale, v[e], b[e]);
         }
-        const int64_t at = static_cast<int64_t>(t) * a.ldo + k0;
-        if (whole && a.out_bf16) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = row::pack_bf16(o[2 * e], o[2 * e + 1]);
-          wave::u32x4_t* out = reinterpret_cast<wave::u32x4_t*>(static_cast<uint16_t*>(a.out) + at);
-          out[0] = wave::u32x4_t{h[0], h[1], h[2], h[3]};
-          out[1] = wave::u32x4_t{h[4], h[5], h[6], h[7]};
-        } else if (whole) {
-          wave::f32x4_t* out = reinterpret_cast<wave::f32x4_t*>(static_cast<float*>(a.out) + at);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = wave::f32x4_t{o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (k0 + e < a.R) row::store_elem(a.out, at + e, o[e], a.out_bf16);
-        }
+        store_results(a, t, k0, o, whole);
       }
     }
   }
@@ -495,18 +505,7 @@ __global__ __launch_bounds__(256) void w8_join_kernel(W8Args a, int tiles_m, int
   float o[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) o[c] = finish(a, t, min(k + c, a.R - 1), sum[c]);
-  const int64_t to = static_cast<int64_t>(t) * a.ldo + k;
-  if (k + 4 <= a.R && a.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
-    if (a.out_bf16)
-      *reinterpret_cast<wave::u32x2_t*>(static_cast<uint16_t*>(a.out) + to) =
-          wave::u32x2_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3])};
-    else
-      *reinterpret_cast<wave::f32x4_t*>(static_cast<float*>(a.out) + to) = wave::f32x4_t{o[0], o[1], o[2], o[3]};
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (k + c < a.R) row::store_elem(a.out, to + c, o[c], a.out_bf16);
-  }
+  store_results(a, t, k, o, k + 4 <= a.R);
 }
 
 template <bool A4, int WK, int WT, int FK, int FT, int KU, int S>
@@ -531,25 +530,27 @@ hipError_t run_tile(const W8Args& a, int splits, hipStream_t s) {
 
 // The tiles there are, and what they cost: microseconds for 128 of k with one
 // work-group on a CU and with two side by side, and for a tile's start and
-// stores, fitted to 300 timings of 25 shapes (40 x 4096 x 4096 to 8192 x 1024 x
-// 1024; 10 % rms).  Taking the least estimate lands on the fastest of the timed
-// choices, or within 6 % of it, at every one of those shapes.  Both operands of
+// stores, fitted to 714 timings of 25 shapes (40 x 4096 x 4096 to 8192 x 1024 x
+// 1024; 10 % rms) beside the call's 4 us.  The least estimate picks the fastest
+// of the timed choices or one within 3 % of it, but for 64 x 14336 x 4096 (5 %)
+// and 64 x 28672 x 8192 (11 %); 0.5 % on average.  Both operands of
 // the smaller tiles come a whole 128-byte line a row and step (KU = 2): 512 x
-// 4096 x 4096 took 19.8 us with 64 bytes a step, 13.9 with 128.
+// 4096 x 4096 took 19.8 us with 64 bytes a step, 13.9 with 128 (12.8 now, see
+// the factors above).
 struct TileCost {
   int bm, bn, step, fit;
   double one, two, tile;
 };
-constexpr TileCost kTiles8[] = {{256, 256, 64, 1, 1.40, 0, 3.6},   // 4 x 2 waves of 64 channels x 128 tokens
-                                {128, 128, 128, 1, 0.474, 0, 1.8},  // 2 x 2 waves of 64 x 64
-                                {64, 128, 128, 1, 0.287, 0, 1.5},   // 2 x 2 waves of 64 x 32
-                                {64, 64, 128, 2, 0.193, 0.352, 1.7},  // 1 x 4 waves of 64 x 16
-                                {64, 64, 256, 1, 0.182, 0, 1.5}};   // the same, 256 of k a step
-constexpr TileCost kTiles4[] = {{256, 256, 64, 1, 1.48, 0, 4.9},   // 2 x 4 waves of 128 x 64: codes are widened twice
-                                {128, 128, 128, 1, 0.539, 0, 2.0},  // 2 x 4 waves of 64 x 32
-                                {128, 64, 128, 1, 0.313, 0, 1.3},   // 1 x 4 waves of 64 x 32
-                                {64, 64, 128, 2, 0.236, 0.373, 1.7},
-                                {64, 64, 256, 1, 0.190, 0, 1.6}};
+constexpr TileCost kTiles8[] = {{256, 256, 64, 1, 1.35, 0, 2.8},   // 4 x 2 waves of 64 channels x 128 tokens
+                                {128, 128, 128, 1, 0.453, 0, 1.4},  // 2 x 2 waves of 64 x 64
+                                {64, 128, 128, 1, 0.280, 0, 1.2},   // 2 x 2 waves of 64 x 32
+                                {64, 64, 128, 2, 0.184, 0.341, 1.4},  // 1 x 4 waves of 64 x 16
+                                {64, 64, 256, 1, 0.176, 0, 1.3}};   // the same, 256 of k a step
+constexpr TileCost kTiles4[] = {{256, 256, 64, 1, 1.44, 0, 3.7},   // 2 x 4 waves of 128 x 64: codes are widened twice
+                                {128, 128, 128, 1, 0.535, 0, 1.7},  // 2 x 4 waves of 64 x 32
+                                {128, 64, 128, 1, 0.308, 0, 1.2},   // 1 x 4 waves of 64 x 32
+                                {64, 64, 128, 2, 0.238, 0.363, 1.7},
+                                {64, 64, 256, 1, 0.187, 0, 1.5}};
 
 struct Plan {
   int kind, splits;
@@ -557,7 +558,7 @@ struct Plan {
 };
 
 // The least estimate over the tiles and over parts of the row joined by a
-// second kernel (3.2 us, and 3.3 TB/s over the partial sums).
+// second kernel (3.5 us, and 3.3 TB/s over the partial sums).
 Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
   Plan best{0, 1, 1e30};
   const double bytes = static_cast<double>(R) * n + (a4 ? 0.5 : 1.0) * T * n + 2.0 * T * R;
@@ -571,7 +572,7 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
       double us = t.fit == 1 ? per_cu * (k * t.one + t.tile)
                              : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
       us = fmax(us, bytes / 7e6);
-      if (splits > 1) us += 3.2 + tiles * splits * t.bm * t.bn * 4 / 3.3e6;
+      if (splits > 1) us += 3.5 + tiles * splits * t.bm * t.bn * 4 / 3.3e6;
       if (us < best.us) best = {c, splits, us};
     }
   }
@@ -798,8 +799,8 @@ bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24)
 // them, moved back where they would pass the row's end, and the shifts that
 // take the bytes out and leave zeros beyond n.  (A load at an odd address costs
 // several times an aligned one: 1 x 14338 x 4096 took 27 us with those, 17.6
-// us so.)  No
-// dword without a byte of the row is read.  TINY: rows shorter than a chunk, byte by byte.
+// us so.)  No dword without a byte of the row is read, if the row has the chunk's
+// bytes at least.  TINY: shorter rows, byte by byte.
 template <bool A4, bool TINY>
 struct AnyChunk {
   static constexpr int kBytes = A4 ? 8 : 16, kWords = kBytes / 4;
@@ -988,17 +989,17 @@ __global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
     const int t = m0 + 16 * (wt * FT + j) + (lane & 15);
     if (t >= a.T) continue;
 #pragma unroll
-    for (int f = 0; f < FK; ++f)
+    for (int f = 0; f < FK; ++f) {
+      float o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = n0 + 16 * (wk * FK + f) + 4 * (lane >> 4) + e;
-        if (k < a.R)
-          row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, fac.finish(f, e, j, acc[f][j][e]), a.out_bf16);
-      }
+      for (int e = 0; e < 4; ++e) o[e] = fac.finish(f, e, j, acc[f][j][e]);
+      const int k = n0 + 16 * (wk * FK + f) + 4 * (lane >> 4);
+      store_results(a, t, k, o, k + 4 <= a.R);
+    }
   }
 }
 
-constexpr double kAnyOne = 0.62, kAnyTwo = 0.73;  // as in TileCost, for its 64 x 64 tile
+constexpr double kAnyOne = 0.50, kAnyTwo = 0.74;  // as in TileCost, for its 64 x 64 tile
 
 template <bool A4>
 hipError_t run_any(const W8Args& a, hipStream_t s) {
@@ -1082,7 +1083,7 @@ hipError_t run_few_any(const W8Args& a, hipStream_t s) {
 // Many tokens: the rows are laid out anew in the workspace, in whole chunks with
 // zeros beyond n, and the tile kernels run on those.  One launch for both
 // operands: rows 0 .. rows_w - 1 are the weights', the rest the codes'.
-struct PackArgs {
+struct PackArgs {  // rows of at least sixteen bytes
   const uint8_t* src[2];
   uint8_t* dst[2];
   int64_t ld[2];
@@ -1157,13 +1158,18 @@ Way way_of(const W8Args& a) {
   if (aligned) return {Way::kTiles, tile_plan(a.T, a.n, a.R, a.a4 != 0)};
   const Packed k = packing(a);
   Plan p = tile_plan(a.T, k.n, a.R, a.a4 != 0);
-  // packing: a launch and the workspace, and 4 TB/s over what it reads and writes
-  p.us += 5.0 + 2.0 * (k.w_bytes + k.t_bytes) / 4e6;
+  // packing: a launch and the workspace, and 5 TB/s over what it reads and writes
+  p.us += 7.0 + 2.0 * (k.w_bytes + k.t_bytes) / 5e6;
   const double tiles = static_cast<double>((a.T + int64_t{63}) / 64) * static_cast<double>((a.R + int64_t{63}) / 64);
   const double per_cu = ceil(tiles / kCus), deep = a.n / 128.0;
   const double any =
-      floor(per_cu / 2) * (deep * kAnyTwo + 1.5) + fmod(per_cu, 2) * (deep * kAnyOne + 1.5);
-  if ((any < p.us && tiles < (1 << 22)) || a.n < 16) return {Way::kAny, {0, 1, any}};
+      floor(per_cu / 2) * (deep * kAnyTwo + 2.0) + fmod(per_cu, 2) * (deep * kAnyOne + 1.8);
+  // w8_any up to where packing both operands and the tiles are less: 1000 x 1111 x
+  // 1000 8.0 us, packed 11.5; 64 x 4098 x 4096 18.0 and 23.7; 256 x 4098 x 14336
+  // 51.8 and 45.3; 4000 x 300 x 4000 33.4 and 20.6.  (At 18 shapes the estimate
+  // takes the slower one by 15 % at most.)  Packing reads whole 16-byte chunks, so
+  // rows of fewer bytes stay here.
+  if ((any < p.us && tiles < (1 << 22)) || (a.a4 ? a.n / 2 : a.n) < 16) return {Way::kAny, {0, 1, any}};
   return {Way::kPackTiles, p};
 }
 

@@ -377,3 +377,40 @@ def test_bindings_refuse_wrong_operands():
         with pytest.raises(ValueError):
             f()
             print("accepted", i)
+
+
+@pytest.mark.parametrize("n", [16, 22, 30])
+def test_many_short_int4_rows(n):
+    t, rows = 4100, 4000
+    codes, s, z, w, v, b = operands(t, n, rows, 11, True)
+    ref = B.w8_linear(B.unpack_int4(codes), s, z, w, v, b)
+    c, dw = dev(codes), dev(w)
+    assert R.int4_w8_linear_kernel_name(c, dw) == "w8_any"
+    got = R.int4_w8_linear(c, dev(s), dev(z), dw, dev(v), dev(w.sum(axis=1, dtype=np.int32)), bias=dev(b),
+                           dtype=torch.float32)
+    check_product(got, ref, s, v, torch.float32, f"int4_w8_linear {t} x {n} x {rows}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t,n,rows", [(40, 2048, 2046), (200, 4096, 1030), (700, 256, 515), (520, 1024, 2049),
+                                      (2500, 128, 1537)])
+def test_output_rows_of_any_alignment(t, n, rows, dtype):
+    """Output rows that start anywhere and end inside a vector, on the aligned tiles
+    (with and without the split row): every element, and nothing around them."""
+    codes, s, z, w, v, b = operands(t, n, rows, 12, False)
+    ref = B.w8_linear(codes.astype(np.float64), s, None, w, v, b)
+    dc, dw = dev(codes), dev(w)
+    name = R.int8_linear_kernel_name(dc, dw)
+    for ldo, off in ((rows, 1), (rows + 3, 0)):
+        buf = torch.full((off + t * ldo,), float(GUARD), dtype=dtype, device="cuda")
+        out = buf[off:].view(t, ldo)[:, :rows]
+        R.int8_linear(dc, dev(s), dw, dev(v), bias=dev(b), out=out)
+        check_product(out, ref, s, v, dtype, f"int8_linear into {ldo} + {off} [{name}]")
+        assert (buf[:off] == GUARD).all() and (buf[off:].view(t, ldo)[:, rows:] == GUARD).all()
+    codes, s, z, w, v, b = operands(t, n, rows, 13, True)
+    ref = B.w8_linear(B.unpack_int4(codes), s, z, w, v, b)
+    out = torch.full((t, rows + 1), float(GUARD), dtype=dtype, device="cuda")
+    R.int4_w8_linear(dev(codes), dev(s), dev(z), dev(w), dev(v), dev(w.sum(axis=1, dtype=np.int32)), bias=dev(b),
+                     out=out[:, :rows])
+    check_product(out[:, :rows], ref, s, v, dtype, f"int4_w8_linear into {rows + 1}")
+    assert (out[:, rows:] == GUARD).all()

@@ -133,3 +133,16 @@ def test_struct_layout_matches_the_header(tmp_path):
     want = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     got = [getattr(R._ResidualNormArgs, n).offset for n in names] + [ctypes.sizeof(R._ResidualNormArgs)]
     assert got == want
+
+
+def test_rows_shorter_than_a_chunk_are_not_laid_out_anew(L):
+    """Laying rows out anew reads sixteen bytes at a time: INT4 rows of fewer (n < 32)
+    and INT8 rows of fewer (n < 16) take the kernel that reads what there is, however
+    many tokens and channels there are."""
+    for tokens, rows in ((33, 40), (4000, 4000), (8192, 28672), (100000, 70000)):
+        for n in (16, 18, 24, 30):
+            assert L.signrot_int4_w8_linear_kernel_name(FAKE, tokens, n, FAKE, n, rows) == b"w8_any", (tokens, n, rows)
+            assert L.signrot_int4_w8_linear_workspace(FAKE, tokens, n, FAKE, n, rows) == 0
+        for n in (1, 2, 15):
+            assert L.signrot_int8_linear_kernel_name(FAKE, n, tokens, n, FAKE, n, rows) == b"w8_any", (tokens, n, rows)
+            assert L.signrot_int8_linear_workspace(FAKE, n, tokens, n, FAKE, n, rows) == 0
