@@ -339,7 +339,18 @@ void run_rows_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
 template <bool WHOLE>
 void run_rows(const NormArgs& a, dim3 grid, hipStream_t s) {
   const int chunks = static_cast<int>((a.n + 7) / 8);
-  const int v = row::chunks_per_thread(chunks, a.tokens);
+  int v = row::chunks_per_thread(chunks, a.tokens);
+  // A CU holds 24 waves of the bf16 kernel with two chunks a thread and 16 of the one
+  // with four, each of which does twice as much: where only the latter takes
+  // all rows in one round (2048 x 4096: 15.7 us, 17.9 with two; 1024 x 8192 16.1 and
+  // 19.1; 1237 x 5120 14.8 and 15.7; but 1024 x 5120, one round of either, 13.1 and
+  // 12.1).  The binary32 kernel gains nothing (1237 x 5120 22.7 and 22.1).
+  if (WHOLE && a.h_type == SIGNROT_BF16 && v == 2) {
+    auto places = [&](int chunks_each, int waves) {
+      return device_cu_count() * (waves / (row::threads_for(chunks, chunks_each) / 64));
+    };
+    if (a.tokens > places(2, 24) && a.tokens <= places(4, 16)) v = 4;
+  }
   const dim3 block(static_cast<unsigned>(row::threads_for(chunks, v)));
   switch (v) {
     case 1: run_rows_as<1, WHOLE>(a, grid, block, s); break;

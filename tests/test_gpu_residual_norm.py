@@ -306,3 +306,12 @@ def test_side_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)), i
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("t,n", [(1024, 8192), (1025, 8192), (769, 8192), (768, 8192), (1280, 5120), (1025, 5120),
+                                 (2048, 4096), (2049, 4096), (1537, 4096), (6000, 1024)])
+def test_row_counts_around_a_full_device(t, n, norm):
+    """Row counts on both sides of what the device holds at once, where the number
+    of chunks a thread takes changes."""
+    check(t, n, norm=norm, bias=norm == "layer", mods="index")
