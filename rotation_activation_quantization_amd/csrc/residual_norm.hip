@@ -23,9 +23,14 @@ __device__ __forceinline__ int64_t modulation_row(const NormArgs& a, int64_t t) 
 }
 
 // One work-group per row, the row in registers (V chunks of eight values a
-// thread).  y and h are read once, h' and u
-// written once; the statistics are one or two reductions each (a LayerNorm's
-// centred sum of squares follows its mean, so that it cannot cancel).
+// thread).  y and h are read once, h' and u written once; the statistics are one
+// or two reductions each (a LayerNorm's centred sum of squares follows its mean,
+// so that it cannot cancel).  Many rows are bound by memory: 8192 x 8192 in bf16,
+// RMS, 99 to 106 us, 5.1 to 5.4 TB/s, where a copy reaches 5.2; LayerNorms with
+// modulations take 137, for four reductions and seven rows of parameters from L2.
+// One row is bound by its latency: 3.7 us at 4096.  Registers decide how many
+// rows a CU holds: a single reduction for mean and variance took twelve more
+// and was slower (106 us at 8192 x 8192).
 template <int V, bool HB, bool WHOLE>
 __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
   __shared__ float sh[4][16];
