@@ -10,8 +10,8 @@ namespace signrot {
 namespace {
 
 // One work-group per row, the row in registers (V chunks of eight values a
-// thread), so it is read once.  Bound by memory: 8192 x 4096 23 us with the
-// input in no cache (4.4 TB/s), and by latency for one row (2.5 us at 4096).
+// thread), so it is read once.  Bound by memory: 8192 x 4096 23 us between two
+// large products (4.4 TB/s), and by latency for one row (2.5 us at 4096).
 template <int V, bool WHOLE>
 __global__ __launch_bounds__(1024) void quant_int8_rows_kernel(const uint16_t* __restrict__ x, int n, int64_t ld,
                                                               int8_t* __restrict__ codes, int64_t ldc,
