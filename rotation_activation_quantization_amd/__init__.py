@@ -201,6 +201,8 @@ def _stream_of(t):
 
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+    if not t.is_cuda:
+        raise ValueError(f"expected a tensor on a GPU, not on {t.device}")
     return _raw_stream(t.device.index)
 
 
