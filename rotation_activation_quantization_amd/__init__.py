@@ -647,7 +647,10 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
             ldm = ldm2
         elif cptr and ldm != ldm2:
             raise ValueError("mod_scale and mod_shift must have the same row stride")
-        mod_rows = min((r for r in (grows, mrows, crows) if r is not None), default=0)
+        counts = {r for r in (grows, mrows, crows) if r is not None}
+        if mod_index is not None and len(counts) > 1:
+            raise ValueError(f"gate, mod_scale and mod_shift have {sorted(counts)} rows for one mod_index")
+        mod_rows = min(counts, default=0)
     if h_out is None:
         h_out = torch.empty(t, n, dtype=h.dtype, device=device)
         hoptr, ldho = h_out.data_ptr(), n
@@ -689,7 +692,8 @@ def signrot_residual_norm(h, y=None, norm: str = "rms", post_norm: str | None = 
     h (bf16 or f32) and y (bf16, None: no branch) are [T, n]; norm and
     post_norm (default: the same) are "rms", "layer" or "none"; weights and
     biases are [n]; gate, mod_scale and mod_shift are [n], or [m, n] with a row
-    per token, or one per sequence picked by mod_index (int32 [T]); all of
+    per token, or one per sequence picked by mod_index (int32 [T]; the same m
+    for all three then), mod_scale and mod_shift in the same layout; all of
     them bf16, or all f32.  Returns (h' of h's type, u bf16).  h_out may be h,
     to update the stream in place; `out` may pass u's tensor."""
     return _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight,

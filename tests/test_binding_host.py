@@ -20,3 +20,85 @@ def test_operands_in_host_memory_are_refused_with_a_value_error():
                  lambda: R.residual_norm(x), lambda: R.rotate_quant_int4_outlier(x, 0, 1)):
         with pytest.raises(ValueError):
             call()
+
+
+class GpuTensor:
+    """What the binding asks of a tensor in GPU memory; nothing reads its pointer."""
+
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.bfloat16, step=None, gpu=0):
+        self.shape, self.dtype, self.gpu = torch.Size(shape), dtype, gpu
+        self.device = torch.device("cuda", gpu)
+        self.step = step
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i=None):
+        s = (1,) if self.dim() == 1 else (self.shape[1] if self.step is None else self.step, 1)
+        return s if i is None else s[i]
+
+    def is_contiguous(self):
+        return self.step is None
+
+    def get_device(self):
+        return self.gpu
+
+    def data_ptr(self):
+        return 0x100000
+
+
+class Recorder:
+    """Stands in for the library: notes its calls, all of which succeed."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    recorder = Recorder()
+    monkeypatch.setattr(R, "_lib", recorder)
+    monkeypatch.setattr(R, "_raw_stream", lambda index: 0x5000 + index)
+    return recorder
+
+
+def norm_args(call):
+    (name, (packed, _)), = call.calls
+    assert name == "signrot_residual_norm"
+    return R._ResidualNormArgs.from_buffer_copy(packed)
+
+
+def norm(tokens=4, n=64, **kw):
+    h = GpuTensor(tokens, n)
+    return R.residual_norm(h, h, h_out=GpuTensor(tokens, n), out=GpuTensor(tokens, n), **kw)
+
+
+def test_modulations_of_different_row_counts_are_refused(library):
+    """An index that is valid for the longer one would be clamped to the shorter."""
+    index = GpuTensor(4, dtype=torch.int32)
+    for a, b in (("gate", "mod_scale"), ("gate", "mod_shift"), ("mod_scale", "mod_shift")):
+        with pytest.raises(ValueError):
+            norm(mod_index=index, **{a: GpuTensor(3, 64), b: GpuTensor(2, 64)})
+        with pytest.raises(ValueError):
+            norm(mod_index=index, **{a: GpuTensor(1, 64), b: GpuTensor(2, 64)})
+    assert not library.calls
+    norm(mod_index=index, gate=GpuTensor(64), mod_scale=GpuTensor(3, 64), mod_shift=GpuTensor(3, 64))
+    a = norm_args(library)
+    assert (a.ldg, a.ldm, a.mod_rows) == (0, 64, 3)
+
+
+def test_without_an_index_more_modulation_rows_than_tokens_are_taken(library):
+    norm(gate=GpuTensor(6, 64), mod_scale=GpuTensor(5, 64))
+    a = norm_args(library)
+    assert (a.ldg, a.ldm, a.mod_rows) == (64, 64, 5)
