@@ -616,6 +616,8 @@ def _modulation(v, name, t, n, index, dtype, gpu):
     ptr, step = _matrix(v, name, None, n, dtype, gpu)
     if v.shape[0] < (1 if index is not None else t):
         raise ValueError(f"{name} has {v.shape[0]} rows for {t} tokens")
+    if v.shape[0] == 1 or (index is None and t == 1):
+        step = 0  # row 0 is the only one taken
     return ptr, step, v.shape[0]
 
 

@@ -102,3 +102,18 @@ def test_without_an_index_more_modulation_rows_than_tokens_are_taken(library):
     norm(gate=GpuTensor(6, 64), mod_scale=GpuTensor(5, 64))
     a = norm_args(library)
     assert (a.ldg, a.ldm, a.mod_rows) == (64, 64, 5)
+
+
+@pytest.mark.parametrize("tokens,index", [(1, False), (1, True), (4, True)])
+def test_the_stride_of_a_single_modulation_row_does_not_matter(library, tokens, index):
+    """One row cut from a wider projection beside a contiguous one."""
+    kw = {"mod_index": GpuTensor(tokens, dtype=torch.int32)} if index else {}
+    norm(tokens, gate=GpuTensor(1, 64, step=384), mod_scale=GpuTensor(1, 64), mod_shift=GpuTensor(1, 64, step=384), **kw)
+    a = norm_args(library)
+    assert (a.ldg, a.ldm) == (0, 0) and a.gate and a.mod_scale and a.mod_shift
+
+
+def test_one_token_takes_the_first_row_of_any_modulations(library):
+    norm(1, gate=GpuTensor(3, 64), mod_scale=GpuTensor(1, 64), mod_shift=GpuTensor(2, 64, step=128))
+    a = norm_args(library)
+    assert (a.ldg, a.ldm) == (0, 0) and a.gate and a.mod_scale and a.mod_shift
