@@ -206,6 +206,21 @@ def _stream_of(t):
     return _raw_stream(t.device.index)
 
 
+def _run(name, t, *args):
+    """Calls the library's function `name` with args and the current stream of
+    t's GPU, and with that GPU as the current one: a device's default stream has
+    no handle of its own, so it is the current device that the kernel runs on."""
+    import torch
+
+    call, stream, gpu = getattr(lib(), name), _stream_of(t), t.get_device()
+    if gpu == torch.cuda.current_device():
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(gpu):
+            status = call(*args, stream)
+    check(status, name)
+
+
 def _rows(x):
     """(pointer, tokens, n, ld) of a [T, n] bf16 tensor whose rows are contiguous."""
     import torch
@@ -227,8 +242,8 @@ def signrot_calibrate(x):
     c = ctypes.c_int32()
     tt = ctypes.c_int64()
     m = ctypes.c_float()
-    check(lib().signrot_calibrate(ptr, t, n, ld, d.data_ptr(), ctypes.addressof(c), ctypes.addressof(tt),
-                                  ctypes.addressof(m), _stream_of(x)), "signrot_calibrate")
+    _run("signrot_calibrate", x, ptr, t, n, ld, d.data_ptr(), ctypes.addressof(c), ctypes.addressof(tt),
+         ctypes.addressof(m))
     return d, c.value, tt.value, m.value
 
 
@@ -243,8 +258,8 @@ def signrot_calibrate_noalloc(x, d_out):
     c = ctypes.c_int32()
     tt = ctypes.c_int64()
     m = ctypes.c_float()
-    check(lib().signrot_calibrate_noalloc(ptr, t, n, ld, d_out.data_ptr(), ctypes.addressof(c), ctypes.addressof(tt),
-                                          ctypes.addressof(m), _stream_of(x)), "signrot_calibrate_noalloc")
+    _run("signrot_calibrate_noalloc", x, ptr, t, n, ld, d_out.data_ptr(), ctypes.addressof(c), ctypes.addressof(tt),
+         ctypes.addressof(m))
     return c.value, tt.value, m.value
 
 
@@ -264,9 +279,8 @@ def signrot_rotate_quant_int4(x, d, y_out: bool = False, out=None):
     else:
         codes, scale, zero = out[:3]
         y = out[3] if len(out) > 3 else None
-    check(lib().signrot_rotate_quant_int4(ptr, t, n, ld, d.data_ptr(), codes.data_ptr(), scale.data_ptr(),
-                                          zero.data_ptr(), y.data_ptr() if y is not None else None,
-                                          _stream_of(x)), "signrot_rotate_quant_int4")
+    _run("signrot_rotate_quant_int4", x, ptr, t, n, ld, d.data_ptr(), codes.data_ptr(), scale.data_ptr(),
+         zero.data_ptr(), y.data_ptr() if y is not None else None)
     return (codes, scale, zero, y) if y is not None else (codes, scale, zero)
 
 
@@ -284,10 +298,8 @@ def signrot_rotate_quant_int4_outlier(x, c: int, sigma: int, y_out: bool = False
     else:
         codes, scale, zero = out[:3]
         y = out[3] if len(out) > 3 else None
-    check(lib().signrot_rotate_quant_int4_outlier(ptr, t, n, ld, int(c), int(sigma), codes.data_ptr(),
-                                                  scale.data_ptr(), zero.data_ptr(),
-                                                  y.data_ptr() if y is not None else None, _stream_of(x)),
-          "signrot_rotate_quant_int4_outlier")
+    _run("signrot_rotate_quant_int4_outlier", x, ptr, t, n, ld, int(c), int(sigma), codes.data_ptr(),
+         scale.data_ptr(), zero.data_ptr(), y.data_ptr() if y is not None else None)
     return (codes, scale, zero, y) if y is not None else (codes, scale, zero)
 
 
@@ -303,9 +315,8 @@ def signrot_rotate_quant_int4_zint(x, c: int, sigma: int, out=None):
         zero = torch.empty(t, dtype=torch.float32, device=x.device)
     else:
         codes, scale, zero = out[:3]
-    check(lib().signrot_rotate_quant_int4_zint(ptr, t, n, ld, int(c), int(sigma), codes.data_ptr(),
-                                               scale.data_ptr(), zero.data_ptr(), _stream_of(x)),
-          "signrot_rotate_quant_int4_zint")
+    _run("signrot_rotate_quant_int4_zint", x, ptr, t, n, ld, int(c), int(sigma), codes.data_ptr(), scale.data_ptr(),
+         zero.data_ptr())
     return codes, scale, zero
 
 
@@ -326,10 +337,8 @@ def signrot_swiglu_rotate_quant_int4(gate, up, c: int, sigma: int, y_out: bool =
     else:
         codes, scale, zero = out[:3]
         y = out[3] if len(out) > 3 else None
-    check(lib().signrot_swiglu_rotate_quant_int4(ptr, uptr, t, n, ld, int(c), int(sigma), codes.data_ptr(),
-                                                 scale.data_ptr(), zero.data_ptr(),
-                                                 y.data_ptr() if y is not None else None, _stream_of(gate)),
-          "signrot_swiglu_rotate_quant_int4")
+    _run("signrot_swiglu_rotate_quant_int4", gate, ptr, uptr, t, n, ld, int(c), int(sigma), codes.data_ptr(),
+         scale.data_ptr(), zero.data_ptr(), y.data_ptr() if y is not None else None)
     return (codes, scale, zero, y) if y is not None else (codes, scale, zero)
 
 
@@ -340,8 +349,7 @@ def signrot_dequant(codes, scale, zero, n: int | None = None):
     t = codes.shape[0]
     n = codes.shape[1] * 2 if n is None else int(n)
     y = torch.empty((t, n), dtype=torch.float32, device=codes.device)
-    check(lib().signrot_dequant(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), t, n, y.data_ptr(),
-                                _stream_of(codes)), "signrot_dequant")
+    _run("signrot_dequant", codes, codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), t, n, y.data_ptr())
     return y
 
 
@@ -354,8 +362,7 @@ def signrot_fold_weights(w, d):
     if d.dtype != torch.int8 or d.numel() != n or not d.is_contiguous():
         raise ValueError("d must be a contiguous int8 tensor of n entries")
     out = torch.empty((rows, n), dtype=torch.float32, device=w.device)
-    check(lib().signrot_fold_weights(ptr, rows, n, ld, d.data_ptr(), out.data_ptr(), _stream_of(w)),
-          "signrot_fold_weights")
+    _run("signrot_fold_weights", w, ptr, rows, n, ld, d.data_ptr(), out.data_ptr())
     return out
 
 
@@ -365,7 +372,7 @@ def signrot_weight_rowsum(w):
 
     ptr, rows, n, ld = _rows(w)
     out = torch.empty(rows, dtype=torch.float32, device=w.device)
-    check(lib().signrot_weight_rowsum(ptr, rows, n, ld, out.data_ptr(), _stream_of(w)), "signrot_weight_rowsum")
+    _run("signrot_weight_rowsum", w, ptr, rows, n, ld, out.data_ptr())
     return out
 
 
@@ -393,9 +400,8 @@ def signrot_int4_linear(codes, scale, zero, w, rowsum, out=None):
             raise ValueError(f"{name} must be a contiguous float32 tensor of {size} entries")
     if out is None:
         out = torch.empty((t, rows), dtype=torch.float32, device=codes.device)
-    check(lib().signrot_int4_linear(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), t, n, wptr, ld,
-                                    rowsum.data_ptr(), rows, out.data_ptr(), _stream_of(codes)),
-          "signrot_int4_linear")
+    _run("signrot_int4_linear", codes, codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), t, n, wptr, ld,
+         rowsum.data_ptr(), rows, out.data_ptr())
     return out
 
 
@@ -489,9 +495,8 @@ def signrot_quant_int8(x, sums: bool = False, out=None):
             raise ValueError("out must hold (codes, scale[, sum])")
         qptr, ldc = _matrix(out[0], "codes", t, n, torch.int8, gpu)
         sptr = _vector(out[1], "scale", t, torch.float32, gpu)
-    check(lib().signrot_quant_int8(ptr, t, n, ld, qptr, ldc, sptr,
-                                   _vector(out[2], "sum", t, torch.int32, gpu) if sums else 0, _stream_of(x)),
-          "signrot_quant_int8")
+    _run("signrot_quant_int8", x, ptr, t, n, ld, qptr, ldc, sptr,
+         _vector(out[2], "sum", t, torch.int32, gpu) if sums else 0)
     return out
 
 
@@ -536,8 +541,7 @@ def signrot_int8_linear(codes, scale, w, w_scale, bias=None, dtype=None, out=Non
     out, kind, optr, ldo = _product_out(out, dtype, t, rows, device, gpu)
     L = lib()
     ws, size, _owner = _workspace(L.signrot_int8_linear_workspace(aptr, lda, t, n, wptr, ldw, rows), device)
-    check(L.signrot_int8_linear(aptr, lda, sptr, t, n, wptr, ldw, vptr, bptr, rows, optr, ldo, kind, ws, size,
-                                _stream_of(codes)), "signrot_int8_linear")
+    _run("signrot_int8_linear", codes, aptr, lda, sptr, t, n, wptr, ldw, vptr, bptr, rows, optr, ldo, kind, ws, size)
     return out
 
 
@@ -563,8 +567,8 @@ def signrot_int4_w8_linear(codes, scale, zero, w, w_scale, w_sum, bias=None, dty
     L = lib()
     aptr = codes.data_ptr()
     ws, size, _owner = _workspace(L.signrot_int4_w8_linear_workspace(aptr, t, n, wptr, ldw, rows), device)
-    check(L.signrot_int4_w8_linear(aptr, sptr, zptr, t, n, wptr, ldw, vptr, uptr, bptr, rows, optr, ldo,
-                                   kind, ws, size, _stream_of(codes)), "signrot_int4_w8_linear")
+    _run("signrot_int4_w8_linear", codes, aptr, sptr, zptr, t, n, wptr, ldw, vptr, uptr, bptr, rows, optr, ldo, kind,
+         ws, size)
     return out
 
 
@@ -622,7 +626,7 @@ def _modulation(v, name, t, n, index, dtype, gpu):
 
 
 def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight, bias,
-                   mod_scale, mod_shift, mod_index, h_out, out, codes, where):
+                   mod_scale, mod_shift, mod_index, h_out, out, codes):
     """Checks, allocates what the caller did not give and launches; `codes`: out is (codes, scale), not u."""
     import torch
 
@@ -678,7 +682,7 @@ def _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias,
         gptr, ldg, _vector(weight, "weight", n, param, gpu), _vector(bias, "bias", n, param, gpu),
         mptr, cptr, ldm, _vector(mod_index, "mod_index", t, torch.int32, gpu), mod_rows,
         alpha, beta, eps if post_eps is None else post_eps, eps, _NORMS[post_norm], _NORMS[norm], h_type, p_type)
-    check(lib().signrot_residual_norm(args, _stream_of(h)), where)
+    _run("signrot_residual_norm", h, args)
     return h_out, out
 
 
@@ -699,7 +703,7 @@ def signrot_residual_norm(h, y=None, norm: str = "rms", post_norm: str | None = 
     them bf16, or all f32.  Returns (h' of h's type, u bf16).  h_out may be h,
     to update the stream in place; `out` may pass u's tensor."""
     return _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha, beta, weight,
-                          bias, mod_scale, mod_shift, mod_index, h_out, out, False, "signrot_residual_norm")
+                          bias, mod_scale, mod_shift, mod_index, h_out, out, False)
 
 
 def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: str | None = None, eps: float = 1e-6,
@@ -710,8 +714,7 @@ def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: st
     its binary32 values: returns (h', codes int8 [T, n], scale f32 [T]).
     `out` may pass (codes, scale)."""
     h_out, (codes, scale) = _residual_norm(h, y, norm, post_norm, eps, post_eps, post_weight, post_bias, gate, alpha,
-                                           beta, weight, bias, mod_scale, mod_shift, mod_index, h_out, out, True,
-                                           "signrot_residual_norm")
+                                           beta, weight, bias, mod_scale, mod_shift, mod_index, h_out, out, True)
     return h_out, codes, scale
 
 
@@ -726,8 +729,7 @@ def signrot_stream_ceiling(x, out=None):
         out = (torch.empty((t, n // 2), dtype=torch.uint8, device=x.device),
                torch.empty(t, dtype=torch.float32, device=x.device),
                torch.empty(t, dtype=torch.float32, device=x.device))
-    check(lib().signrot_stream_ceiling(ptr, t, n, ld, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-                                       _stream_of(x)), "signrot_stream_ceiling")
+    _run("signrot_stream_ceiling", x, ptr, t, n, ld, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr())
     return out
 
 

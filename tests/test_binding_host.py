@@ -53,16 +53,32 @@ class GpuTensor:
 
 
 class Recorder:
-    """Stands in for the library: notes its calls, all of which succeed."""
+    """Stands in for the library and the current device: notes the calls, all of
+    which succeed, and the device each was made on."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.devices, self.current = [], [], 0
 
     def __getattr__(self, name):
         def call(*args):
+            if name.endswith("_workspace"):
+                return 0
             self.calls.append((name, args))
+            self.devices.append(self.current)
             return 0
         return call
+
+    def device(self, index):
+        recorder = self
+
+        class Use:
+            def __enter__(self):
+                self.before, recorder.current = recorder.current, index
+
+            def __exit__(self, *_):
+                recorder.current = self.before
+
+        return Use()
 
 
 @pytest.fixture
@@ -70,6 +86,8 @@ def library(monkeypatch):
     recorder = Recorder()
     monkeypatch.setattr(R, "_lib", recorder)
     monkeypatch.setattr(R, "_raw_stream", lambda index: 0x5000 + index)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: recorder.current)
+    monkeypatch.setattr(torch.cuda, "device", recorder.device)
     return recorder
 
 
@@ -117,3 +135,39 @@ def test_one_token_takes_the_first_row_of_any_modulations(library):
     norm(1, gate=GpuTensor(3, 64), mod_scale=GpuTensor(1, 64), mod_shift=GpuTensor(2, 64, step=128))
     a = norm_args(library)
     assert (a.ldg, a.ldm) == (0, 0) and a.gate and a.mod_scale and a.mod_shift
+
+
+def on(gpu, *shape, dtype=torch.float32):
+    return GpuTensor(*shape, dtype=dtype, gpu=gpu)
+
+
+CALLS = {
+    "signrot_quant_int8": lambda g: R.quant_int8(
+        on(g, 4, 64, dtype=torch.bfloat16), out=(on(g, 4, 64, dtype=torch.int8), on(g, 4))),
+    "signrot_int8_linear": lambda g: R.int8_linear(
+        on(g, 4, 64, dtype=torch.int8), on(g, 4), on(g, 8, 64, dtype=torch.int8), on(g, 8), out=on(g, 4, 8)),
+    "signrot_int4_w8_linear": lambda g: R.int4_w8_linear(
+        on(g, 4, 32, dtype=torch.uint8), on(g, 4), on(g, 4), on(g, 8, 64, dtype=torch.int8), on(g, 8),
+        on(g, 8, dtype=torch.int32), out=on(g, 4, 8)),
+    "signrot_residual_norm": lambda g: R.residual_norm(
+        on(g, 4, 64), h_out=on(g, 4, 64), out=on(g, 4, 64, dtype=torch.bfloat16)),
+    "signrot_rotate_quant_int4": lambda g: R.rotate_quant_int4(
+        on(g, 4, 64, dtype=torch.bfloat16), on(g, 64, dtype=torch.int8),
+        out=(on(g, 4, 32, dtype=torch.uint8), on(g, 4), on(g, 4))),
+    "signrot_rotate_quant_int4_outlier": lambda g: R.rotate_quant_int4_outlier(
+        on(g, 4, 64, dtype=torch.bfloat16), 0, 1, out=(on(g, 4, 32, dtype=torch.uint8), on(g, 4), on(g, 4))),
+    "signrot_int4_linear": lambda g: R.int4_linear(
+        on(g, 4, 32, dtype=torch.uint8), on(g, 4), on(g, 4), on(g, 8, 64, dtype=torch.bfloat16), on(g, 8),
+        out=on(g, 4, 8)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_runs_on_the_gpu_of_its_tensors(library, name):
+    """Also when another is the current one, which is the same again afterwards."""
+    for gpu, current in ((0, 0), (1, 0), (0, 1), (1, 1)):
+        library.current = current
+        CALLS[name](gpu)
+        assert library.calls[-1][0] == name and library.calls[-1][1][-1] == 0x5000 + gpu
+        assert library.devices[-1] == gpu and library.current == current
+    assert len(library.calls) == 4
