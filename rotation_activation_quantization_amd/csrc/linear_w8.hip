@@ -907,13 +907,12 @@ struct Factors {
 };
 
 template <bool A4, int WK, int WT, int FK, int FT, int KU, bool TINY>
-__global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a) {
+__global__ __launch_bounds__(64 * WK * WT) void w8_any_kernel(W8Args a, int first_m, int first_n, int tiles_n) {
   using C = AnyTile<A4, WK, WT, FK, FT, KU>;
   __shared__ i32x4_t lds[2][C::kWSlots + C::kTSlots];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-  const int tiles_n = (a.R + C::kBN - 1) / C::kBN;
-  const int m0 = static_cast<int>(blockIdx.x / tiles_n) * C::kBM;
-  const int n0 = static_cast<int>(blockIdx.x % tiles_n) * C::kBN;
+  const int m0 = (first_m + static_cast<int>(blockIdx.x / tiles_n)) * C::kBM;
+  const int n0 = (first_n + static_cast<int>(blockIdx.x % tiles_n)) * C::kBN;
   const int wk = wid % WK, wt = wid / WK;
   const int steps = (a.n + C::kStep - 1) / C::kStep;
 
@@ -1008,13 +1007,26 @@ constexpr double kAnyOne = 0.50, kAnyTwo = 0.74;  // as in TileCost, for its 64 
 template <bool A4>
 hipError_t run_any(const W8Args& a, hipStream_t s) {
   using C = AnyTile<A4, 2, 2, 2, 2, 2>;
-  const int tiles = ((a.T + C::kBM - 1) / C::kBM) * ((a.R + C::kBN - 1) / C::kBN);
-  const dim3 grid(static_cast<unsigned>(tiles)), block(static_cast<unsigned>(C::kThreads));
-  if (a.n < 16)
-    w8_any_kernel<A4, 2, 2, 2, 2, 2, true><<<grid, block, 0, s>>>(a);
-  else
-    w8_any_kernel<A4, 2, 2, 2, 2, 2, false><<<grid, block, 0, s>>>(a);
-  return hipGetLastError();
+  // A launch holds fewer than 2^32 threads, so rows too short to be laid out anew
+  // may take several, each over some token tiles and channel tiles.
+  constexpr int kMost = 1 << 23;
+  const int tiles_m = (a.T + C::kBM - 1) / C::kBM, tiles_n = (a.R + C::kBN - 1) / C::kBN;
+  const int step_n = tiles_n < kMost ? tiles_n : kMost, step_m = kMost / step_n;
+  const dim3 block(static_cast<unsigned>(C::kThreads));
+  for (int m = 0; m < tiles_m; m += step_m) {
+    for (int n = 0; n < tiles_n; n += step_n) {
+      const int rows = tiles_m - m < step_m ? tiles_m - m : step_m;
+      const int columns = tiles_n - n < step_n ? tiles_n - n : step_n;
+      const dim3 grid(static_cast<unsigned>(rows) * static_cast<unsigned>(columns));
+      if (a.n < 16)
+        w8_any_kernel<A4, 2, 2, 2, 2, 2, true><<<grid, block, 0, s>>>(a, m, n, columns);
+      else
+        w8_any_kernel<A4, 2, 2, 2, 2, 2, false><<<grid, block, 0, s>>>(a, m, n, columns);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
 }
 
 // Few tokens: as w8_few, with both operands straight to registers, a lane (g, i)
