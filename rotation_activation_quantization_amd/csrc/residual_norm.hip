@@ -22,6 +22,18 @@ __device__ __forceinline__ int64_t modulation_row(const NormArgs& a, int64_t t) 
   return i < 0 ? 0 : (i >= a.mod_rows ? a.mod_rows - 1 : i);
 }
 
+// s / n for the sum s that every thread holds, inv_n = 1 / n rounded: one Newton
+// step from s inv_n, which leaves a representable quotient exact.  So a row of n
+// equal bf16 values, whose sum is exact, has that value as its mean and centres
+// to zeros (s inv_n alone was a rounding off for two of three values at n = 1000
+// or 28672, which the norm blew up to 0.1).  The mean is held in a scalar
+// register: as a vector one it cost rows of two chunks a place on the CU (8192 x
+// 1111 23.4 us, 22.0 so).
+__device__ __forceinline__ float mean_of(float s, int n, float inv_n) {
+  const float q = s * inv_n;
+  return row::lane_of(fmaf(fmaf(-q, static_cast<float>(n), s), inv_n, q), 0);
+}
+
 // One work-group per row, the row in registers (V chunks of eight values a
 // thread).  y and h are read once, h' and u written once; the statistics are one
 // or two reductions each (a LayerNorm's centred sum of squares follows its mean,
@@ -75,7 +87,7 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) s += WHOLE || k.own(e) ? x[e] : 0.f;
         }
-        mean = row::block_reduce(s, sh1) * inv_n;
+        mean = mean_of(row::block_reduce(s, sh1), n, inv_n);
       }
       float q = 0.f;
 #pragma unroll
@@ -259,7 +271,7 @@ __global__ __launch_bounds__(kAnyThreads) void residual_norm_any_kernel(NormArgs
       if (kind == SIGNROT_NORM_LAYER) {
         float s = 0.f;
         for (int j = tid; j < n; j += kAnyThreads) s += f(j);
-        mean = row::block_reduce(s, sh1) * inv_n;
+        mean = mean_of(row::block_reduce(s, sh1), n, inv_n);
       }
       float q = 0.f;
       for (int j = tid; j < n; j += kAnyThreads) {
