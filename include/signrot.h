@@ -442,6 +442,8 @@ typedef enum { SIGNROT_NORM_NONE = 0, SIGNROT_NORM_RMS = 1, SIGNROT_NORM_LAYER =
  * h' before it is rounded to the stream's type.  All arithmetic is binary32;
  * each output is rounded once.  A row that holds an infinity or NaN gives
  * unspecified outputs in that row only; its code scale is non-finite.
+ * So does a row whose h' or, for LAYER, whose sum passes binary32's range (its
+ * squares may).
  *
  *   tokens, n     rows, and channels of a row: 0 <= tokens < 2^31,
  *                 1 <= n <= 131071.

@@ -5,6 +5,7 @@
 //
 // u stored as bf16 and/or as symmetric per-token INT8 codes.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "internal.h"
@@ -33,6 +34,12 @@ __device__ __forceinline__ float mean_of(float s, int n, float inv_n) {
   const float q = s * inv_n;
   return row::lane_of(fmaf(fmaf(-q, static_cast<float>(n), s), inv_n, q), 0);
 }
+
+// Squares of values around 2^64 and more pass binary32's range, and an infinite
+// sum of them would make every result of a finite row zero.  Such a row's squares
+// are summed again, scaled by this, which keeps the sum below 2^17 (2^129
+// 2^-80)^2; eps (unless it is 2^86 or more) is below a rounding of their mean.
+constexpr float kSmall = 0x1p-80f;
 
 // One work-group per row, the row in registers (V chunks of eight values a
 // thread).  y and h are read once, h' and u written once; the statistics are one
@@ -103,7 +110,26 @@ __global__ __launch_bounds__(1024) void residual_norm_rows_kernel(NormArgs a) {
           q = fmaf(d, d, q);
         }
       }
-      inv = 1.f / sqrtf(row::block_reduce(q, sh2) * inv_n + eps);
+      q = row::block_reduce(q, sh2);
+      inv = 1.f / sqrtf(q * inv_n + eps);
+      if (__builtin_expect(q == INFINITY, 0)) {  // every thread's q
+        __syncthreads();
+        q = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int c = tid + v * step;
+          if (c >= chunks) continue;
+          float x[8];
+          get(v, x);
+          const row::Chunk<WHOLE> k(c, n);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = WHOLE || k.own(e) ? (x[e] - mean) * kSmall : 0.f;
+            q = fmaf(d, d, q);
+          }
+        }
+        inv = kSmall / sqrtf(row::block_reduce(q, sh2) * inv_n);
+      }
     };
     // x = (x - mean) inv w + b on the chunk from element j on
     auto affine = [&](float (&x)[8], int kind, float mean, float inv, const void* w, const void* b, int j) {
@@ -278,7 +304,17 @@ __global__ __launch_bounds__(kAnyThreads) void residual_norm_any_kernel(NormArgs
         const float d = f(j) - mean;
         q = fmaf(d, d, q);
       }
-      inv = 1.f / sqrtf(row::block_reduce(q, sh2) * inv_n + eps);
+      q = row::block_reduce(q, sh2);
+      inv = 1.f / sqrtf(q * inv_n + eps);
+      if (__builtin_expect(q == INFINITY, 0)) {
+        __syncthreads();
+        q = 0.f;
+        for (int j = tid; j < n; j += kAnyThreads) {
+          const float d = (f(j) - mean) * kSmall;
+          q = fmaf(d, d, q);
+        }
+        inv = kSmall / sqrtf(row::block_reduce(q, sh2) * inv_n);
+      }
     };
     auto affine = [&](float v, int kind, float mean, float inv, const void* w, const void* b, int j) {
       if (kind == SIGNROT_NORM_NONE) return v;
