@@ -85,3 +85,69 @@ def test_an_infinity_is_no_overflow(n):
         assert not torch.isfinite(got[2][1])
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 7, 9, 1003, 1024, 4099, 32768, 32776])
+def test_in_place_equals_out_of_place(n, stream):
+    """h_out is h, in rows whose last chunk is moved back over the one before, in
+    kernels that read a row again, and without a reduction (so no barrier) before the
+    first store: bit for bit what a separate output gets."""
+    t = 37
+    g = torch.Generator(device="cuda").manual_seed(n)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+
+    y = normal(t, n).to(torch.bfloat16)
+    gate, weight = normal(n).to(torch.bfloat16), normal(n).to(torch.bfloat16)
+    for ld, off in ((n, 0), (n + 3, 1), ((n + 7) // 8 * 8 + 8, 8)):
+        buf = torch.full((off + t * ld,), 9.0, dtype=stream, device="cuda")
+        h = buf[off:].view(t, ld)[:, :n]
+        start = normal(t, n).to(stream)
+        for branch, post in ((None, "none"), (y, "none"), (y, "rms"), (y, "layer")):
+            kw = {"post_norm": post, "weight": weight, "beta": 0.75, "alpha": 1.25}
+            if branch is not None:
+                kw["gate"] = gate
+            for call in (R.residual_norm, R.residual_norm_quant_int8):
+                h.copy_(start)
+                want = call(h, branch, **kw)
+                assert torch.equal(h, start)
+                got = call(h, branch, h_out=h, **kw)
+                print(f"[gpu] in place {n} {stream} {ld} {post} {call.__name__}", flush=True)
+                assert got[0] is h and all(torch.equal(a, b) for a, b in zip(got, want))
+        keep = torch.ones_like(buf, dtype=torch.bool)
+        keep[off:].view(t, ld)[:, :n] = False
+        assert (buf[keep] == 9).all()
+
+
+@pytest.mark.parametrize("n", [5, 9, 1024])
+def test_more_rows_than_work_groups(n):
+    """A launch has 2^20 work-groups at most; the rows beyond are second ones of some,
+    whose reductions go through the same words."""
+    t = 2 ** 20 + 3
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn((t, n), generator=g, device="cuda").to(torch.bfloat16)
+    y = torch.randn((t, n), generator=g, device="cuda").to(torch.bfloat16)
+    weight = torch.randn(n, generator=g, device="cuda").to(torch.bfloat16)
+    # 700 rows: with up to 512 a thread takes one chunk, whose sums are added in another order
+    parts = (slice(0, 700), slice(2 ** 19, 2 ** 19 + 700), slice(t - 700, t))
+    print(f"[gpu] {t} rows of {n}", flush=True)
+    codes, scale, sums = R.quant_int8(x, sums=True)
+    top = x.float().abs().amax(dim=1)
+    quotient = top.cpu().numpy() / np.float32(127)  # rounded once; torch multiplies by 1 / 127 on the GPU
+    assert np.array_equal(scale.cpu().numpy(), np.where(quotient > 0, quotient, np.float32(1)))
+    assert torch.equal(sums, codes.sum(dim=1, dtype=torch.int32))
+    assert torch.equal(codes.abs().amax(dim=1), (top > 0).to(torch.int8) * 127)
+    for norm in ("rms", "layer"):
+        h, u = R.residual_norm(x, y, norm=norm, weight=weight)
+        h8, codes8, scale8 = R.residual_norm_quant_int8(x, y, norm=norm, weight=weight)
+        assert torch.equal(h, h8)
+        for p in parts:
+            alone = R.residual_norm(x[p], y[p], norm=norm, weight=weight)
+            assert torch.equal(h[p], alone[0]) and torch.equal(u[p], alone[1])
+            alone = R.residual_norm_quant_int8(x[p], y[p], norm=norm, weight=weight)
+            assert torch.equal(codes8[p], alone[1]) and torch.equal(scale8[p], alone[2])
+    for p in parts:
+        alone = R.quant_int8(x[p], sums=True)
+        assert torch.equal(codes[p], alone[0]) and torch.equal(sums[p], alone[2])
