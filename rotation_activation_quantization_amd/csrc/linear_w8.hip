@@ -534,9 +534,10 @@ hipError_t run_tile(const W8Args& a, int splits, hipStream_t s) {
 // The tiles there are, and what they cost: microseconds for 128 of k with one
 // work-group on a CU and with two side by side, and for a tile's start and
 // stores, fitted to 714 timings of 25 shapes (40 x 4096 x 4096 to 8192 x 1024 x
-// 1024; 10 % rms) beside the call's 4 us.  The least estimate picks the fastest
-// of the timed choices or one within 3 % of it, but for 64 x 14336 x 4096 (5 %)
-// and 64 x 28672 x 8192 (11 %); 0.5 % on average.  Both operands of
+// 1024; 10 % rms) beside the call's 4 us.  The least estimate picked the fastest
+// of the timed choices or one within 3 % of it, 0.5 % off on average, but with
+// weights that no cache holds it is further off at 64 x 14336 x 4096 (W8A8 20.6
+// and 18.3 us) and 64 x 28672 x 8192 (53.4 and 49.3).  Both operands of
 // the smaller tiles come a whole 128-byte line a row and step (KU = 2): 512 x
 // 4096 x 4096 took 19.8 us with 64 bytes a step, 13.9 with 128 (12.8 now, see
 // the factors above).
@@ -561,9 +562,17 @@ struct Plan {
 };
 
 // The least estimate over the tiles and over parts of the row joined by a
-// second kernel (3.5 us, and 3.3 TB/s over the partial sums).
+// second kernel (3.5 us, and 3.3 TB/s over the partial sums).  Where the bytes bound
+// several of them their estimates are equal, and the first in the table stays
+// unless another's own work is less by a tenth, the fit's error: W8A8 64 x 128 for
+// 128 x 128 at 33 x 2048 x 28672 (14.5 us, 17.3) and 64 x 14336 x 28672 (78.7,
+// 81.1), 64 x 64 for 64 x 128 in two parts at 64 x 28672 x 8192 (51.9, 70.7), W8A4
+// 256 of k a step for 128 at 64 x 14336 x 14336 (41.2, 45.5).  Of W8A8 choices closer than
+// that the first is the faster one as often as not (64 x 8192 x 5120 14.6 us, the other
+// 16.0; 33 x 13824 x 11008 36.1 and 34.8).
 Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
   Plan best{0, 1, 1e30};
+  double best_work = 1e30;
   const double bytes = static_cast<double>(R) * n + (a4 ? 0.5 : 1.0) * T * n + 2.0 * T * R;
   for (int c = 0; c < 5; ++c) {
     const TileCost& t = a4 ? kTiles4[c] : kTiles8[c];
@@ -574,9 +583,13 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R, bool a4) {
       const double k = n / 128.0 / splits;
       double us = t.fit == 1 ? per_cu * (k * t.one + t.tile)
                              : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
-      us = fmax(us, bytes / 7e6);
-      if (splits > 1) us += 3.5 + tiles * splits * t.bm * t.bn * 4 / 3.3e6;
-      if (us < best.us) best = {c, splits, us};
+      const double join = splits > 1 ? 3.5 + tiles * splits * t.bm * t.bn * 4 / 3.3e6 : 0;
+      const double work = us + join;
+      us = fmax(us, bytes / 7e6) + join;
+      if (us < best.us || (us == best.us && work < 0.9 * best_work)) {
+        best = {c, splits, us};
+        best_work = work;
+      }
     }
   }
   return best;
