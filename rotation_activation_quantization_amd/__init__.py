@@ -188,37 +188,39 @@ def debug_h28():
     return [list(buf[r * 28:(r + 1) * 28]) for r in range(28)]
 
 
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
-def _stream_of(t):
-    """The handle of the current stream on t's device: without the Stream
-    object of the public call (2 us of a small call's 7) where torch has the
-    direct one."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
+def _direct_calls():
+    """torch's look-ups of a device's current stream and of the current device
+    by number, without the objects and checks of the public calls (2 us of a
+    small call's 7) where torch has the direct ones."""
+    global _raw_stream, _current_device
+    import torch
 
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
-    if not t.is_cuda:
-        raise ValueError(f"expected a tensor on a GPU, not on {t.device}")
-    return _raw_stream(t.device.index)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(name, t, *args):
     """Calls the library's function `name` with args and the current stream of
     t's GPU, and with that GPU as the current one: a device's default stream has
     no handle of its own, so it is the current device that the kernel runs on."""
-    import torch
-
-    call, stream, gpu = getattr(lib(), name), _stream_of(t), t.get_device()
-    if gpu == torch.cuda.current_device():
-        status = call(*args, stream)
+    if _raw_stream is None:
+        _direct_calls()
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"expected a tensor on a GPU, not on {t.device}")
+    if gpu == _current_device():
+        status = getattr(lib(), name)(*args, _raw_stream(gpu))
     else:
+        import torch
+
         with torch.cuda.device(gpu):
-            status = call(*args, stream)
-    check(status, name)
+            status = getattr(lib(), name)(*args, _raw_stream(gpu))
+    if status != SIGNROT_OK:
+        check(status, name)
 
 
 def _rows(x):

@@ -86,7 +86,7 @@ def library(monkeypatch):
     recorder = Recorder()
     monkeypatch.setattr(R, "_lib", recorder)
     monkeypatch.setattr(R, "_raw_stream", lambda index: 0x5000 + index)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: recorder.current)
+    monkeypatch.setattr(R, "_current_device", lambda: recorder.current)
     monkeypatch.setattr(torch.cuda, "device", recorder.device)
     return recorder
 
