@@ -1,5 +1,6 @@
 """A transformer block's MLP with 8-bit weights, from the attention's output to
-the next block's normed input, in five launches:
+the next block's normed input, in five launches (a few more at widths without
+the fused SwiGLU):
 
     h', codes = residual_norm_quant_int8(h, attn)        residual sum, RMS norm, INT8 codes
     gate | up = int8_linear(codes, W_gate|up)            one product for both projections

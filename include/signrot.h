@@ -377,7 +377,9 @@ int signrot_quant_int8(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld
  * 1 <= n <= 131071 (an int32 sum cannot overflow); any alignment and stride
  * of codes, w and out.  Rows that are not 16-byte aligned with n a multiple of
  * 16 (32 of packed INT4 codes) cost more; large ones are laid out anew in the
- * workspace first.  tokens == 0 or rows == 0 is a no-op.  Negative
+ * workspace first.  Rows of codes and w are read in words: bytes before and after a row
+ * that lie in one aligned 16-byte chunk with a byte of it may be read too (so no
+ * page but the row's own); their values do not matter.  tokens == 0 or rows == 0 is a no-op.  Negative
  * sizes, tokens or rows >= 2^30, a leading dimension below its row, an unknown
  * out_type, a workspace that is too small or a null pointer ->
  * SIGNROT_EINVAL.  No allocation.  Asynchronous.
@@ -469,7 +471,8 @@ typedef enum { SIGNROT_NORM_NONE = 0, SIGNROT_NORM_RMS = 1, SIGNROT_NORM_LAYER =
  * at all, codes without code_scale or the reverse, an unknown norm or type,
  * a non-finite or negative eps or non-finite alpha or beta, sizes out of
  * range -> SIGNROT_EINVAL.  tokens == 0 is a no-op.  No allocation.
- * Asynchronous.
+ * Asynchronous.  The order of a row's sums is fixed for a number of tokens, and
+ * may be another one for another number.
  */
 typedef struct {
   int64_t tokens, n;

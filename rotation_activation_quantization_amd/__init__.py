@@ -466,7 +466,9 @@ def _on_gpu(v, name):
 
 
 def _empty_codes(t, n, device):
-    """int8 [T, n] in rows of whole 16-byte chunks, which the products read as they are."""
+    """int8 [T, n] in rows that start on 16-byte boundaries.  The products take
+    them as they are where n is a multiple of 16; else they read them through
+    registers, or, when they lay out the weights anew, codes from where they are."""
     import torch
 
     if n % 16 == 0:

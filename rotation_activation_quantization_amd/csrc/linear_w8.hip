@@ -143,8 +143,9 @@ struct Tile {
 // per 16-row group as the first 16 bytes of every row, then the second; a lane
 // reads its 8 bytes there and widens them in registers.
 //
-// 8192 x 14336 x 4096 runs 365 us, 2.6 POP/s (W8A4 382 us), with the MFMAs 58 to
-// 61 % busy.  The clock bounds it: the same instructions on zeros take 285 us.
+// 8192 x 14336 x 4096 runs 359 us, 2.7 POP/s (W8A4 379 us), with the MFMAs 68 %
+// (61 %) busy.  The clock bounds it: the same instructions on zeros take 278 us
+// (300).
 //
 // Slot 16 f + i of a 64-channel group holds channel 16 (i / 4) + 4 f + i % 4:
 // the four 16 x 16 results f = 0 .. 3 then leave a lane sixteen consecutive
@@ -1259,8 +1260,9 @@ hipError_t launch_w8(const W8Args& all, hipStream_t s) {
     a.a = at + k.w_bytes;
     a.lda = pitch;
   }
-  // aligned codes are read to the end of their last 16-byte chunk, which lies in
-  // the page of its first byte; whatever is there meets weights of zero
+  // aligned codes are read to the end of their last 16-byte chunk, up to 15 bytes
+  // past the row (of the last row too) but in the page of the chunk's first byte;
+  // whatever is there meets weights of zero
   a.row_bytes = pitch;
   a.partial = reinterpret_cast<int32_t*>(at + k.w_bytes + k.t_bytes);
   return run_tiles(a, way.plan, s);

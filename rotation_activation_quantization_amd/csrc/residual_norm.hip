@@ -46,7 +46,7 @@ constexpr float kSmall = 0x1p-80f;
 // or two reductions each (a LayerNorm's centred sum of squares follows its mean,
 // so that it cannot cancel).  Many rows are bound by memory: 8192 x 8192 in bf16,
 // RMS, 99 to 106 us, 5.1 to 5.4 TB/s, where a copy reaches 5.2; LayerNorms with
-// modulations take 137, for four reductions and seven rows of parameters from L2.
+// modulations take 144, for four reductions and seven rows of parameters from L2.
 // One row is bound by its latency: 3.7 us at 4096.  Registers decide how many
 // rows a CU holds: a single reduction for mean and variance took twelve more
 // and was slower (106 us at 8192 x 8192).
@@ -397,7 +397,8 @@ void run_rows(const NormArgs& a, dim3 grid, hipStream_t s) {
   // with four, each of which does twice as much: where only the latter takes
   // all rows in one round (2048 x 4096: 15.7 us, 17.9 with two; 1024 x 8192 16.1 and
   // 19.1; 1237 x 5120 14.8 and 15.7; but 1024 x 5120, one round of either, 13.1 and
-  // 12.1).  The binary32 kernel gains nothing (1237 x 5120 22.7 and 22.1).
+  // 12.1).  The binary32 kernel loses (1237 x 5120 with modulations 25.5 us with
+  // four, 23.9 with two; RMS without 19.8 and 18.0).
   if (WHOLE && a.h_type == SIGNROT_BF16 && v == 2) {
     auto places = [&](int chunks_each, int waves) {
       return device_cu_count() * (waves / (row::threads_for(chunks, chunks_each) / 64));
