@@ -151,3 +151,16 @@ def test_more_rows_than_work_groups(n):
     for p in parts:
         alone = R.quant_int8(x[p], sums=True)
         assert torch.equal(codes[p], alone[0]) and torch.equal(sums[p], alone[2])
+
+
+@pytest.mark.parametrize("t,index", [(1, False), (1, True), (6, True)])
+@pytest.mark.parametrize("n", [100, 4096])
+def test_one_modulation_row_of_any_stride_is_the_shared_one(t, index, n):
+    """[1, n] rows, contiguous or cut from a wider projection, give what [n] vectors do."""
+    wide = torch.randn((1, 6 * n), device="cuda").to(torch.bfloat16)
+    h, y = (torch.randn((t, n), device="cuda").to(torch.bfloat16) for _ in range(2))
+    gate, scale, shift = wide[:, :n], wide[:, n:2 * n].clone(), wide[:, 2 * n:3 * n]
+    where = torch.zeros(t, dtype=torch.int32, device="cuda") if index else None
+    got = R.residual_norm(h, y, gate=gate, mod_scale=scale, mod_shift=shift, mod_index=where)
+    want = R.residual_norm(h, y, gate=gate[0], mod_scale=scale[0], mod_shift=shift[0])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
