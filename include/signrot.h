@@ -506,6 +506,190 @@ typedef struct {
 int signrot_residual_norm(const signrot_residual_norm_args* args, void* stream);
 
 /*
+ * Microscaled 4-bit floating point (MXFP4, the OCP microscaling formats' E2M1
+ * elements with E8M0 scales).  A row is cut into blocks of 32 channels.  A
+ * block's scale byte b stands for 2^(b - 127) (255: NaN); a code stands for
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 (its low three bits) with the sign of its high
+ * bit, times the scale.  A row of n channels has nb = ceil(n / 32) blocks: 16
+ * bytes of codes a block (channel 2m in the low nibble of byte m) and one scale
+ * byte.  Channels beyond n in the last block have code 0.
+ *
+ * Choice of a block's scale 2^e, a = max |x| of the block:
+ *   FLOOR   e = floor(log2 a) - 2: a / 2^e in [4, 8), values over 6 saturate.
+ *   NOCLIP  the same, and one more where a > 6 2^e: the least e of which no
+ *           value saturates.
+ * e is kept within [-127, 127]; an all-zero block has e = -127.
+ */
+typedef enum { SIGNROT_MX_FLOOR = 0, SIGNROT_MX_NOCLIP = 1 } signrot_mx_rule;
+
+/*
+ * MXFP4 quantizer: code = x / 2^e rounded to the nearest level, to the even
+ * code at a tie, the sign kept (also of zero).  Exact: the same codes and
+ * scales as the definition in real numbers.  A block that holds an infinity or
+ * NaN gets scale byte 255 and codes 0.
+ *
+ *   x       device, [tokens][ld] of x_type, ld >= n.
+ *   codes   device, [tokens][ldc] uint8, ldc >= 16 nb.
+ *   scale   device, [tokens][lds] uint8, lds >= nb.
+ *
+ * 0 <= tokens < 2^31, 1 <= n <= 131072; any alignment and stride (16-byte
+ * aligned rows with n a multiple of 8 are the fast case).  tokens == 0 is a
+ * no-op.  Sizes out of range, a leading dimension below its row, an unknown
+ * type or rule, a null pointer -> SIGNROT_EINVAL.  No allocation.  Asynchronous.
+ */
+int signrot_quant_mxfp4(const void* x, int x_type, int64_t tokens, int64_t n, int64_t ld, int rule, uint8_t* codes,
+                        int64_t ldc, uint8_t* scale, int64_t lds, void* stream);
+
+/*
+ * The values MXFP4 codes stand for: y [tokens][ldy] of y_type, ldy >= n, the
+ * first n channels of every row.  Exact in either type (2^e level passes
+ * binary32's range, and becomes an infinity, for scale bytes above 252 only).
+ * The other arguments and errors as for signrot_quant_mxfp4.
+ */
+int signrot_dequant_mxfp4(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                          int64_t n, void* y, int y_type, int64_t ldy, void* stream);
+
+/*
+ * The product of MXFP4 operands:
+ *   out[t][k] = sum_j x[t][j] * w[k][j] + bias[k],
+ * x and w the values the codes stand for, both in blocks along j.  The matrix
+ * cores multiply the codes and apply both scales; sums are binary32, and the
+ * result is rounded once to the output type.  The order of the sums is fixed
+ * for given sizes and alignments.  A NaN scale makes the results of its row (of
+ * tokens or weights) NaN.
+ *
+ *   codes, scale      device, [tokens][ldc] and [tokens][lds] uint8.
+ *   w, w_scale        device, [rows][ldw] and [rows][ldws] uint8: row k is
+ *                     output channel k.
+ *   bias              device, [rows] float, or NULL.
+ *   out               device, [tokens][ldo] of out_type, ldo >= rows.
+ *   workspace, workspace_bytes
+ *                     device scratch of at least signrot_mxfp4_linear_workspace
+ *                     bytes (for the same operands), 16-byte aligned; NULL when
+ *                     that is 0.  Its contents are unspecified before and after
+ *                     the call; it must not be used by anything else until the
+ *                     call's work has ended.
+ *
+ * n a multiple of 32 (whole blocks), 32 <= n <= 131072; tokens and rows below
+ * 2^30; any alignment and stride (code rows on 16-byte boundaries and scale rows
+ * on 4-byte ones are the fast case; others are laid out anew in the workspace).
+ * Scale rows are read in aligned words of four: bytes of the word that holds a
+ * row's last scale may be read too; their values do not matter.  tokens == 0 or
+ * rows == 0 is a no-op.  Negative sizes, a leading dimension below its row, an
+ * unknown out_type, a workspace that is too small or a null pointer ->
+ * SIGNROT_EINVAL.  No allocation.  Asynchronous.
+ */
+int signrot_mxfp4_linear(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                         int64_t n, const uint8_t* w, int64_t ldw, const uint8_t* w_scale, int64_t ldws,
+                         const float* bias, int64_t rows, void* out, int64_t ldo, int out_type, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Scratch bytes of the product for these operands (0: none, the pointer may be
+ * NULL), or -1 when the sizes are invalid, and the kernel it would launch (a
+ * static string; NULL when the sizes are invalid).  They depend on the sizes
+ * and on the alignment of the pointers and strides.  Host-only. */
+int64_t signrot_mxfp4_linear_workspace(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds,
+                                       int64_t tokens, int64_t n, const uint8_t* w, int64_t ldw,
+                                       const uint8_t* w_scale, int64_t ldws, int64_t rows);
+const char* signrot_mxfp4_linear_kernel_name(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds,
+                                             int64_t tokens, int64_t n, const uint8_t* w, int64_t ldw,
+                                             const uint8_t* w_scale, int64_t ldws, int64_t rows);
+
+/*
+ * The rotation and sign flip of signrot_rotate_quant_int4_outlier (d = sigma *
+ * row c of H) with MXFP4 output: the codes and scales that signrot_quant_mxfp4
+ * gives of y = (x.H / sqrt(n)) * d in binary32 (the y_out of that call).
+ *
+ *   x_bf16, tokens, n, ld, c, sigma   as for signrot_rotate_quant_int4_outlier.
+ *   rule, codes, ldc, scale, lds      as for signrot_quant_mxfp4; codes 16-byte
+ *                     aligned and ldc a multiple of 16.
+ *   workspace, workspace_bytes        device scratch of at least
+ *                     signrot_rotate_quant_mxfp4_workspace(tokens, n) bytes,
+ *                     16-byte aligned (as for the product): 0 at the widths of
+ *                     the fused kernels (signrot_kernel_name "rq_mfma..."), the
+ *                     rotated rows at the others.
+ *
+ * Any supported n; errors as for the two calls.  Asynchronous.  No allocation
+ * beyond signrot_rotate_quant_int4_outlier's own.
+ */
+int signrot_rotate_quant_mxfp4(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, int64_t c, int sigma,
+                               int rule, uint8_t* codes, int64_t ldc, uint8_t* scale, int64_t lds, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+int64_t signrot_rotate_quant_mxfp4_workspace(int64_t tokens, int64_t n);
+
+/*
+ * The same on x = bf16(SiLU(gate) * up), the producer fused in, as
+ * signrot_swiglu_rotate_quant_int4 (gate and up with one stride ld; the widths
+ * of the fused kernels only).
+ */
+int signrot_swiglu_rotate_quant_mxfp4(const void* gate_bf16, const void* up_bf16, int64_t tokens, int64_t n, int64_t ld,
+                                      int64_t c, int sigma, int rule, uint8_t* codes, int64_t ldc, uint8_t* scale,
+                                      int64_t lds, void* stream);
+
+/*
+ * The norm of each head of the queries and keys and their rotation by the
+ * token's position, in one pass.  Per token t and head, v = Norm(x) over the
+ * head's channels (signrot_norm, with weight and bias; the same norm for
+ * queries and keys), then for each pair p < rotary / 2 of its first `rotary`
+ * channels, (a, b) = channels (p, p + rotary / 2), or (2p, 2p + 1) when
+ * interleaved:
+ *   a' = a cos[r][p] - b sin[r][p],   b' = b cos[r][p] + a sin[r][p],
+ * r = positions[t] (clamped into [0, places)), or t when positions is NULL.
+ * Channels from `rotary` on are normed only.  All arithmetic is binary32; each
+ * result is rounded once.  A head that holds an infinity or NaN gives
+ * unspecified results in that head only; so does one whose sum, for LAYER,
+ * passes binary32's range (its squares may).
+ *
+ *   tokens, head, rotary   0 <= tokens < 2^31; channels of a head, even, in
+ *                 [8, 512]; rotated channels, even, in [0, head].
+ *   q, ldq, hsq   device, in_type: channel j of head h of token t at
+ *                 q[t * ldq + h * hsq + j]; strides in elements, any sign-free
+ *                 order of tokens and heads (each >= 0).
+ *   q_out, ldqo, hsqo   device, out_type, the same; may be q itself (same
+ *                 pointer, strides and type); may not overlap q or k otherwise,
+ *                 and its rows may not overlap each other.
+ *   k, k_out, ... the same for the keys; NULL with k_heads 0: no keys.
+ *   q_heads, k_heads   heads of a token, in [1, 65536] and [0, 65536].
+ *   cos, sin, ldt, places   device, [places][ldt] float, ldt >= rotary / 2;
+ *                 may be NULL when rotary is 0.
+ *   positions     device, [tokens] int32 (positions_64 0) or int64 (1), or NULL
+ *                 (places >= tokens then).
+ *   q_weight, k_weight, q_bias, k_bias   device, [head] of param_type, each may
+ *                 be NULL (weight 1, bias 0); not applied with NORM_NONE.
+ *
+ * Any alignment (16-byte aligned heads of a multiple of 8 channels are the fast
+ * case).  tokens == 0 is a no-op.  Sizes out of range, an unknown norm or type,
+ * a negative or non-finite eps, a null pointer -> SIGNROT_EINVAL.  No
+ * allocation.  Asynchronous.
+ */
+typedef struct {
+  int64_t tokens, head, rotary;
+  const void* q;
+  int64_t ldq, hsq;
+  void* q_out;
+  int64_t ldqo, hsqo;
+  const void* k;
+  int64_t ldk, hsk;
+  void* k_out;
+  int64_t ldko, hsko;
+  const float* cos;
+  const float* sin;
+  int64_t ldt, places;
+  const void* positions;
+  const void* q_weight;
+  const void* k_weight;
+  const void* q_bias;
+  const void* k_bias;
+  int32_t q_heads, k_heads;
+  float eps;
+  int32_t norm;                             /* signrot_norm */
+  int32_t interleaved, positions_64;        /* 0 or 1 */
+  int32_t in_type, out_type, param_type;    /* signrot_type */
+} signrot_qk_norm_rope_args;
+
+int signrot_qk_norm_rope(const signrot_qk_norm_rope_args* args, void* stream);
+
+/*
  * Measurement aid, not part of the method: a kernel that moves the bytes the
  * online path moves per token -- reads the bf16 row (2n bytes), writes n/2
  * bytes to out [tokens][n/2] and one float each to s0 [tokens] and

@@ -83,6 +83,25 @@ def lib() -> ctypes.CDLL:
     L.signrot_int4_w8_linear_kernel_name.restype = ctypes.c_char_p
     L.signrot_residual_norm.argtypes = [vp, vp]
     L.signrot_residual_norm.restype = ctypes.c_int
+    ci = ctypes.c_int
+    L.signrot_quant_mxfp4.argtypes = [vp, ci, i64, i64, i64, ci, vp, i64, vp, i64, vp]
+    L.signrot_quant_mxfp4.restype = ci
+    L.signrot_dequant_mxfp4.argtypes = [vp, i64, vp, i64, i64, i64, vp, ci, i64, vp]
+    L.signrot_dequant_mxfp4.restype = ci
+    L.signrot_mxfp4_linear.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, i64, vp]
+    L.signrot_mxfp4_linear.restype = ci
+    L.signrot_mxfp4_linear_workspace.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64]
+    L.signrot_mxfp4_linear_workspace.restype = i64
+    L.signrot_mxfp4_linear_kernel_name.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64]
+    L.signrot_mxfp4_linear_kernel_name.restype = ctypes.c_char_p
+    L.signrot_rotate_quant_mxfp4.argtypes = [vp, i64, i64, i64, i64, ci, ci, vp, i64, vp, i64, vp, i64, vp]
+    L.signrot_rotate_quant_mxfp4.restype = ci
+    L.signrot_rotate_quant_mxfp4_workspace.argtypes = [i64, i64]
+    L.signrot_rotate_quant_mxfp4_workspace.restype = i64
+    L.signrot_swiglu_rotate_quant_mxfp4.argtypes = [vp, vp, i64, i64, i64, i64, ci, ci, vp, i64, vp, i64, vp]
+    L.signrot_swiglu_rotate_quant_mxfp4.restype = ci
+    L.signrot_qk_norm_rope.argtypes = [vp, vp]
+    L.signrot_qk_norm_rope.restype = ci
     L.signrot_stream_ceiling.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
     L.signrot_stream_ceiling.restype = ctypes.c_int
     L.signrot_strerror.argtypes = [ctypes.c_int]
@@ -126,6 +145,15 @@ EXPORTED = (
     "signrot_int4_w8_linear_workspace",
     "signrot_int4_w8_linear_kernel_name",
     "signrot_residual_norm",
+    "signrot_quant_mxfp4",
+    "signrot_dequant_mxfp4",
+    "signrot_mxfp4_linear",
+    "signrot_mxfp4_linear_workspace",
+    "signrot_mxfp4_linear_kernel_name",
+    "signrot_rotate_quant_mxfp4",
+    "signrot_rotate_quant_mxfp4_workspace",
+    "signrot_swiglu_rotate_quant_mxfp4",
+    "signrot_qk_norm_rope",
     "signrot_strerror",
     "signrot_last_error",
     "signrot_debug_h28",
@@ -722,6 +750,268 @@ def signrot_residual_norm_quant_int8(h, y=None, norm: str = "rms", post_norm: st
     return h_out, codes, scale
 
 
+# ---- microscaled 4-bit floating point (MXFP4) --------------------------------
+
+_MX_RULES = {"floor": 0, "noclip": 1}
+
+
+def _mx_rule(rule):
+    if rule not in _MX_RULES:
+        raise ValueError(f"rule must be one of {sorted(_MX_RULES)}")
+    return _MX_RULES[rule]
+
+
+def _mx_out(out, t, n, device, gpu):
+    """(out, codes pointer, its row stride, scales pointer, their row stride) of the codes and scales of [T, n]
+    values; allocated ones have rows of scales that start on 16-byte boundaries."""
+    import torch
+
+    nb = (n + 31) // 32
+    if out is None:
+        pitch = (nb + 15) // 16 * 16
+        codes = torch.empty(t, 16 * nb, dtype=torch.uint8, device=device)
+        scale = torch.empty(t, pitch, dtype=torch.uint8, device=device)
+        return (codes, scale if pitch == nb else scale[:, :nb]), codes.data_ptr(), 16 * nb, scale.data_ptr(), pitch
+    codes, scale = out
+    qptr, ldc = _matrix(codes, "codes", t, 16 * nb, torch.uint8, gpu)
+    sptr, lds = _matrix(scale, "scale", t, nb, torch.uint8, gpu)
+    return (codes, scale), qptr, ldc, sptr, lds
+
+
+def _mx_operand(codes, scale, names, gpu):
+    """(codes pointer, stride, scales pointer, stride, blocks of a row) of an MXFP4 operand."""
+    import torch
+
+    qptr, ldc = _matrix(codes, names[0], None, None, torch.uint8, gpu)
+    rows, size = codes.shape
+    if size % 16 != 0:
+        raise ValueError(f"{names[0]} rows hold {size} bytes, not whole blocks of 16")
+    sptr, lds = _matrix(scale, names[1], rows, size // 16, torch.uint8, gpu)
+    return qptr, ldc, sptr, lds, size // 16
+
+
+def signrot_quant_mxfp4(x, rule: str = "floor", out=None):
+    """bf16 or f32 [T, n] -> (codes u8 [T, 16 nb], scale u8 [T, nb]), nb =
+    ceil(n / 32): MXFP4 in blocks of 32 channels along a row, channel 2m in the
+    low nibble of byte m, codes beyond n zero, scales 2^(byte - 127) (255: the
+    block holds an infinity or NaN).  rule "floor": the scale's exponent is
+    floor(log2 max|x|) - 2 and values over 6 scales saturate; "noclip": one more
+    where the largest would.  Rows of scales start on 16-byte boundaries (a view
+    of wider rows where nb is no multiple of 16).  `out` may pass preallocated
+    (codes, scale)."""
+    device, gpu = _on_gpu(x, "x")
+    kind = _type_of(x.dtype, "x")
+    ptr, ld = _matrix(x, "x", None, None, x.dtype, gpu)
+    t, n = x.shape
+    out, qptr, ldc, sptr, lds = _mx_out(out, t, n, device, gpu)
+    _run("signrot_quant_mxfp4", x, ptr, kind, t, n, ld, _mx_rule(rule), qptr, ldc, sptr, lds)
+    return out
+
+
+def signrot_dequant_mxfp4(codes, scale, n: int | None = None, dtype=None, out=None):
+    """The values of MXFP4 codes and scales, [T, n] (n: all channels of the
+    blocks) of `dtype` (float32, the default, or bfloat16), exact.  `out` may
+    pass the result's tensor."""
+    import torch
+
+    device, gpu = _on_gpu(codes, "codes")
+    qptr, ldc, sptr, lds, nb = _mx_operand(codes, scale, ("codes", "scale"), gpu)
+    t = codes.shape[0]
+    n = 32 * nb if n is None else int(n)
+    if (n + 31) // 32 != nb:
+        raise ValueError(f"codes hold {nb} blocks of 32 channels, not {n} channels")
+    if out is None and dtype is None:
+        dtype = torch.float32
+    out, kind, optr, ldo = _product_out(out, dtype, t, n, device, gpu)
+    _run("signrot_dequant_mxfp4", codes, qptr, ldc, sptr, lds, t, n, optr, kind, ldo)
+    return out
+
+
+def signrot_mxfp4_linear(codes, scale, w, w_scale, bias=None, dtype=None, out=None):
+    """MXFP4 activations (codes u8 [T, 16 nb], scale u8 [T, nb]) times MXFP4
+    weights (w u8 [rows, 16 nb], w_scale u8 [rows, nb]) -> [T, rows] of `dtype`
+    (bfloat16, the default, or float32), plus bias f32 [rows].  Sums in binary32
+    on the matrix cores, which apply the scales.  `out` may pass the result's
+    tensor."""
+    device, gpu = _on_gpu(codes, "codes")
+    aptr, lda, sptr, lds, nb = _mx_operand(codes, scale, ("codes", "scale"), gpu)
+    wptr, ldw, vptr, ldws, wb = _mx_operand(w, w_scale, ("w", "w_scale"), gpu)
+    if wb != nb:
+        raise ValueError(f"codes hold {nb} blocks of 32 channels, w {wb}")
+    t, rows = codes.shape[0], w.shape[0]
+    import torch
+
+    bptr = _vector(bias, "bias", rows, torch.float32, gpu)
+    out, kind, optr, ldo = _product_out(out, dtype, t, rows, device, gpu)
+    sizes = (aptr, lda, sptr, lds, t, 32 * nb, wptr, ldw, vptr, ldws)
+    ws, size, _owner = _workspace(lib().signrot_mxfp4_linear_workspace(*sizes, rows), device)
+    _run("signrot_mxfp4_linear", codes, *sizes, bptr, rows, optr, ldo, kind, ws, size)
+    return out
+
+
+def mxfp4_linear_kernel_name(codes, scale, w, w_scale) -> str | None:
+    gpu = codes.get_device()
+    aptr, lda, sptr, lds, nb = _mx_operand(codes, scale, ("codes", "scale"), gpu)
+    wptr, ldw, vptr, ldws, _ = _mx_operand(w, w_scale, ("w", "w_scale"), gpu)
+    r = lib().signrot_mxfp4_linear_kernel_name(aptr, lda, sptr, lds, codes.shape[0], 32 * nb, wptr, ldw, vptr, ldws,
+                                               w.shape[0])
+    return r.decode() if r else None
+
+
+def signrot_rotate_quant_mxfp4(x, c: int, sigma: int, rule: str = "floor", out=None):
+    """bf16 [T, n] -> MXFP4 (codes, scale) of its rotation y = (x H / sqrt n) * d,
+    d = sigma * (row c of H) (what signrot_calibrate returns): what
+    signrot_quant_mxfp4 gives of the binary32 y.  `out` may pass preallocated
+    (codes, scale), codes rows on 16-byte boundaries."""
+    device, gpu = _on_gpu(x, "x")
+    ptr, t, n, ld = _rows(x)
+    size = lib().signrot_rotate_quant_mxfp4_workspace(t, n)
+    if size < 0:
+        check(SIGNROT_EUNSUPPORTED_N, "signrot_rotate_quant_mxfp4")
+    out, qptr, ldc, sptr, lds = _mx_out(out, t, n, device, gpu)
+    ws, size, _owner = _workspace(size, device)
+    _run("signrot_rotate_quant_mxfp4", x, ptr, t, n, ld, int(c), int(sigma), _mx_rule(rule), qptr, ldc, sptr, lds, ws,
+         size)
+    return out
+
+
+def signrot_swiglu_rotate_quant_mxfp4(gate, up, c: int, sigma: int, rule: str = "floor", out=None):
+    """signrot_rotate_quant_mxfp4 of x = bf16(SiLU(gate) * up), the producer
+    fused in: gate and up bf16 [T, n] with the same row stride, n one of the
+    fused kernels' widths."""
+    device, gpu = _on_gpu(gate, "gate")
+    ptr, t, n, ld = _rows(gate)
+    uptr, tu, nu, ldu = _rows(up)
+    if (tu, nu) != (t, n) or (t > 1 and ldu != ld) or up.get_device() != gpu:
+        raise ValueError("gate and up must have the same shape, row stride and GPU")
+    out, qptr, ldc, sptr, lds = _mx_out(out, t, n, device, gpu)
+    _run("signrot_swiglu_rotate_quant_mxfp4", gate, ptr, uptr, t, n, ld, int(c), int(sigma), _mx_rule(rule), qptr, ldc,
+         sptr, lds)
+    return out
+
+
+# ---- the norm of each head and the position rotation --------------------------
+
+
+class _QkNormRopeArgs(ctypes.Structure):
+    """signrot_qk_norm_rope_args."""
+
+    _fields_ = [(name, kind) for names, kind in (
+        (("tokens", "head", "rotary"), ctypes.c_int64),
+        (("q",), ctypes.c_void_p), (("ldq", "hsq"), ctypes.c_int64),
+        (("q_out",), ctypes.c_void_p), (("ldqo", "hsqo"), ctypes.c_int64),
+        (("k",), ctypes.c_void_p), (("ldk", "hsk"), ctypes.c_int64),
+        (("k_out",), ctypes.c_void_p), (("ldko", "hsko"), ctypes.c_int64),
+        (("cos", "sin"), ctypes.c_void_p), (("ldt", "places"), ctypes.c_int64),
+        (("positions", "q_weight", "k_weight", "q_bias", "k_bias"), ctypes.c_void_p),
+        (("q_heads", "k_heads"), ctypes.c_int32), (("eps",), ctypes.c_float),
+        (("norm", "interleaved", "positions_64", "in_type", "out_type", "param_type"), ctypes.c_int32))
+        for name in names]
+
+
+_pack_qk_args = struct.Struct("@" + "".join(
+    {ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f", ctypes.c_int32: "i"}[kind]
+    for _, kind in _QkNormRopeArgs._fields_) + "0q").pack  # the struct's size is a multiple of eight
+
+
+def _heads_of(v, name, t, heads, d, dtype, gpu):
+    """(pointer, token stride, head stride) of a [T, heads, d] tensor with contiguous heads; None sizes are free."""
+    shape = v.shape
+    if v.dtype is not dtype or len(shape) != 3 or v.get_device() != gpu:
+        raise ValueError(f"{name} must be a 3-D {dtype} tensor on GPU {gpu}")
+    if (t is not None and shape[0] != t) or (heads is not None and shape[1] != heads) or (
+            d is not None and shape[2] != d):
+        raise ValueError(f"{name} has shape {tuple(shape)}, not "
+                         f"[{'*' if t is None else t}, {'*' if heads is None else heads}, {'*' if d is None else d}]")
+    step, hop, unit = v.stride()
+    if unit != 1:
+        raise ValueError(f"{name} heads must be contiguous")
+    return v.data_ptr(), step, hop
+
+
+def _heads_out(v, name, like, dtype, gpu):
+    """(out, pointer, strides) of the result for the [T, heads, d] tensor `like`, allocated when v is None."""
+    import torch
+
+    t, heads, d = like.shape
+    if v is None:
+        v = torch.empty(t, heads, d, dtype=dtype, device=like.device)
+        return v, v.data_ptr(), heads * d, d
+    ptr, step, hop = _heads_of(v, name, t, heads, d, dtype, gpu)
+    reach = d  # elements of the axes so far: the next one has to step over them
+    for stride, count in sorted(((hop, heads), (step, t))):
+        if count > 1:
+            if stride < reach:
+                raise ValueError(f"{name} heads overlap")
+            reach += stride * (count - 1)
+    return v, ptr, step, hop
+
+
+def signrot_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, norm: str = "rms", eps: float = 1e-6,
+                         q_weight=None, k_weight=None, q_bias=None, k_bias=None, interleaved: bool = False, dtype=None,
+                         q_out=None, k_out=None):
+    """The norm of each head of the queries and keys, then the rotation of its
+    first 2 R channels by the token's position, in one pass:
+
+        v = Norm(x);  a' = a cos[p] - b sin[p],  b' = b cos[p] + a sin[p]
+
+    q [T, heads, D] and k [T, kv_heads, D] (or None) are bf16 or f32, of any
+    token and head stride, D even in [8, 512]; cos and sin are f32 [places, R]
+    (None: no rotation), read at row positions[t] (int32 or int64 [T], clamped
+    into the table) or t; the pair p is channels (p, p + R), or (2p, 2p + 1) when
+    interleaved.  norm is "rms", "layer" or "none", weights and biases [D], all
+    bf16 or all f32.  Returns (q', k') of `dtype` (default: the input's); q_out
+    and k_out may pass their tensors, among them q and k themselves."""
+    import torch
+
+    device, gpu = _on_gpu(q, "q")
+    in_type = _type_of(q.dtype, "q")
+    qptr, ldq, hsq = _heads_of(q, "q", None, None, None, q.dtype, gpu)
+    t, heads, d = q.shape
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}")
+    for v in (q_out, k_out):
+        if v is not None:
+            if dtype is not None and v.dtype is not dtype:
+                raise ValueError(f"an output is {v.dtype}, dtype {dtype}")
+            dtype = v.dtype
+    dtype = q.dtype if dtype is None else dtype
+    out_type = _type_of(dtype, "the result")
+    param = torch.bfloat16
+    for v in (q_weight, k_weight, q_bias, k_bias):
+        if v is not None:
+            param = v.dtype
+            break
+    p_type = _type_of(param, "the norm's parameters")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    cptr = zptr = pptr = ldt = places = rotary = wide = 0
+    if cos is not None:
+        cptr, ldt = _matrix(cos, "cos", None, None, torch.float32, gpu)
+        places, rotary = cos.shape[0], 2 * cos.shape[1]
+        zptr, lds = _matrix(sin, "sin", places, cos.shape[1], torch.float32, gpu)
+        if places > 1 and ldt != lds:
+            raise ValueError("cos and sin must have the same row stride")
+        if positions is not None:
+            wide = positions.dtype is torch.int64
+            pptr = _vector(positions, "positions", t, torch.int64 if wide else torch.int32, gpu)
+    kptr = ldk = hsk = koptr = ldko = hsko = kv = 0
+    q_out, qoptr, ldqo, hsqo = _heads_out(q_out, "q_out", q, dtype, gpu)
+    if k is not None:
+        kptr, ldk, hsk = _heads_of(k, "k", t, None, d, q.dtype, gpu)
+        kv = k.shape[1]
+        k_out, koptr, ldko, hsko = _heads_out(k_out, "k_out", k, dtype, gpu)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    args = _pack_qk_args(
+        t, d, rotary, qptr, ldq, hsq, qoptr, ldqo, hsqo, kptr, ldk, hsk, koptr, ldko, hsko, cptr, zptr, ldt, places,
+        pptr, _vector(q_weight, "q_weight", d, param, gpu), _vector(k_weight, "k_weight", d, param, gpu),
+        _vector(q_bias, "q_bias", d, param, gpu), _vector(k_bias, "k_bias", d, param, gpu), heads, kv, eps,
+        _NORMS[norm], 1 if interleaved else 0, 1 if wide else 0, in_type, out_type, p_type)
+    _run("signrot_qk_norm_rope", q, args)
+    return q_out, k_out
+
+
 def signrot_stream_ceiling(x, out=None):
     """The memory-traffic ceiling kernel (a measurement aid: the online path's
     bytes per token, no arithmetic) on bf16 [T, n] -> (u8 [T, n/2], f32 [T],
@@ -752,3 +1042,9 @@ int8_linear = signrot_int8_linear
 int4_w8_linear = signrot_int4_w8_linear
 residual_norm = signrot_residual_norm
 residual_norm_quant_int8 = signrot_residual_norm_quant_int8
+quant_mxfp4 = signrot_quant_mxfp4
+dequant_mxfp4 = signrot_dequant_mxfp4
+mxfp4_linear = signrot_mxfp4_linear
+rotate_quant_mxfp4 = signrot_rotate_quant_mxfp4
+swiglu_rotate_quant_mxfp4 = signrot_swiglu_rotate_quant_mxfp4
+qk_norm_rope = signrot_qk_norm_rope

@@ -32,6 +32,9 @@ SOURCES = [
     "linear_w8.hip",
     "quant_int8.hip",
     "residual_norm.hip",
+    "quant_mx.hip",
+    "linear_mx.hip",
+    "qk_norm_rope.hip",
     "hadamard28.cpp",
     "outer.cpp",
 ]

@@ -399,9 +399,16 @@ int signrot_rotate_quant_int4(const void* x_bf16, int64_t tokens, int64_t n, int
 }  // extern "C"
 
 namespace {
+// MXFP4 output of the fused rotate kernels: `codes` is then [tokens][ldc].
+struct MxOut {
+  uint8_t* scale;
+  int64_t ldc, lds;
+  int noclip;
+};
+
 int rotate_quant_outlier_impl(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, int64_t c, int sigma,
                               uint8_t* codes, float* scale, float* zero, float* y_out, int zint, void* stream,
-                              const void* up_bf16 = nullptr) {
+                              const void* up_bf16 = nullptr, const MxOut* mx = nullptr) {
   g_last_error[0] = '\0';
   const Shape sh = factor_n(n);
   if (!sh.ok) {
@@ -420,7 +427,7 @@ int rotate_quant_outlier_impl(const void* x_bf16, int64_t tokens, int64_t n, int
   if (ld & 7) return fail_einval("ld must be a multiple of 8");
   if (tokens == 0) return SIGNROT_OK;
   if (tokens > (int64_t{1} << 40)) return fail_einval("tokens too large");
-  if (!x_bf16 || !codes || !scale || !zero) return fail_einval("null device pointer");
+  if (!x_bf16 || !codes || (mx ? !mx->scale : !scale || !zero)) return fail_einval("null device pointer");
   if (!aligned16(x_bf16)) return fail_einval("x must be 16-byte aligned");
   if (!aligned16(codes)) return fail_einval("codes must be 16-byte aligned");
   if (y_out && !aligned16(y_out)) return fail_einval("y_out must be 16-byte aligned");
@@ -444,6 +451,12 @@ int rotate_quant_outlier_impl(const void* x_bf16, int64_t tokens, int64_t n, int
   a.form_c = static_cast<int>(c);
   a.form_neg = sigma < 0 ? 1 : 0;
   a.zint = zint;
+  if (mx) {
+    a.mx_scale = mx->scale;
+    a.mx_lds = mx->lds;
+    a.mx_ldc = mx->ldc;
+    a.mx_noclip = mx->noclip;
+  }
   for (int i = 0; i < 28; ++i) a.h28mask[i] = h28().rowmask[i];
   {
     const hipError_t he = set_outer_tables(a, sh, static_cast<hipStream_t>(stream));
@@ -803,6 +816,241 @@ int signrot_residual_norm(const signrot_residual_norm_args* args, void* stream) 
   const hipError_t e = launch_residual_norm(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, "residual_norm launch");
   return SIGNROT_OK;
+}
+
+namespace {
+int mx_rows(int64_t tokens, int64_t n, int64_t ldc, int64_t lds) {
+  if (tokens < 0 || tokens >= (int64_t{1} << 31)) return fail_einval("tokens must be in [0, 2^31)");
+  if (n < 1 || n > kMxMaxN) return fail_einval("n must be in [1, 131072]");
+  const int64_t nb = (n + 31) / 32;
+  if (ldc < 16 * nb || lds < nb) return fail_einval("ldc must be >= 16 ceil(n / 32) and lds >= ceil(n / 32)");
+  return SIGNROT_OK;
+}
+bool known_type(int type) { return type == SIGNROT_F32 || type == SIGNROT_BF16; }
+bool misaligned(const void* p, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & (type == SIGNROT_F32 ? 3u : 1u)) != 0;
+}
+}  // namespace
+
+int signrot_quant_mxfp4(const void* x, int x_type, int64_t tokens, int64_t n, int64_t ld, int rule, uint8_t* codes,
+                        int64_t ldc, uint8_t* scale, int64_t lds, void* stream) {
+  g_last_error[0] = '\0';
+  const int st = mx_rows(tokens, n, ldc, lds);
+  if (st != SIGNROT_OK) return st;
+  if (!known_type(x_type)) return fail_einval("unknown x_type");
+  if (rule != SIGNROT_MX_FLOOR && rule != SIGNROT_MX_NOCLIP) return fail_einval("unknown rule");
+  if (ld < n) return fail_einval("ld < n");
+  if (tokens == 0) return SIGNROT_OK;
+  if (!x || !codes || !scale) return fail_einval("null device pointer");
+  if (misaligned(x, x_type)) return fail_einval("a pointer is not aligned to its type");
+  const hipError_t e = launch_quant_mx(x, x_type == SIGNROT_BF16, tokens, static_cast<int>(n), ld, codes, ldc, scale,
+                                       lds, rule == SIGNROT_MX_NOCLIP, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "quant_mxfp4 launch");
+  return SIGNROT_OK;
+}
+
+int signrot_dequant_mxfp4(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                          int64_t n, void* y, int y_type, int64_t ldy, void* stream) {
+  g_last_error[0] = '\0';
+  const int st = mx_rows(tokens, n, ldc, lds);
+  if (st != SIGNROT_OK) return st;
+  if (!known_type(y_type)) return fail_einval("unknown y_type");
+  if (ldy < n) return fail_einval("ldy < n");
+  if (tokens == 0) return SIGNROT_OK;
+  if (!codes || !scale || !y) return fail_einval("null device pointer");
+  if (misaligned(y, y_type)) return fail_einval("a pointer is not aligned to its type");
+  const hipError_t e = launch_dequant_mx(codes, ldc, scale, lds, tokens, static_cast<int>(n), y, ldy,
+                                         y_type == SIGNROT_BF16, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "dequant_mxfp4 launch");
+  return SIGNROT_OK;
+}
+
+namespace {
+// Sizes and operands of the MXFP4 product, shared by the call and its host-only
+// helpers.
+int mx_operands(MxArgs& a, const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                int64_t n, const uint8_t* w, int64_t ldw, const uint8_t* w_scale, int64_t ldws, int64_t rows) {
+  if (tokens < 0 || rows < 0 || tokens >= (int64_t{1} << 30) || rows >= (int64_t{1} << 30))
+    return fail_einval("tokens and rows must be in [0, 2^30)");  // the kernels round them up to tiles in int
+  if (n < 32 || n > kMxMaxN || n % 32 != 0) return fail_einval("n must be a multiple of 32 in [32, 131072]");
+  if (ldc < n / 2 || ldw < n / 2) return fail_einval("ldc and ldw must be >= n / 2");
+  if (lds < n / 32 || ldws < n / 32) return fail_einval("lds and ldws must be >= n / 32");
+  memset(&a, 0, sizeof(a));
+  a.a = codes;
+  a.lda = ldc;
+  a.scale = scale;
+  a.lds = lds;
+  a.w = w;
+  a.ldw = ldw;
+  a.w_scale = w_scale;
+  a.ldws = ldws;
+  a.T = static_cast<int>(tokens);
+  a.R = static_cast<int>(rows);
+  a.n = static_cast<int>(n);
+  return SIGNROT_OK;
+}
+}  // namespace
+
+int signrot_mxfp4_linear(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                         int64_t n, const uint8_t* w, int64_t ldw, const uint8_t* w_scale, int64_t ldws,
+                         const float* bias, int64_t rows, void* out, int64_t ldo, int out_type, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  MxArgs a;
+  const int st = mx_operands(a, codes, ldc, scale, lds, tokens, n, w, ldw, w_scale, ldws, rows);
+  if (st != SIGNROT_OK) return st;
+  if (ldo < rows) return fail_einval("ldo < rows");
+  if (!known_type(out_type)) return fail_einval("unknown out_type");
+  if (tokens == 0 || rows == 0) return SIGNROT_OK;
+  if (!codes || !scale || !w || !w_scale || !out) return fail_einval("null device pointer");
+  if (misaligned(bias, SIGNROT_F32) || misaligned(out, out_type))
+    return fail_einval("a pointer is not aligned to its type");
+  a.bias = bias;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_bf16 = out_type == SIGNROT_BF16;
+  const int64_t need = mx_workspace(a);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return fail_einval("workspace too small");
+    if (!aligned16(workspace)) return fail_einval("workspace must be 16-byte aligned");
+  }
+  a.workspace = static_cast<uint8_t*>(workspace);
+  const hipError_t e = launch_mx(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "mxfp4_linear launch");
+  return SIGNROT_OK;
+}
+
+int64_t signrot_mxfp4_linear_workspace(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds,
+                                       int64_t tokens, int64_t n, const uint8_t* w, int64_t ldw,
+                                       const uint8_t* w_scale, int64_t ldws, int64_t rows) {
+  g_last_error[0] = '\0';
+  MxArgs a;
+  return mx_operands(a, codes, ldc, scale, lds, tokens, n, w, ldw, w_scale, ldws, rows) == SIGNROT_OK ? mx_workspace(a)
+                                                                                                      : -1;
+}
+
+const char* signrot_mxfp4_linear_kernel_name(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds,
+                                             int64_t tokens, int64_t n, const uint8_t* w, int64_t ldw,
+                                             const uint8_t* w_scale, int64_t ldws, int64_t rows) {
+  g_last_error[0] = '\0';
+  MxArgs a;
+  return mx_operands(a, codes, ldc, scale, lds, tokens, n, w, ldw, w_scale, ldws, rows) == SIGNROT_OK ? mx_name(a)
+                                                                                                      : nullptr;
+}
+
+namespace {
+// Scratch of the rotation to MXFP4 at widths without a fused kernel: the
+// rotated rows, the INT4 codes that come with them, their scales and zeros.
+int64_t rotate_mx_scratch(int64_t tokens, int64_t n, int64_t& codes, int64_t& factors) {
+  codes = (4 * tokens * n + 15) & ~int64_t{15};
+  factors = codes + ((tokens * (n / 2) + 15) & ~int64_t{15});
+  return factors + 8 * tokens;
+}
+
+const char s_no_rows = 0;
+
+bool rotate_mx_fused(const Shape& sh) { return rq_kernel_for(sh) != RqKernel::kGeneric; }
+
+int rotate_mx(const void* x_bf16, const void* up_bf16, int64_t tokens, int64_t n, int64_t ld, int64_t c, int sigma,
+              int rule, uint8_t* codes, int64_t ldc, uint8_t* scale, int64_t lds, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  const Shape sh = factor_n(n);
+  if (!sh.ok) {
+    set_error("unsupported n=%s", std::to_string(n).c_str());
+    return SIGNROT_EUNSUPPORTED_N;
+  }
+  const int st = mx_rows(tokens, n, ldc, lds);
+  if (st != SIGNROT_OK) return st;
+  if (rule != SIGNROT_MX_FLOOR && rule != SIGNROT_MX_NOCLIP) return fail_einval("unknown rule");
+  if (ldc & 15) return fail_einval("ldc must be a multiple of 16");
+  if (tokens > 0 && (!codes || !scale)) return fail_einval("null device pointer");
+  if (rotate_mx_fused(sh) || up_bf16) {
+    const MxOut mx = {scale, ldc, lds, rule == SIGNROT_MX_NOCLIP};
+    return rotate_quant_outlier_impl(x_bf16, tokens, n, ld, c, sigma, codes, nullptr, nullptr, nullptr, 0, stream,
+                                     up_bf16, &mx);
+  }
+  if (!aligned16(codes)) return fail_einval("codes must be 16-byte aligned");
+  int64_t at_codes, at_factors;
+  const int64_t need = rotate_mx_scratch(tokens, n, at_codes, at_factors);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  if (tokens > 0 && (!ws || workspace_bytes < need)) return fail_einval("workspace too small");
+  if (tokens > 0 && !aligned16(ws)) return fail_einval("workspace must be 16-byte aligned");
+  float* const y = reinterpret_cast<float*>(ws);
+  float* const factors = reinterpret_cast<float*>(ws + at_factors);
+  const int rs = rotate_quant_outlier_impl(x_bf16, tokens, n, ld, c, sigma, ws + at_codes, factors, factors + tokens, y,
+                                           0, stream);
+  if (rs != SIGNROT_OK || tokens == 0) return rs;
+  const hipError_t e = launch_quant_mx(y, 0, tokens, static_cast<int>(n), n, codes, ldc, scale, lds,
+                                       rule == SIGNROT_MX_NOCLIP, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "rotate_quant_mxfp4 launch");
+  return SIGNROT_OK;
+}
+}  // namespace
+
+int signrot_rotate_quant_mxfp4(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, int64_t c, int sigma,
+                               int rule, uint8_t* codes, int64_t ldc, uint8_t* scale, int64_t lds, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  return rotate_mx(x_bf16, nullptr, tokens, n, ld, c, sigma, rule, codes, ldc, scale, lds, workspace, workspace_bytes,
+                   stream);
+}
+
+int64_t signrot_rotate_quant_mxfp4_workspace(int64_t tokens, int64_t n) {
+  g_last_error[0] = '\0';
+  const Shape sh = factor_n(n);
+  if (tokens < 0 || tokens >= (int64_t{1} << 31) || !sh.ok) return -1;
+  int64_t codes, factors;
+  return rotate_mx_fused(sh) ? 0 : rotate_mx_scratch(tokens, n, codes, factors);
+}
+
+int signrot_qk_norm_rope(const signrot_qk_norm_rope_args* args, void* stream) {
+  g_last_error[0] = '\0';
+  if (!args) return fail_einval("args is NULL");
+  const signrot_qk_norm_rope_args& a = *args;
+  if (a.tokens < 0 || a.tokens >= (int64_t{1} << 31)) return fail_einval("tokens must be in [0, 2^31)");
+  if (a.head < 8 || a.head > 512 || (a.head & 1)) return fail_einval("head must be even and in [8, 512]");
+  if (a.rotary < 0 || a.rotary > a.head || (a.rotary & 1)) return fail_einval("rotary must be even and in [0, head]");
+  if (a.q_heads < 1 || a.q_heads > 65536 || a.k_heads < 0 || a.k_heads > 65536)
+    return fail_einval("q_heads must be in [1, 65536] and k_heads in [0, 65536]");
+  if (!known_type(a.in_type) || !known_type(a.out_type) || !known_type(a.param_type))
+    return fail_einval("unknown in_type, out_type or param_type");
+  if (a.norm < SIGNROT_NORM_NONE || a.norm > SIGNROT_NORM_LAYER) return fail_einval("unknown norm");
+  if (!isfinite(a.eps) || a.eps < 0.f) return fail_einval("eps must be finite and >= 0");
+  if ((a.interleaved | a.positions_64) & ~1) return fail_einval("interleaved and positions_64 must be 0 or 1");
+  if (a.ldq < 0 || a.hsq < 0 || a.ldqo < 0 || a.hsqo < 0 || a.ldk < 0 || a.hsk < 0 || a.ldko < 0 || a.hsko < 0)
+    return fail_einval("a stride is negative");
+  if (a.rotary > 0 && a.ldt < a.rotary / 2) return fail_einval("ldt < rotary / 2");
+  if (a.tokens == 0) return SIGNROT_OK;
+  if (!a.q || !a.q_out || (a.k_heads > 0 && (!a.k || !a.k_out))) return fail_einval("null device pointer");
+  if (a.rotary > 0) {
+    if (!a.cos || !a.sin) return fail_einval("null device pointer");
+    if (a.places < 1) return fail_einval("places must be >= 1");
+    if (!a.positions && a.places < a.tokens) return fail_einval("places < tokens without positions");
+  }
+  if (misaligned(a.q, a.in_type) || misaligned(a.k, a.in_type) || misaligned(a.q_out, a.out_type) ||
+      misaligned(a.k_out, a.out_type) || misaligned(a.cos, SIGNROT_F32) || misaligned(a.sin, SIGNROT_F32) ||
+      (reinterpret_cast<uintptr_t>(a.positions) & (a.positions_64 ? 7u : 3u)) != 0 ||
+      misaligned(a.q_weight, a.param_type) || misaligned(a.k_weight, a.param_type) ||
+      misaligned(a.q_bias, a.param_type) || misaligned(a.k_bias, a.param_type))
+    return fail_einval("a pointer is not aligned to its type");
+  if ((a.q_out == a.q && (a.ldqo != a.ldq || a.hsqo != a.hsq || a.out_type != a.in_type)) ||
+      (a.k_heads > 0 && a.k_out == a.k && (a.ldko != a.ldk || a.hsko != a.hsk || a.out_type != a.in_type)))
+    return fail_einval("an output is its input with another stride or type");
+  const hipError_t e = launch_qk_norm_rope(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail_hip(e, "qk_norm_rope launch");
+  return SIGNROT_OK;
+}
+
+int signrot_swiglu_rotate_quant_mxfp4(const void* gate_bf16, const void* up_bf16, int64_t tokens, int64_t n, int64_t ld,
+                                      int64_t c, int sigma, int rule, uint8_t* codes, int64_t ldc, uint8_t* scale,
+                                      int64_t lds, void* stream) {
+  if (tokens > 0 && !up_bf16) {
+    g_last_error[0] = '\0';
+    return fail_einval("null device pointer");
+  }
+  // (a call without tokens has no pointers: any marks the producer as fused)
+  return rotate_mx(gate_bf16, tokens > 0 ? up_bf16 : &s_no_rows, tokens, n, ld, c, sigma, rule, codes, ldc, scale, lds,
+                   nullptr, 0, stream);
 }
 
 int signrot_stream_ceiling(const void* x_bf16, int64_t tokens, int64_t n, int64_t ld, uint8_t* out, float* s0,

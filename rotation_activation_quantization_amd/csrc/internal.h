@@ -91,6 +91,10 @@ struct RqArgs {
   int hw;                // 32-bit words per mask row of H_m
   const uint32_t* hm;    // device mask table of H_m (m > 1), see OuterTable
   const uint32_t* hmt;   // device mask table of H_m^T (set for the outer-order MFMA kernel)
+  uint8_t* mx_scale;     // MXFP4 output: block scales [tokens][mx_lds], codes then [tokens][mx_ldc]; else null
+  int64_t mx_lds;
+  int64_t mx_ldc;
+  int mx_noclip;
 };
 
 // Launchers; each returns the hipError_t of the launch.
@@ -178,5 +182,35 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t tokens, int n, int64_t l
                              float* scale, int32_t* sum, hipStream_t s);
 
 hipError_t launch_residual_norm(const signrot_residual_norm_args& a, hipStream_t s);
+
+// MXFP4: the quantizer, its inverse, and the product.
+hipError_t launch_quant_mx(const void* x, int bf16, int64_t tokens, int n, int64_t ld, uint8_t* codes, int64_t ldc,
+                           uint8_t* scale, int64_t lds, int noclip, hipStream_t s);
+hipError_t launch_dequant_mx(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds, int64_t tokens,
+                             int n, void* y, int64_t ldy, int bf16, hipStream_t s);
+struct MxArgs {
+  const uint8_t* a;      // [T][lda] codes
+  int64_t lda;           // bytes
+  const uint8_t* scale;  // [T][lds]
+  int64_t lds;
+  const uint8_t* w;  // [R][ldw]
+  int64_t ldw;
+  const uint8_t* w_scale;  // [R][ldws]
+  int64_t ldws;
+  const float* bias;  // [R] or nullptr
+  void* out;          // [T][ldo]
+  int64_t ldo;
+  uint8_t* workspace;
+  int out_bf16;
+  int T;
+  int R;
+  int n;  // a multiple of 32
+};
+constexpr int kMxMaxN = 131072;
+int64_t mx_workspace(const MxArgs& a);
+const char* mx_name(const MxArgs& a);
+hipError_t launch_mx(const MxArgs& a, hipStream_t s);
+
+hipError_t launch_qk_norm_rope(const signrot_qk_norm_rope_args& a, hipStream_t s);
 
 }  // namespace signrot

@@ -47,6 +47,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "mx_ops.h"
 #include "rq_fast_common.h"
 
 
@@ -70,7 +71,9 @@ __device__ __forceinline__ float max3_of(float x, float y, float z) {
 // cases share one register allocation.  Without it d is given as (c, sigma).
 // get_form() yields the form of d; every thread calls it once, after the
 // first row's loads have been issued.
-template <int KA, int KB, bool MAYBE_GENERAL, bool YOUT, bool ZINT = false, bool SWIGLU = false, class GetForm>
+// MX: MXFP4 codes and block scales in place of the INT4 ones.
+template <int KA, int KB, bool MAYBE_GENERAL, bool YOUT, bool ZINT = false, bool SWIGLU = false, bool MX = false,
+          class GetForm>
 __device__ void rq_fast_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbits, const uint32_t* h28,
                              GetForm get_form, float* red, float* xcl) {
   using S = FastShape<KA, KB>;
@@ -334,8 +337,10 @@ __device__ void rq_fast_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbit
     if (nxt < tokens) {
       // The loads were issued a row ago; after them every wave issued the
       // previous row's code store (plus NT y stores with y_out); wave 0 also
-      // scale and zero, so the same count only makes it wait longer.
+      // scale and zero, so the same count only makes it wait longer.  With MX
+      // every wave issued a code and a scale store.
       if (first) wait_vmcnt<0>();
+      else if (MX) wait_vmcnt<2>();
       else if (YOUT) wait_vmcnt<1 + NT>();
       else wait_vmcnt<1>();
       if constexpr (PAR) write_row(Buf0{});
@@ -362,6 +367,41 @@ __device__ void rq_fast_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbit
         const uint32_t sbit = (dw << (31 - e)) & 0x80000000u;
         v[e] = __uint_as_float(__float_as_uint(v[e]) ^ sbit);
       }
+    }
+
+    if constexpr (MX) {
+      // (4) and (5) for blocks of 32 channels: a block is 8 / NT lanes' values,
+      // so its maximum needs no other wave; the barrier publishes the next row.
+      const float xc = xcl[PAR];
+      lds_barrier();
+      const float shift = sig > 0 ? xc : -xc;
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        v[e] = (v[e] + shift) * a.inv_sqrt_n;
+        top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+      }
+      top = mx::lanes_top<8 / NT>(top);
+      const uint32_t b = mx::scale_byte(top, a.mx_noclip);
+      uint32_t q[NT / 2];
+#pragma unroll
+      for (int u = 0; u < NT / 2; ++u) q[u] = mx::codes_f32(v + 8 * u, b);
+      const __amdgpu_buffer_rsrc_t cs = buffer_rsrc(a.codes + urow * a.mx_ldc, S::N / 2);
+      const uint32_t coff = static_cast<uint32_t>(chan0 / 2);
+      if constexpr (NT == 8)
+        store_b128_held<kNontemporal>(u32x4_t{q[0], q[1], q[2], q[3]}, cs, coff, 0);
+      else if constexpr (NT == 4)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{q[0], q[1]}, cs, coff, 0, kNontemporal);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(q[0], cs, coff, 0, kNontemporal);
+      if (outm % (8 / NT) == 0)
+        __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(b),
+                                             buffer_rsrc(a.mx_scale + urow * a.mx_lds, S::N / 32),
+                                             static_cast<uint32_t>(chan0 / 32), 0, 0);
+      cur = nxt;
+      nxt = nn;
+      nn += grid;
+      return;
     }
 
     // (4) min / max over the row: lanes, then waves through LDS
@@ -471,7 +511,7 @@ __device__ void rq_fast_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbit
 }
 
 // DVEC: d is a vector (its form is decided here); otherwise (c, sigma) given.
-template <int KA, int KB, bool DVEC, bool YOUT, bool ZINT = false, bool SWIGLU = false>
+template <int KA, int KB, bool DVEC, bool YOUT, bool ZINT = false, bool SWIGLU = false, bool MX = false>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4)))
 void rq_fast_kernel(RqArgs a) {
   using S = FastShape<KA, KB>;
@@ -502,7 +542,7 @@ void rq_fast_kernel(RqArgs a) {
   if constexpr (!DVEC) {
     // d = sigma * (row c of H) by construction: nothing to read or decode;
     // the barrier publishes h28_lds and the zeroed rows
-    rq_fast_body<KA, KB, false, YOUT, ZINT, SWIGLU>(
+    rq_fast_body<KA, KB, false, YOUT, ZINT, SWIGLU, MX>(
         a, lds, dbits, h28_lds,
         [&] {
           __syncthreads();
@@ -545,9 +585,14 @@ hipError_t launch_shape(const RqArgs& a, hipStream_t stream) {
     s.tokens = (a.tokens - r0 < kMaxRows) ? a.tokens - r0 : kMaxRows;
     s.x = a.x + r0 * a.ld;
     if (a.x2) s.x2 = a.x2 + r0 * a.ld;
-    s.codes = a.codes + r0 * (a.n / 2);
-    s.scale = a.scale + r0;
-    s.zero = a.zero + r0;
+    if (a.mx_scale) {
+      s.codes = a.codes + r0 * a.mx_ldc;
+      s.mx_scale = a.mx_scale + r0 * a.mx_lds;
+    } else {
+      s.codes = a.codes + r0 * (a.n / 2);
+      s.scale = a.scale + r0;
+      s.zero = a.zero + r0;
+    }
     if (a.yout) s.yout = a.yout + r0 * a.n;
     const hipError_t e = launch_shape_rows<KA, KB>(s, stream);
     if (e != hipSuccess) return e;
@@ -581,7 +626,10 @@ hipError_t launch_shape_rows(const RqArgs& a, hipStream_t stream) {
   if (grid > a.tokens) grid = a.tokens;
   const dim3 blocks(static_cast<unsigned>(grid));
   const dim3 threads(static_cast<unsigned>(S::kThreads));
-  if (a.x2)  // SwiGLU producer fused in: d given as (c, sigma)
+  if (a.mx_scale)  // MXFP4 output: d given as (c, sigma)
+    (a.x2 ? rq_fast_kernel<KA, KB, false, false, false, true, true>
+          : rq_fast_kernel<KA, KB, false, false, false, false, true>)<<<blocks, threads, 0, stream>>>(a);
+  else if (a.x2)  // SwiGLU producer fused in: d given as (c, sigma)
     (a.yout ? rq_fast_kernel<KA, KB, false, true, false, true> : rq_fast_kernel<KA, KB, false, false, false, true>)
         <<<blocks, threads, 0, stream>>>(a);
   else if (a.zint)  // only with d given as (c, sigma), and no y_out

@@ -8,6 +8,7 @@
 
 #include <atomic>
 
+#include "mx_ops.h"
 #include "rq_fast_common.h"
 
 namespace signrot {
@@ -33,7 +34,8 @@ namespace {
 // transform; the weights then carry no fold); otherwise d = sigma * H[c][.].
 // The d-vector kernel branches between the two bodies once per work-group,
 // so each is register-allocated on its own.
-template <bool GENERAL, bool YOUT, bool ZINT, bool SWIGLU>
+// MX: MXFP4 codes and block scales in place of the INT4 ones.
+template <bool GENERAL, bool YOUT, bool ZINT, bool SWIGLU, bool MX = false>
 __device__ void rq_halves_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbits, const uint32_t* h28,
                                const DForm& form, float* red, float* xcl) {
   using S = FastShape<28, 9>;  // one half
@@ -229,10 +231,11 @@ __device__ void rq_halves_body(const RqArgs& a, uint8_t* lds, const uint32_t* db
 
     // Phase 1: half 0 from buffer 0; stage half 1 (its loads were issued
     // between the previous row's two code stores; after them came the second
-    // code store and, with y_out, NT y stores).
+    // code store and, with y_out, NT y stores, or with MX a scale store).
     float v0[NV];
     mfma_half(v0, 0u);
     if (it == 0) wait_vmcnt<0>();
+    else if (MX) wait_vmcnt<2>();
     else if (YOUT) wait_vmcnt<1 + NT>();
     else wait_vmcnt<1>();
     write_half(kB1, par, 1);
@@ -277,6 +280,35 @@ __device__ void rq_halves_body(const RqArgs& a, uint8_t* lds, const uint32_t* db
         v0[e] = __uint_as_float(__float_as_uint(v0[e]) ^ ((d0 << (31 - e)) & 0x80000000u));
         v1[e] = __uint_as_float(__float_as_uint(v1[e]) ^ ((d1 << (31 - e)) & 0x80000000u));
       }
+    }
+
+    if constexpr (MX) {
+      // blocks of 32 channels: the lane's values of an output half
+      const float xc = xcl[par];
+      lds_barrier();
+      const float shift = sig > 0 ? xc : -xc;
+      const __amdgpu_buffer_rsrc_t cs = buffer_rsrc(a.codes + row * a.mx_ldc, kFull / 2);
+      const __amdgpu_buffer_rsrc_t ss = buffer_rsrc(a.mx_scale + row * a.mx_lds, kFull / 32);
+      auto store_block = [&](float (&v)[NV], int half) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+          v[e] = (v[e] + shift) * a.inv_sqrt_n;
+          top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+        const uint32_t b = mx::scale_byte(top, a.mx_noclip);
+        u32x4_t q;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q[u] = mx::codes_f32(v + 8 * u, b);
+        __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(b), ss, static_cast<uint32_t>(chan0 / 32), 16 * half,
+                                             0);
+        store_b128_held<kNontemporal>(q, cs, static_cast<uint32_t>(chan0 / 2), 256 * half);
+      };
+      store_block(v0, 0);
+      next_half(nxt, 1);
+      store_block(v1, 1);
+      cur = nxt;
+      continue;
     }
 
     // min / max over the 64 values, the lanes, then the waves through LDS
@@ -379,7 +411,7 @@ __device__ void rq_halves_body(const RqArgs& a, uint8_t* lds, const uint32_t* db
 }
 
 // n = 28672 in two halves of 28 x 512 (seven waves).
-template <bool DVEC, bool YOUT, bool ZINT = false, bool SWIGLU = false>
+template <bool DVEC, bool YOUT, bool ZINT = false, bool SWIGLU = false, bool MX = false>
 __global__ __launch_bounds__(448) __attribute__((amdgpu_waves_per_eu(4)))
 void rq_halves_kernel(RqArgs a) {
   using S = FastShape<28, 9>;
@@ -410,7 +442,7 @@ void rq_halves_kernel(RqArgs a) {
   if (DVEC && __builtin_amdgcn_readfirstlane(form.structured) == 0)
     rq_halves_body<true, YOUT, ZINT, SWIGLU>(a, lds, dbits, h28_lds, form, red, xcl);
   else
-    rq_halves_body<false, YOUT, ZINT, SWIGLU>(a, lds, dbits, h28_lds, form, red, xcl);
+    rq_halves_body<false, YOUT, ZINT, SWIGLU, MX>(a, lds, dbits, h28_lds, form, red, xcl);
 }
 
 }  // namespace
@@ -432,7 +464,10 @@ hipError_t launch_rq_halves(const RqArgs& a, hipStream_t stream) {
   if (grid > a.tokens) grid = a.tokens;
   const dim3 blocks(static_cast<unsigned>(grid));
   const dim3 threads(static_cast<unsigned>(S::kThreads));
-  if (a.x2)
+  if (a.mx_scale)
+    (a.x2 ? rq_halves_kernel<false, false, false, true, true> : rq_halves_kernel<false, false, false, false, true>)
+        <<<blocks, threads, 0, stream>>>(a);
+  else if (a.x2)
     (a.yout ? rq_halves_kernel<false, true, false, true> : rq_halves_kernel<false, false, false, true>)
         <<<blocks, threads, 0, stream>>>(a);
   else if (a.zint)

@@ -47,6 +47,7 @@
 #include <atomic>
 
 #include "device_common.h"
+#include "mx_ops.h"
 #include "wave_ops.h"
 
 namespace signrot {
@@ -112,7 +113,8 @@ __device__ __forceinline__ int one_tile_out(int nl) {
   return (nl & 9) ^ ((nl & 2) ? 6 : 0) ^ ((nl & 4) ? 3 : 0);
 }
 
-template <int KC, int NTL, int MTW, bool GENERAL, bool YOUT, bool ZINT = false>
+// MX: MXFP4 codes and block scales in place of the INT4 ones.
+template <int KC, int NTL, int MTW, bool GENERAL, bool YOUT, bool ZINT = false, bool MX = false>
 __device__ void rq_outer_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbits, const DForm& form, float* red,
                               float* xcl) {
   using S = OuterShape<KC, NTL, MTW>;
@@ -325,6 +327,67 @@ __device__ void rq_outer_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbi
         }
     }
 
+    if constexpr (MX) {
+      // (4) and (5) for blocks of 32 channels: 32 / NTL lanes' values of one row
+      // a' (with one column tile, all sixteen lanes' of rows r and r + 1), so a
+      // block's maximum needs no other wave; the barrier publishes the next row.
+      lds_barrier();
+      const float shift = sig > 0 ? xc : -xc;
+      uint8_t* const crow = a.codes + row * a.mx_ldc;
+      uint8_t* const srow = a.mx_scale + row * a.mx_lds;
+      constexpr int kRows = NTL == 1 ? 2 : 1;  // rows a' of a block
+#pragma unroll
+      for (int i = 0; i < MTW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; r += kRows) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+              float& e = v[(i * NTL + t) * 4 + r + h];
+              e = (e + shift) * a.inv_sqrt_n;
+              top = max(top, __float_as_uint(e) & 0x7fffffffu);
+            }
+          top = mx::lanes_top<(NTL >= 2 ? 32 / NTL : 16)>(top);
+          const uint32_t b = mx::scale_byte(top, a.mx_noclip);
+          if constexpr (NTL == 1) {
+            // rows r and r + 1 of a lane in one conversion: the nibbles of one
+            // byte go to two rows, and the partner's nibble joins each
+            const float pair[8] = {v[i * 4 + r], v[i * 4 + r + 1]};
+            const uint32_t mine = mx::codes_f32(pair, b);
+            const uint32_t other = mx::from_lane<0xB1>(mine);  // quad_perm 1, 0, 3, 2: output outm ^ 1
+            if (rv[i][r] && (outm & 1) == 0) {
+              const int j0 = (16 * (w * MTW + i) + 4 * g4 + r) * B + outm;
+              crow[j0 / 2] = static_cast<uint8_t>((mine & 15u) | ((other & 15u) << 4));
+              crow[(j0 + B) / 2] = static_cast<uint8_t>(((mine >> 4) & 15u) | (other & 0xf0u));
+              if (outm == 0) srow[j0 / 32] = static_cast<uint8_t>(b);
+            }
+          } else {
+            if (!rv[i][r]) continue;
+            const int j0 = (16 * (w * MTW + i) + 4 * g4 + r) * B + NTL * outm;
+            uint32_t q[(NTL + 7) / 8];
+#pragma unroll
+            for (int u = 0; u < (NTL + 7) / 8; ++u) {
+              float o[8] = {};
+#pragma unroll
+              for (int k = 0; k < 8 && k < NTL; ++k) o[k] = v[(i * NTL + 8 * u + k) * 4 + r];
+              q[u] = mx::codes_f32(o, b);
+            }
+            uint8_t* const cp = crow + j0 / 2;
+            if constexpr (NTL == 2) *cp = static_cast<uint8_t>(q[0]);
+            else if constexpr (NTL == 4) *reinterpret_cast<uint16_t*>(cp) = static_cast<uint16_t>(q[0]);
+            else if constexpr (NTL == 8) *reinterpret_cast<uint32_t*>(cp) = q[0];
+            else *reinterpret_cast<uint2*>(cp) = make_uint2(q[0], q[1]);
+            if (j0 % 32 == 0) srow[j0 / 32] = static_cast<uint8_t>(b);
+          }
+        }
+      cur = nxt;
+      nxt = nn;
+      nn += grid;
+      continue;
+    }
+
     // (4) min / max over the row's valid outputs: lanes, then waves via LDS
     float mn = INFINITY, mx = -INFINITY;
 #pragma unroll
@@ -442,7 +505,7 @@ __device__ void rq_outer_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbi
   }
 }
 
-template <int KC, int NTL, int MTW, bool YOUT, bool ZINT = false>
+template <int KC, int NTL, int MTW, bool YOUT, bool ZINT = false, bool MX = false>
 __global__ __launch_bounds__((64 * OuterShape<KC, NTL, MTW>::kMaxWaves)) void rq_outer_kernel(RqArgs a) {
   using S = OuterShape<KC, NTL, MTW>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::kBufBytes];
@@ -459,9 +522,9 @@ __global__ __launch_bounds__((64 * OuterShape<KC, NTL, MTW>::kMaxWaves)) void rq
     __syncthreads();
     form = decode_d_form(a, dbits, scratch);
   }
-  if constexpr (ZINT) {
+  if constexpr (ZINT || MX) {
     // only with d given as (c, sigma): always the structured form
-    rq_outer_body<KC, NTL, MTW, false, YOUT, true>(a, lds, dbits, form, red, xcl);
+    rq_outer_body<KC, NTL, MTW, false, YOUT, ZINT, MX>(a, lds, dbits, form, red, xcl);
   } else {
     if (form.structured) rq_outer_body<KC, NTL, MTW, false, YOUT>(a, lds, dbits, form, red, xcl);
     else rq_outer_body<KC, NTL, MTW, true, YOUT>(a, lds, dbits, form, red, xcl);
@@ -490,7 +553,9 @@ hipError_t launch_outer_shape(const RqArgs& a, hipStream_t stream) {
   if (grid > a.tokens) grid = a.tokens;
   const dim3 blocks(static_cast<unsigned>(grid));
   const dim3 thr(static_cast<unsigned>(threads));
-  if (a.zint)
+  if (a.mx_scale)
+    rq_outer_kernel<KC, NTL, MTW, false, false, true><<<blocks, thr, 0, stream>>>(a);
+  else if (a.zint)
     rq_outer_kernel<KC, NTL, MTW, false, true><<<blocks, thr, 0, stream>>>(a);  // no y_out with zint
   else if (a.yout)
     rq_outer_kernel<KC, NTL, MTW, true><<<blocks, thr, 0, stream>>>(a);

@@ -1,0 +1,255 @@
+"""The per-head norms with the position rotation against the float64
+definition."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import rotation_activation_quantization_amd as R  # noqa: E402
+from oracle import mx_oracle as M  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+EPS = 1e-6
+
+
+def host(x):
+    return None if x is None else x.double().cpu().numpy()
+
+
+def make(t, hq, hk, d, rotary, dtype, seed, packed=True, places=512, params=BF16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((t, (hq + 2 * hk) * d), generator=g, device="cuda") * 2
+    x[:, ::7] *= 20
+    x = x.to(dtype)
+    q, k = x[:, :hq * d].view(t, hq, d), x[:, hq * d:(hq + hk) * d].view(t, hk, d)
+    if not packed:
+        q, k = q.contiguous(), k.contiguous()
+    angle = torch.rand((places, rotary // 2), generator=g, device="cuda", dtype=torch.float64) * 7
+    p = {"cos": angle.cos().float(), "sin": angle.sin().float(),
+         "positions": torch.randint(0, places, (t,), generator=g, device="cuda", dtype=torch.int32)}
+    for name in ("q_weight", "k_weight", "q_bias", "k_bias"):
+        p[name] = (torch.randn(d, generator=g, device="cuda") + 1).to(params)
+    return q, k, p
+
+
+def tolerance(x, v, ref, p, which, norm, dtype, interleaved, rotary):
+    """Binary32 roundings: v = x r w + b, r from a sum of at most 512 squares (a chain of 8 and six joins, mean, eps,
+    root, quotient: under 24 half-steps), the subtraction of a mean that is off by 16 half-steps of the largest
+    magnitude's sum, and a rotation of three operations: 48 u of both channels of a pair and, for LAYER, of |w| r
+    max|x|.  Then the result's rounding."""
+    w = host(p[which + "_weight"])
+    size = np.abs(v)
+    if norm != "none" and p[which + "_bias"] is not None:
+        size = size + np.abs(host(p[which + "_bias"]))
+    if norm == "layer":
+        c = x - x.mean(axis=2, keepdims=True)
+        r = 1 / np.sqrt((c * c).mean(axis=2, keepdims=True) + EPS)
+        size = size + r * np.abs(x).max(axis=2, keepdims=True) * (1 if w is None else np.abs(w))
+    other, h = size.copy(), rotary // 2
+    if interleaved:
+        other[:, :, 0:rotary:2], other[:, :, 1:rotary:2] = size[:, :, 1:rotary:2], size[:, :, 0:rotary:2]
+    else:
+        other[:, :, :h], other[:, :, h:rotary] = size[:, :, h:rotary], size[:, :, :h]
+    return 48 * U * (size + other) + (2.0 ** -8 if dtype is BF16 else U) * np.abs(ref)
+
+
+def check(got, x, p, which, norm, interleaved, dtype, places=None):
+    xs = host(x)
+    rotary = 2 * p["cos"].shape[1]
+    at = np.arange(len(xs)) if places is None else places
+    ref, v = M.qk_norm_rope(xs, host(p["cos"]), host(p["sin"]), at, norm, EPS, host(p[which + "_weight"]),
+                            host(p[which + "_bias"]), interleaved)
+    assert got.dtype is dtype and got.shape == x.shape
+    off = np.abs(host(got) - ref) - tolerance(xs, v, ref, p, which, norm, dtype, interleaved, rotary)
+    worst = np.unravel_index(np.argmax(off), off.shape)
+    assert off[worst] <= 0, f"{which}: over by {off[worst]} at {worst}: {host(got)[worst]} for {ref[worst]}"
+
+
+def call(q, k, p, **kw):
+    return R.qk_norm_rope(q, k, **{**p, **kw})
+
+
+SHAPES = [(1, 32, 8, 128, 128), (5, 3, 1, 64, 64), (777, 12, 12, 80, 40), (2, 1, 1, 8, 8), (9, 7, 2, 10, 6),
+          (33, 5, 5, 36, 18), (4, 64, 8, 256, 64), (3, 2, 2, 512, 512), (6, 9, 3, 262, 100), (17, 4, 1, 96, 96),
+          (300, 8, 2, 128, 2), (2, 300, 1, 24, 0), (4100, 4, 1, 32, 32), (8, 16, 16, 192, 126), (3, 5, 2, 510, 510)]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", ["rms", "layer", "none"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,hq,hk,d,rotary", SHAPES)
+def test_parity(t, hq, hk, d, rotary, dtype, norm, interleaved):
+    q, k, p = make(t, hq, hk, d, rotary, dtype, 1)
+    if norm == "rms":
+        p["q_bias"] = p["k_bias"] = None
+    at = p["positions"].cpu().numpy()
+    got = call(q, k, p, norm=norm, interleaved=interleaved)
+    for which, g, x in (("q", got[0], q), ("k", got[1], k)):
+        check(g, x, p, which, norm, interleaved, dtype, at)
+    # other output types, and the same again
+    other = F32 if dtype is BF16 else BF16
+    wide = call(q, k, p, norm=norm, interleaved=interleaved, dtype=other)
+    check(wide[0], q, p, "q", norm, interleaved, other, at)
+    again = call(q, k, p, norm=norm, interleaved=interleaved)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("d,rotary", [(128, 128), (80, 60), (36, 18)])
+def test_alone_without_weights_positions_or_rotation(d, rotary):
+    q, k, p = make(40, 6, 2, d, rotary, BF16, 2, params=F32)
+    got, none = R.qk_norm_rope(q, cos=p["cos"], sin=p["sin"], eps=EPS)
+    assert none is None
+    bare = {**p, "q_weight": None, "q_bias": None, "k_weight": None, "k_bias": None}
+    check(got, q, bare, "q", "rms", False, BF16)
+    flat = {**p, "cos": p["cos"][:, :0], "sin": p["sin"][:, :0]}
+    got = R.qk_norm_rope(q, k, q_weight=p["q_weight"], q_bias=p["q_bias"], k_weight=p["k_weight"], k_bias=p["k_bias"])
+    check(got[0], q, flat, "q", "rms", False, BF16)
+    check(got[1], k, flat, "k", "rms", False, BF16)
+    only = R.qk_norm_rope(q, k, p["cos"], p["sin"], k_weight=p["k_weight"], norm="rms")
+    check(only[0], q, bare, "q", "rms", False, BF16)
+    check(only[1], k, {**bare, "k_weight": p["k_weight"]}, "k", "rms", False, BF16)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_positions_are_clamped_into_the_table(wide):
+    q, k, p = make(6, 4, 2, 64, 64, BF16, 3, places=9)
+    p["positions"] = torch.tensor([-5, 0, 8, 9, 1 << 30, 3], device="cuda", dtype=torch.int64 if wide else torch.int32)
+    if wide:
+        p["positions"][4] = 1 << 40
+    check(call(q, k, p, norm="layer")[0], q, p, "q", "layer", False, BF16, np.array([0, 0, 8, 8, 8, 3]))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [128, 80, 36])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_in_place_equals_out_of_place(d, dtype, interleaved):
+    q, k, p = make(70, 6, 3, d, d // 2 // 2 * 2, dtype, 4)
+    ref = call(q, k, p, interleaved=interleaved, norm="layer")
+    both = call(q, k, p, interleaved=interleaved, norm="layer", q_out=q, k_out=k)
+    assert both[0] is q and both[1] is k
+    assert torch.equal(q, ref[0]) and torch.equal(k, ref[1])
+
+
+@pytest.mark.parametrize("d", [128, 40, 18])
+@pytest.mark.parametrize("off", [0, 1])
+def test_strides_orders_offsets_and_guards(d, off):
+    """Heads before tokens, padded heads, tables in wider rows, results in a strided cache."""
+    t, hq, hk, rotary = 21, 5, 2, d // 2 // 2 * 2
+    q, k, p = make(t, hq, hk, d, rotary, BF16, 5)
+    ref = call(q, k, p)
+    at = p["positions"].cpu().numpy()
+
+    def moved(x, order):
+        th, step = (x.shape[1], x.shape[0]) if order else (x.shape[0], x.shape[1])
+        buf = torch.full((off + th * (step * (d + 8)) + 64,), 7.0, dtype=BF16, device="cuda")
+        view = buf[off:].as_strided((th, step, d), (step * (d + 8), d + 8, 1))
+        return buf, view.transpose(0, 1) if order else view
+
+    for order in (False, True):
+        src = [moved(x, order)[1] for x in (q, k)]
+        for s, x in zip(src, (q, k)):
+            s.copy_(x)
+        outs = [moved(x, not order) for x in (q, k)]
+        wide = torch.zeros((2, p["cos"].shape[0], rotary // 2 + 3), device="cuda")
+        wide[0, :, :rotary // 2], wide[1, :, :rotary // 2] = p["cos"], p["sin"]
+        call(*src, {**p, "cos": wide[0, :, :rotary // 2], "sin": wide[1, :, :rotary // 2]}, q_out=outs[0][1],
+             k_out=outs[1][1])
+        for (buf, view), x, which in zip(outs, (q, k), "qk"):
+            check(view, x, p, which, "rms", False, BF16, at)
+            mask = torch.ones_like(buf, dtype=torch.bool)
+            mask.as_strided(view.shape, view.stride(), off).fill_(False)
+            assert (buf[mask] == 7.0).all()
+    assert ref[0].is_contiguous()
+
+
+def test_large_and_non_finite_heads():
+    q, k, p = make(5, 4, 4, 128, 128, F32, 6)
+    q[1, 2] *= 1e36  # squares pass binary32's range
+    k[0, 0] *= 1e-30
+    at = p["positions"].cpu().numpy()
+    for norm in ("rms", "layer"):
+        got = call(q, k, p, norm=norm)
+        check(got[0], q, p, "q", norm, False, F32, at)
+        check(got[1], k, p, "k", norm, False, F32, at)
+    clean = call(q, k, p)
+    q[3, 1, 77] = float("nan")
+    k[2, 3, 0] = float("inf")
+    got = call(q, k, p)
+    for g, c, bad in ((got[0], clean[0], (3, 1)), (got[1], clean[1], (2, 3))):
+        keep = torch.ones(g.shape[:2], dtype=torch.bool, device="cuda")
+        keep[bad] = False
+        assert not torch.isfinite(g[bad]).all() and torch.equal(g[keep], c[keep])
+
+
+def test_equal_channels_center_to_the_bias():
+    q = torch.full((3, 2, 72), 1.1, dtype=BF16, device="cuda")
+    got, _ = R.qk_norm_rope(q, norm="layer")
+    assert not got.any()
+
+
+def test_many_tokens_and_empty():
+    q, k, p = make(40000, 2, 1, 64, 64, BF16, 7)
+    at = p["positions"].cpu().numpy()
+    got = call(q, k, p)
+    check(got[0], q, p, "q", "rms", False, BF16, at)
+    check(got[1], k, p, "k", "rms", False, BF16, at)
+    assert call(q[:0], k[:0], {**p, "positions": p["positions"][:0]})[0].shape == (0, 2, 64)
+
+
+def test_offsets_past_32_bits():
+    d, step = 64, (1 << 31) + 8
+    buf = torch.empty(2 * step + 2 * d, dtype=BF16, device="cuda")
+    q = buf.as_strided((3, 2, d), (step, d, 1))
+    q.copy_(torch.randn((3, 2, d), device="cuda"))
+    _, _, p = make(3, 2, 1, d, d, BF16, 8)
+    got, _ = R.qk_norm_rope(q, cos=p["cos"], sin=p["sin"], positions=p["positions"], q_weight=p["q_weight"])
+    ref, _ = R.qk_norm_rope(q.contiguous(), cos=p["cos"], sin=p["sin"], positions=p["positions"],
+                            q_weight=p["q_weight"])
+    assert torch.equal(got, ref)
+
+
+def test_in_a_graph_and_on_a_side_stream():
+    q, k, p = make(50, 8, 2, 128, 64, BF16, 9)
+    q2, k2, _ = make(50, 8, 2, 128, 64, BF16, 10)
+    refs = [call(q, k, p), call(q2, k2, p)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = call(q, k, p)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], refs[0][0]) and torch.equal(got[1], refs[0][1])
+    hq, hk = q.clone(), k.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(hq, hk, p)
+    for n, (a, b, ref) in enumerate(((q, k, refs[0]), (q2, k2, refs[1]), (q, k, refs[0]))):
+        hq.copy_(a)
+        hk.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1]), n
+
+
+def test_refusals():
+    q, k, p = make(4, 4, 2, 64, 64, BF16, 11)
+    out = torch.empty_like(q)
+    for kw in ({"norm": "batch"}, {"cos": None}, {"cos": p["cos"].bfloat16()}, {"sin": p["sin"][:8]},
+               {"positions": p["positions"][:3]}, {"positions": p["positions"].float()},
+               {"q_weight": p["q_weight"][:32]}, {"k_weight": p["k_weight"].float()}, {"dtype": torch.float16},
+               {"q_out": out[:3]}, {"q_out": out, "dtype": F32}, {"q_out": out[:1].expand(4, 4, 64)},
+               {"q_out": out.cpu()}):
+        with pytest.raises(ValueError):
+            call(q, k, p, **kw)
+    for a, b in ((q[0], k), (q, k[:3]), (q, k[:, :, :32]), (q, k.float()), (q.half(), None), (q.transpose(1, 2), None)):
+        with pytest.raises(ValueError):
+            call(a, b, p)
+    with pytest.raises(R.SignRotError):
+        R.qk_norm_rope(torch.zeros((2, 2, 6), dtype=BF16, device="cuda"))
+    with pytest.raises(R.SignRotError):
+        R.qk_norm_rope(torch.zeros((2, 2, 63), dtype=BF16, device="cuda"))
+    with pytest.raises(R.SignRotError):  # a table shorter than the tokens, without positions
+        R.qk_norm_rope(q, cos=p["cos"][:3], sin=p["sin"][:3])
