@@ -44,6 +44,34 @@ __device__ __forceinline__ f32x4_t mfma(const i32x4_t& a, const i32x4_t& b, cons
                                                           static_cast<int>(sb));
 }
 
+// acc += a b in place, for the tiles: left to itself the compiler gives results
+// and sums registers of their own, which a tile that takes nearly all of them
+// does not have, and moves them about.  AGPR: the sums are accumulation
+// registers.  The leading s_nop covers a VALU write of an operand just before.
+// The reader of a sum has to wait for the last one (settle).
+template <int OA, int OB, bool AGPR>
+__device__ __forceinline__ void mfma_to(f32x4_t& acc, const i32x4_t& a, const i32x4_t& b, uint32_t sa, uint32_t sb) {
+#define SR_MFMA "s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+  if constexpr (AGPR)
+    asm volatile(SR_MFMA
+                 : "+a"(acc)
+                 : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
+  else
+    asm volatile(SR_MFMA
+                 : "+v"(acc)
+                 : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
+#undef SR_MFMA
+}
+// A sum's value, read where it is asked for and not before.
+template <bool AGPR>
+__device__ __forceinline__ float value_of(float sum) {
+  if constexpr (!AGPR) return sum;
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(sum));
+  return v;
+}
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
 // Results of token t from channel k on: vectors at whatever address they have,
 // single ones at the row's end.
 template <int N>
@@ -107,11 +135,13 @@ struct Tile {
   static constexpr int kWLoads = KU * kWBlocks / kWaves, kTLoads = KU * kTBlocks / kWaves;
   static constexpr int kLoads = kWLoads + kTLoads;
   static constexpr int kWStage = KU * kWDeep, kTStage = KU * kTDeep;
+  static constexpr bool kAgpr = FK * FT > 32;
   static constexpr int kPart = 256 * FK * FT * kWaves;  // floats of a tile's partial sums
   // scales: groups of 64 rows (weights, then tokens), a word of four rows' for
   // each lane and depth
   static constexpr int kGroupsW = kBN / 64, kGroups = (kBN + kBM) / 64;
   static constexpr int kScales = kGroups * kQuad * 256;
+  static constexpr int kPer = kGroups > kWaves ? kGroups / kWaves : 1;  // groups that a wave lays out
   static constexpr int kRing = S * (kWStage + kTStage);
   static constexpr int kLds = kRing + 2 * kScales;
   // work-groups to a CU: as many as its LDS holds, at most eight waves
@@ -121,8 +151,10 @@ struct Tile {
   static_assert(FK % 4 == 0 && kBM % 64 == 0, "rows come in groups of 64");
   static_assert(KU == 1 || KU == 2, "two to four steps a quad");
   static_assert(FT % 4 == 0 || 4 % FT == 0, "a wave's tokens lie in whole words of scales or in one");
-  static_assert(kGroups <= kWaves, "a wave lays out one group's scales at most");
+  static_assert(kGroups <= kWaves || kPer * kWaves == kGroups, "whole groups of scales per wave");
+  static_assert(kGroupsW % kPer == 0, "a wave's groups are of one operand");
   static_assert(kFit > 0, "LDS");
+  static_assert(kWLoads >= 2 && kTLoads >= 2, "a wave's own 2 KiB of either operand");
 };
 
 // Both operands stream global -> LDS (16 bytes a lane, no registers) through a
@@ -146,9 +178,9 @@ struct Tile {
 // 16) reads row i, chunk g of a 16-row group: block g of the depth for both
 // operands.
 //
-// Slot 16 f + i of a 64-channel group holds channel 16 (i / 4) + 4 f + i % 4:
-// the four 16 x 16 results f = 0 .. 3 then leave a lane sixteen consecutive
-// channels of a token, stored as whole vectors.
+// Slot 16 f + i of a 64-channel group holds channel 32 (f / 2) + 8 (i / 4) +
+// 4 (f % 2) + i % 4: two 16 x 16 results then leave a lane eight consecutive
+// channels of a token.
 //
 // Scales.  An MFMA takes a lane's scale from one byte of a register, the byte
 // fixed in the instruction, so a word for lane (g, i) holds block g of the rows
@@ -158,6 +190,8 @@ struct Tile {
 // that a cache line is touched once for four depths), turns the four by four
 // bytes with eight permutes two steps later, when a step's wait has seen them
 // arrive, and writes them to LDS a step before they are read.
+__device__ __forceinline__ int channel_of(int f, int i) { return 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3); }
+
 template <int WK, int WT, int FK, int FT, int KU, bool SPLIT>
 __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_n, int splits) {
   using C = Tile<WK, WT, FK, FT, KU>;
@@ -203,8 +237,8 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
   auto depth_w = [&](int l) { return (C::kWLoads * wid + l) / C::kWBlocks; };
   auto depth_t = [&](int l) { return (C::kTLoads * wid + l) / C::kTBlocks; };
-  // This wave's group of 64 rows of scales (waves beyond the groups repeat the last).
-  const int group = min(wid, C::kGroups - 1);
+  // This wave's first group of 64 rows of scales (waves beyond the groups repeat the last).
+  const int group = min(C::kPer * wid, C::kGroups - 1);
   const bool of_w = group < C::kGroupsW;
   // (an opaque copy of the lane where its constants are used once a quad or less, so
   // that they are formed there and not kept in registers)
@@ -229,8 +263,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
 #pragma unroll
     for (int l = 0; l < C::kWLoads; ++l) {
       const int slot = 16 * ((C::kWLoads * wid + l) % C::kWBlocks) + (lane >> 2);
-      const int in = slot & 15;
-      const int ch = (slot & ~63) + 16 * (in >> 2) + 4 * ((slot >> 4) & 3) + (in & 3);
+      const int ch = (slot & ~63) + channel_of((slot >> 4) & 3, slot & 15);
       off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + kDeep * depth_w(l) + chunk;
     }
 #pragma unroll
@@ -271,7 +304,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   };
 
   // The scales of the quad, words s = g of the rows; those beyond n read the quad's first.
-  uint32_t raw[4];
+  uint32_t raw[C::kPer][4];
   int raw_left = 0;
   auto load_scales = [&]() {
     const uint32_t ld = static_cast<uint32_t>(of_w ? a.ldws : a.lds);
@@ -283,23 +316,30 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     const __amdgpu_buffer_rsrc_t src =
         wave::buffer_rsrc(base_s, static_cast<uint32_t>(rows - 1) * ld + ((blocks + 3) & ~3));
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int r = r0 + (of_w ? 16 * (i >> 2) + 4 * f + (i & 3) : 16 * f + i);
-      raw[f] = __builtin_amdgcn_raw_buffer_load_b32(src, static_cast<uint32_t>(min(r, rows - 1)) * ld + word,
-                                                    at_quad / mx::kBlockBytes, 0);
-    }
+    for (int x = 0; x < C::kPer; ++x)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int r = r0 + 64 * x + (of_w ? channel_of(f, i) : 16 * f + i);
+        raw[x][f] = __builtin_amdgcn_raw_buffer_load_b32(src, static_cast<uint32_t>(min(r, rows - 1)) * ld + word,
+                                                         at_quad / mx::kBlockBytes, 0);
+      }
   };
   auto turn_scales = [&](int half) {
     const int here = lane_here(), g = here >> 4;
     uint32_t* const turned = reinterpret_cast<uint32_t*>(lds_s + 1024 * group + 256 * g) + (here & 15);
-    const uint32_t a0 = __builtin_amdgcn_perm(raw[1], raw[0], 0x05010400u);
-    const uint32_t a1 = __builtin_amdgcn_perm(raw[1], raw[0], 0x07030602u);
-    const uint32_t b0 = __builtin_amdgcn_perm(raw[3], raw[2], 0x05010400u);
-    const uint32_t b1 = __builtin_amdgcn_perm(raw[3], raw[2], 0x07030602u);
-    const uint32_t o[4] = {__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
-                           __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
 #pragma unroll
-    for (int b = 0; b < 4; ++b) turned[half * (C::kScales / 4) + 16 * b] = 4 * g + b < raw_left ? o[b] : 0;
+    for (int x = 0; x < C::kPer; ++x) {
+      const uint32_t(&d)[4] = raw[x];
+      const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u);
+      const uint32_t a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+      const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
+      const uint32_t b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+      const uint32_t o[4] = {__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                             __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        turned[half * (C::kScales / 4) + 256 * x + 16 * b] = 4 * g + b < raw_left ? o[b] : 0;
+    }
   };
 
   const int read_w = 16 * wk * FK * kDeep + i * kDeep + 16 * (g ^ (2 * (i >> 3)));
@@ -380,7 +420,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
         constexpr int f = decltype(F)::value;
         // The reads follow the block's first MFMA: the wait before that one is
         // then for reads a whole block old.
-        acc[f][0] = mfma<f % 4, 0>(wf[f], now[0], acc[f][0], cw[f / 4], ct[0]);
+        mfma_to<f % 4, 0, C::kAgpr>(acc[f][0], wf[f], now[0], cw[f / 4], ct[0]);
         __builtin_amdgcn_sched_barrier(0);
         // two reads ahead, the last two from the next depth or step
         wf[f + 2] = f + 2 < FK ? weight(pos, u, f + 2) : weight(then_pos, then_depth, f + 2 - FK);
@@ -392,22 +432,15 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
         for (int l = b * C::kLoads / kBlocks; l < (b + 1) * C::kLoads / kBlocks; ++l) issue(l, (j + 3) % C::kSteps, to);
         unrolled<FT - 1>([&](auto T) {
           constexpr int t = decltype(T)::value + 1;
-          acc[f][t] = mfma<f % 4, t % 4>(wf[f], now[t], acc[f][t], cw[f / 4], ct[t / 4]);
+          mfma_to<f % 4, t % 4, C::kAgpr>(acc[f][t], wf[f], now[t], cw[f / 4], ct[t / 4]);
         });
         __builtin_amdgcn_sched_barrier(0);
       });
       wf[0] = wf[FK];
       wf[1] = wf[FK + 1];
     });
-    if (j == 0) {
-      // (the MFMAs stay before the branches)
-#pragma unroll
-      for (int f = 0; f < FK; ++f)
-#pragma unroll
-        for (int t = 0; t < FT; ++t) asm volatile("" : "+v"(acc[f][t]));
-      advance();
-    }
-    wave::wait_vmcnt<(S - 3) * C::kLoads + (j == 1 ? 4 : 0)>();
+    if (j == 0) advance();
+    wave::wait_vmcnt<(S - 3) * C::kLoads + (j == 1 ? 4 * C::kPer : 0)>();
     if (j == 3 % C::kSteps)
       wave::lds_barrier();  // the scales are written
     else
@@ -433,6 +466,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       half ^= 1;
     }
 
+    settle();
     if (SPLIT) {
       // partial sums in operand order, [part][tile][wave][f][j][lane]
       f32x4_t* const out = reinterpret_cast<f32x4_t*>(a.workspace) +
@@ -444,28 +478,107 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       continue;
     }
 
-    // Lane (g, i): token 16 j + i, channels 16 g .. 16 g + 15 of every 64.
+    // Lane (g, i): token 16 j + i, channels 8 g .. 8 g + 7 of every 32.  Stored from
+    // there, neighbouring lanes would write sixteen rows, 16 bytes a request; so
+    // sixteen rows of 128 bytes at a time, a unit, go through LDS and leave as whole
+    // lines: through the places that the wave itself fills next in the ring position
+    // of the last step, which all waves have done with.  Chunk c of row r sits at
+    // chunk c ^ ((r >> 1) & 7): the sixteen lanes that an access serves at a time
+    // cover the banks once.  Units alternate between two places; a wave's LDS
+    // accesses are done in order, so that the next unit is written before this
+    // one has been read back.
+    const int last = C::kSteps == S ? S - 1 : (pos ^ C::kSteps) + C::kSteps - 1;
+    auto chunk_at = [&](int odd, int r, int c) {
+      uint8_t* const mine = odd ? lds_t + C::kTStage * last + 1024 * C::kTLoads * wid
+                                : lds_w + C::kWStage * last + 1024 * C::kWLoads * wid;
+      return reinterpret_cast<wave::u32x4_t*>(mine + 128 * r + 16 * (c ^ ((r >> 1) & 7)));
+    };
+    const int t_wave = m0 + 16 * wt * FT, k_wave = n0 + 16 * wk * FK;
+    float bias[FK / 4][16];
 #pragma unroll
-    for (int q = 0; q < FK / 4; ++q) {
-      const int k0 = n0 + 16 * wk * FK + 64 * q + 16 * g;
-      if (k0 >= a.R) continue;
-      float b[16];
+    for (int q = 0; q < FK / 4; ++q)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) b[e] = 0.f;
-      if (a.bias) {
+      for (int e = 0; e < 16; ++e) bias[q][e] = 0.f;
+    if (a.bias) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) b[e] = a.bias[min(k0 + e, a.R - 1)];
-      }
+      for (int q = 0; q < FK / 4; ++q)
 #pragma unroll
-      for (int j = 0; j < FT; ++j) {
-        const int t = m0 + 16 * (wt * FT + j) + i;
-        if (t >= a.T) continue;
-        float o[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = acc[4 * q + (e >> 2)][j][e & 3] + b[e];
-        store_results(a, t, k0, o);
-      }
+        for (int e = 0; e < 16; ++e)
+          bias[q][e] = a.bias[min(k_wave + 64 * q + 32 * (e >> 3) + 8 * g + (e & 7), a.R - 1)];
     }
+    auto results = [&](auto BF16) {
+      constexpr int per = BF16 ? 8 : 4;                   // results of a chunk
+      constexpr int parts = BF16 ? 1 : 2;                 // units of 64 channels
+      constexpr int units = FK / 4 * FT * parts;
+      auto put = [&](auto U) {
+        constexpr int u = decltype(U)::value, part = u % parts, j = u / parts % FT, q = u / parts / FT;
+        if constexpr (BF16) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wave::u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = row::pack_bf16(
+                  value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1)]) + bias[q][8 * h + 2 * e],
+                  value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1) + 1]) + bias[q][8 * h + 2 * e + 1]);
+            *chunk_at(u & 1, i, 4 * h + g) = v;
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wave::u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = __float_as_uint(value_of<C::kAgpr>(acc[4 * q + 2 * part + h][j][e]) +
+                                     bias[q][8 * part + 4 * h + e]);
+            *chunk_at(u & 1, i, 2 * g + h) = v;
+          }
+        }
+      };
+      const int r0 = lane >> 3, c = lane & 7;
+      uint8_t* const to = static_cast<uint8_t*>(a.out) +
+                          (static_cast<int64_t>(t_wave + r0) * a.ldo + k_wave + per * c) * (16 / per);
+      wave::u32x4_t got[2][2];
+      auto send = [&](auto U) {
+        constexpr int u = decltype(U)::value, part = u % parts, j = u / parts % FT, q = u / parts / FT;
+        const int k = k_wave + 64 * q + 32 * part + per * c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = t_wave + 16 * j + 8 * h + r0;
+          uint8_t* const at = to + (static_cast<int64_t>(16 * j + 8 * h) * a.ldo + 64 * q + 32 * part) * (16 / per);
+          const wave::u32x4_t v = got[u & 1][h];
+          if (t < a.T && k + per <= a.R) {
+            row::store_as<false>(at, v);
+          } else if (t < a.T) {
+#pragma unroll
+            for (int e = 0; e < per; ++e) {
+              if (k + e >= a.R) continue;
+              if constexpr (BF16)
+                reinterpret_cast<uint16_t*>(at)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+              else
+                reinterpret_cast<uint32_t*>(at)[e] = v[e];
+            }
+          }
+        }
+      };
+      put(std::integral_constant<int, 0>{});
+      unrolled<units>([&](auto U) {
+        constexpr int u = decltype(U)::value;
+        if constexpr (u + 1 < units) put(std::integral_constant<int, u + 1>{});
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) got[u & 1][h] = *chunk_at(u & 1, 8 * h + r0, c);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if constexpr (u > 0) send(std::integral_constant<int, u - 1>{});
+      });
+      send(std::integral_constant<int, units - 1>{});
+    };
+    if (a.out_bf16)
+      results(std::true_type{});
+    else
+      results(std::false_type{});
   }
   wave::wait_vmcnt<0>();
 }
@@ -490,7 +603,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(MxArgs a, int tiles_m, int
   int tm, tn;
   tile_at(tile, tiles_m, tiles_n, tm, tn);
   const int t = tm * C::kBM + 16 * ((wid / WK) * FT + j) + (lane & 15);
-  const int k = tn * C::kBN + 16 * (wid % WK) * FK + 64 * (f >> 2) + 16 * (lane >> 4) + 4 * (f & 3);
+  const int k = tn * C::kBN + 16 * (wid % WK) * FK + 64 * (f >> 2) + channel_of(f & 3, 4 * (lane >> 4));
   if (t >= a.T || k >= a.R) return;
   const f32x4_t* src = reinterpret_cast<const f32x4_t*>(a.workspace) + e;
   const int64_t pitch = static_cast<int64_t>(tiles) * (C::kPart / 4);
