@@ -115,68 +115,78 @@ __device__ __forceinline__ void tile_at(int p, int tiles_m, int tiles_n, int& tm
 }
 
 constexpr int kDeep = 64;               // bytes of a row that one MFMA takes: four blocks
-constexpr int kQuad = 4;                // MFMA depths whose scales are handled together
-constexpr int kQuadBytes = kQuad * kDeep;
+constexpr int kStage = 2 * kDeep;       // of a stage: a whole 128-byte line
+constexpr int kQuadBytes = 2 * kStage;  // of a quad, the depths whose scales are handled together
 
-// WK x WT waves of FK x FT 16 x 16 results each, a ring of four steps of KU
+// Channel of a 64-channel group in slot 16 f + i.
+__device__ __forceinline__ int channel_of(int f, int i) { return 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3); }
+
+// The words of scales of four 16-row groups, depth s (lane (s, i): d[f] of row
+// 16 f + i), as those of the MFMA: o[b] for lane (b, i) of that depth.
+__device__ __forceinline__ void turned_words(const uint32_t (&d)[4], uint32_t (&o)[4]) {
+  const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+  const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u), b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+}
+
+// WK x WT waves of FK x FT 16 x 16 results each, a ring of S stages of two
 // MFMAs' depth.
-template <int WK, int WT, int FK, int FT, int KU>
+template <int WK, int WT, int FK, int FT, int S>
 struct Tile {
-  static constexpr int S = 4;
-  static constexpr int kStep = KU * kDeep;  // bytes of a row per step
-  static constexpr int kSteps = kQuad / KU; // of a quad
   static constexpr int kWaves = WK * WT;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kBN = 16 * WK * FK;  // channels
   static constexpr int kBM = 16 * WT * FT;  // tokens
-  // LDS bytes of one MFMA's depth, its 1 KiB loads, and the loads per wave and step
-  static constexpr int kWDeep = kBN * kDeep, kTDeep = kBM * kDeep;
-  static constexpr int kWBlocks = kWDeep / 1024, kTBlocks = kTDeep / 1024;
-  static constexpr int kWLoads = KU * kWBlocks / kWaves, kTLoads = KU * kTBlocks / kWaves;
+  // LDS bytes of a stage, and its 1 KiB loads per wave
+  static constexpr int kWStage = kBN * kStage, kTStage = kBM * kStage;
+  static constexpr int kWLoads = kWStage / 1024 / kWaves, kTLoads = kTStage / 1024 / kWaves;
   static constexpr int kLoads = kWLoads + kTLoads;
-  static constexpr int kWStage = KU * kWDeep, kTStage = KU * kTDeep;
   static constexpr bool kAgpr = FK * FT > 32;
   static constexpr int kPart = 256 * FK * FT * kWaves;  // floats of a tile's partial sums
   // scales: groups of 64 rows (weights, then tokens), a word of four rows' for
   // each lane and depth
   static constexpr int kGroupsW = kBN / 64, kGroups = (kBN + kBM) / 64;
-  static constexpr int kScales = kGroups * kQuad * 256;
+  static constexpr int kScales = kGroups * 4 * 256;
   static constexpr int kPer = kGroups > kWaves ? kGroups / kWaves : 1;  // groups that a wave lays out
   static constexpr int kRing = S * (kWStage + kTStage);
-  static constexpr int kLds = kRing + 2 * kScales;
+  static constexpr int kLds = kRing + 2 * kScales + 2048 * kWaves;  // and a unit of results for each wave
   // work-groups to a CU: as many as its LDS holds, at most eight waves
   static constexpr int kFit = 160 * 1024 / kLds < 8 / kWaves ? 160 * 1024 / kLds : 8 / kWaves;
-  static_assert(kWLoads * kWaves == KU * kWBlocks && kTLoads * kWaves == KU * kTBlocks, "whole loads per wave");
-  static_assert(kWBlocks * 1024 == kWDeep && kTBlocks * 1024 == kTDeep, "whole loads");
+  static_assert(kWLoads * kWaves * 1024 == kWStage && kTLoads * kWaves * 1024 == kTStage, "whole loads per wave");
   static_assert(FK % 4 == 0 && kBM % 64 == 0, "rows come in groups of 64");
-  static_assert(KU == 1 || KU == 2, "two to four steps a quad");
+  static_assert(S == 2 || S == 4, "ring");
   static_assert(FT % 4 == 0 || 4 % FT == 0, "a wave's tokens lie in whole words of scales or in one");
   static_assert(kGroups <= kWaves || kPer * kWaves == kGroups, "whole groups of scales per wave");
   static_assert(kGroupsW % kPer == 0, "a wave's groups are of one operand");
   static_assert(kFit > 0, "LDS");
-  static_assert(kWLoads >= 2 && kTLoads >= 2, "a wave's own 2 KiB of either operand");
 };
 
-// Both operands stream global -> LDS (16 bytes a lane, no registers) through a
-// ring of four steps; one barrier a step.  Step s: the MFMAs of step s, the
-// loads of step s + 3 into the buffers step s - 1 used, and towards its end the
-// first operand reads of step s + 1 (which has landed: the barrier at the end
-// of step s - 1 came after every wave's wait for it).
+// Both operands stream global -> LDS (16 bytes a lane, no registers), a whole
+// 128-byte line of a row at a time, through a ring of S stages of two MFMA
+// depths.  A depth is FK blocks of FT MFMAs, one block for each of the wave's
+// 16-row groups of weights; operands are read two blocks (weights) or a depth
+// (tokens) ahead.  One barrier a stage, before its last two blocks: by then
+// every wave has read all of the stage, whose place the loads of stage s + S may
+// take, and stage s + 1 has landed (the wait before the barrier), so that its
+// first operands are read in the last two blocks.
 //
 // A work-group takes the tiles p, p + stride, ... below `end`, and the ring
-// runs on from tile to tile: the last steps of a tile load the first ones of
+// runs on from tile to tile: the last stages of a tile load the first ones of
 // the next, which arrive while its results are stored.
 //
-// A row is cut into quads of four MFMA depths (512 channels).  Quad 0 of a tile
-// is the row's last, possibly short one.  Its chunks beyond n are read from the
-// quad's first chunk, and the scales of both operands there are 2^-127: the
-// products, below 2^-248, are zero in binary32.
+// A row is cut into quads of four depths (512 channels, two stages).  Quad 0 of
+// a tile is the row's last, possibly short one.  Its chunks beyond n are read
+// from the quad's first chunk, and the scales of both operands there are
+// 2^-127: the products, below 2^-248, are zero in binary32.
 //
-// LDS rows of 64 bytes, four 16-byte chunks: logical chunk c of row r sits at
-// physical chunk c ^ 2 ((r >> 3) & 1), so that the sixteen lanes a 16-byte read
-// serves at a time cover the 64 banks once.  A lane (g = lane / 16, i = lane %
-// 16) reads row i, chunk g of a 16-row group: block g of the depth for both
-// operands.
+// LDS rows of 128 bytes, eight 16-byte chunks: logical chunk c of row r sits at
+// physical chunk c ^ ((r >> 1) & 7), so that the sixteen lanes a
+// 16-byte read serves at a time cover the 64 banks once.  A lane (g = lane / 16,
+// i = lane % 16) reads row i, chunk 4 u + g of a 16-row group: block g of depth
+// u for both operands.
 //
 // Slot 16 f + i of a 64-channel group holds channel 32 (f / 2) + 8 (i / 4) +
 // 4 (f % 2) + i % 4: two 16 x 16 results then leave a lane eight consecutive
@@ -187,15 +197,17 @@ struct Tile {
 // i of four 16-row groups f: one 4-byte LDS read serves four operands.  A row's
 // scales of a quad are sixteen bytes.  For each quad a wave takes the scales of
 // 64 rows into registers (lane (s, i): the word of depth s of rows 16 f + i, so
-// that a cache line is touched once for four depths), turns the four by four
-// bytes with eight permutes two steps later, when a step's wait has seen them
-// arrive, and writes them to LDS a step before they are read.
-__device__ __forceinline__ int channel_of(int f, int i) { return 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3); }
+// that a cache line is touched once for four depths) with the quad's first
+// loads, and before a barrier whose wait has seen them arrive turns the four by
+// four bytes with eight permutes and writes them to LDS.  That work is a tenth of a
+// large product's time (8192 x 28672 x 4096 436 us, 392 without); so for the
+// largest tiles (ORDERED) a kernel of its own turns all scales once, into
+// 1 KiB for 64 rows and a quad, which a wave loads straight to LDS.
+__device__ __forceinline__ int swizzle_of(int r) { return (r >> 1) & 7; }
 
-template <int WK, int WT, int FK, int FT, int KU, bool SPLIT>
+template <int WK, int WT, int FK, int FT, int S, bool SPLIT, bool ORDERED>
 __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_n, int splits) {
-  using C = Tile<WK, WT, FK, FT, KU>;
-  constexpr int S = C::S;
+  using C = Tile<WK, WT, FK, FT, S>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
   uint8_t* const lds_w = lds;
   uint8_t* const lds_t = lds + S * C::kWStage;
@@ -227,19 +239,8 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   auto first = [&](int j) { return static_cast<int>(static_cast<int64_t>(quads) * j / splits); };
 
   // What is loaded next: quad lq of item src_p.  Rows beyond the tensor are
-  // clamped (their results are not stored).
-  // Load l of a wave is block kLoads * wave + l of the step's, counted through
-  // the depths: sixteen rows of weights or tokens.
-  const int chunk = 16 * ((lane & 3) ^ (2 * (lane >> 5)));  // byte of the lane's slot (row lane / 4 of 16) in a depth
-  int src_p = p, lq, lq_end;
-  const uint8_t *base_w, *base_t, *base_s;
-  int rows_w, rows_t;
-  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
-  auto depth_w = [&](int l) { return (C::kWLoads * wid + l) / C::kWBlocks; };
-  auto depth_t = [&](int l) { return (C::kTLoads * wid + l) / C::kTBlocks; };
-  // This wave's first group of 64 rows of scales (waves beyond the groups repeat the last).
-  const int group = min(C::kPer * wid, C::kGroups - 1);
-  const bool of_w = group < C::kGroupsW;
+  // clamped (their results are not stored).  Load l of a wave fills eight rows.
+  const int row8 = lane >> 3;
   // (an opaque copy of the lane where its constants are used once a quad or less, so
   // that they are formed there and not kept in registers)
   auto lane_here = [&]() {
@@ -247,8 +248,18 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     asm volatile("" : "+v"(here));
     return here;
   };
+  int src_p = p, lq, lq_end;
+  const uint8_t *base_w, *base_t, *base_s;
+  int rows_w, rows_t;
+  uint32_t size_w, size_t_;
+  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];  // row and chunk of the lane
+  // byte of the lane's chunk in a stage: rows 8 (k wave + l) + lane / 8
+  auto chunk_of = [&](int lines) { return 16 * ((lane & 7) ^ swizzle_of(8 * lines + row8)); };
+  // This wave's first group of 64 rows of scales (waves beyond the groups repeat the last).
+  const int group = min(C::kPer * wid, C::kGroups - 1);
+  const bool of_w = group < C::kGroupsW;
   auto set_source = [&]() {
-    const int lane = lane_here();
+    const int row8 = lane_here() >> 3;
     const int part = SPLIT ? src_p / tiles : 0;
     lq = __builtin_amdgcn_readfirstlane(first(part));
     lq_end = __builtin_amdgcn_readfirstlane(first(part + 1));
@@ -259,17 +270,23 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     rows_t = min(C::kBM, a.T - m0);
     base_w = a.w + static_cast<int64_t>(n0) * a.ldw;
     base_t = a.a + static_cast<int64_t>(m0) * a.lda;
-    base_s = of_w ? a.w_scale + static_cast<int64_t>(n0) * a.ldws : a.scale + static_cast<int64_t>(m0) * a.lds;
+    size_w = static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + bytes;
+    size_t_ = static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + bytes;
+    if (ORDERED)
+      base_s = of_w ? a.w_scale + 1024 * static_cast<int64_t>(quads) * (n0 / 64 + group)
+                    : a.scale + 1024 * static_cast<int64_t>(quads) * (m0 / 64 + group - C::kGroupsW);
+    else
+      base_s = of_w ? a.w_scale + static_cast<int64_t>(n0) * a.ldws : a.scale + static_cast<int64_t>(m0) * a.lds;
 #pragma unroll
     for (int l = 0; l < C::kWLoads; ++l) {
-      const int slot = 16 * ((C::kWLoads * wid + l) % C::kWBlocks) + (lane >> 2);
+      const int slot = 8 * (C::kWLoads * wid + l) + row8;
       const int ch = (slot & ~63) + channel_of((slot >> 4) & 3, slot & 15);
-      off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw) + kDeep * depth_w(l) + chunk;
+      off_w[l] = static_cast<uint32_t>(min(ch, rows_w - 1)) * static_cast<uint32_t>(a.ldw);
     }
 #pragma unroll
     for (int l = 0; l < C::kTLoads; ++l) {
-      const int r = 16 * ((C::kTLoads * wid + l) % C::kTBlocks) + (lane >> 2);
-      off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda) + kDeep * depth_t(l) + chunk;
+      const int r = 8 * (C::kTLoads * wid + l) + row8;
+      off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda);
     }
   };
   int at_quad;  // its first byte in a row
@@ -278,7 +295,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     at_quad = __builtin_amdgcn_readfirstlane(kQuadBytes * (lq == 0 ? quads - 1 : lq - 1));
     left = __builtin_amdgcn_readfirstlane(min(bytes - at_quad, kQuadBytes));
   };
-  // Past the last item the loads go on with that item's: every step issues the
+  // Past the last item the loads go on with that item's: every stage issues the
   // same number, so the vmcnt thresholds are exact.
   auto advance = [&]() {
     lq = __builtin_amdgcn_readfirstlane(lq + 1);
@@ -288,25 +305,34 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     }
     place();
   };
-  // load l of step lj of the quad, into ring position `to`
-  auto issue = [&](int l, int lj, int to) {
+  // The lane's chunk sits in an even or an odd line of eight rows: two values.
+  const int chunk_even = chunk_of(0), chunk_odd = chunk_of(1);
+  // load l of stage j of the quad, into ring position `to`
+  auto issue = [&](int l, int j, int to) {
     const bool w = l < C::kWLoads;
     const int k = w ? l : l - C::kWLoads;
-    const int depth = w ? depth_w(k) : depth_t(k);
-    const uint32_t off = w ? off_w[k] : off_t[k];
-    const uint32_t in = chunk < left - C::kStep * lj - kDeep * depth ? off + C::kStep * lj : off - kDeep * depth - chunk;
+    const int line = (w ? C::kWLoads : C::kTLoads) * wid + k;
+    const int chunk = ((w ? C::kWLoads : C::kTLoads) % 2 == 0 ? k : line) % 2 == 0 ? chunk_even : chunk_odd;
+    const uint32_t in = (w ? off_w[k] : off_t[k]) + (chunk < left - kStage * j ? chunk + kStage * j : 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        w ? wave::buffer_rsrc(base_w, static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + bytes)
-          : wave::buffer_rsrc(base_t, static_cast<uint32_t>(rows_t - 1) * static_cast<uint32_t>(a.lda) + bytes),
-        (__attribute__((address_space(3))) void*)(w ? lds_w + C::kWStage * to + 1024 * (C::kWLoads * wid + k)
-                                                    : lds_t + C::kTStage * to + 1024 * (C::kTLoads * wid + k)),
+        w ? wave::buffer_rsrc(base_w, size_w) : wave::buffer_rsrc(base_t, size_t_),
+        (__attribute__((address_space(3))) void*)((w ? lds_w + C::kWStage * to : lds_t + C::kTStage * to) + 1024 * line),
         16, in, at_quad, 0, 0);
   };
 
   // The scales of the quad, words s = g of the rows; those beyond n read the quad's first.
   uint32_t raw[C::kPer][4];
   int raw_left = 0;
-  auto load_scales = [&]() {
+  auto load_scales = [&](int half) {
+    if (ORDERED) {
+#pragma unroll
+      for (int x = 0; x < C::kPer; ++x)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wave::buffer_rsrc(base_s + 1024 * static_cast<int64_t>(quads) * x, 1024u * static_cast<uint32_t>(quads)),
+            (__attribute__((address_space(3))) void*)(lds_s + half * C::kScales + 1024 * (group + x)), 16, 16 * lane,
+            1024 / kQuadBytes * at_quad, 0, 0);
+      return;
+    }
     const uint32_t ld = static_cast<uint32_t>(of_w ? a.ldws : a.lds);
     const int rows = of_w ? rows_w : rows_t;
     const int here = lane_here(), g = here >> 4, i = here & 15;
@@ -329,123 +355,130 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     uint32_t* const turned = reinterpret_cast<uint32_t*>(lds_s + 1024 * group + 256 * g) + (here & 15);
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x) {
-      const uint32_t(&d)[4] = raw[x];
-      const uint32_t a0 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u);
-      const uint32_t a1 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
-      const uint32_t b0 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
-      const uint32_t b1 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
-      const uint32_t o[4] = {__builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
-                             __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
+      uint32_t o[4];
+      turned_words(raw[x], o);
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         turned[half * (C::kScales / 4) + 256 * x + 16 * b] = 4 * g + b < raw_left ? o[b] : 0;
     }
   };
 
-  const int read_w = 16 * wk * FK * kDeep + i * kDeep + 16 * (g ^ (2 * (i >> 3)));
-  const int read_t = 16 * wt * FT * kDeep + i * kDeep + 16 * (g ^ (2 * (i >> 3)));
-  auto weight = [&](int pos, int depth, int f) {
-    return *reinterpret_cast<const i32x4_t*>(lds_w + C::kWStage * pos + C::kWDeep * depth + read_w + 16 * kDeep * f);
+  // the lane's bytes in a 16-row group: depth 0; depth 1 is chunk ^ 4
+  const int read = i * kStage + 16 * (g ^ swizzle_of(i));
+  const int read_w = 16 * wk * FK * kStage + read, read_t = 16 * wt * FT * kStage + read;
+  auto weight = [&](int pos, int u, int f) {
+    return *reinterpret_cast<const i32x4_t*>(lds_w + C::kWStage * pos + 16 * kStage * f + (read_w ^ (64 * u)));
   };
-  auto token = [&](int pos, int depth, int j) {
-    return *reinterpret_cast<const i32x4_t*>(lds_t + C::kTStage * pos + C::kTDeep * depth + read_t + 16 * kDeep * j);
+  auto token = [&](int pos, int u, int j) {
+    return *reinterpret_cast<const i32x4_t*>(lds_t + C::kTStage * pos + 16 * kStage * j + (read_t ^ (64 * u)));
   };
   // scales of a depth: a word for four of the wave's 16-row groups
   constexpr int kSW = FK / 4, kST = FT >= 4 ? FT / 4 : 1;
   const int scale_w = 1024 * (wk * FK / 4) + 4 * lane;
   const int scale_t = 1024 * (C::kGroupsW + wt * FT / 4) + 4 * lane;
   const int shift_t = FT >= 4 ? 0 : 8 * (wt * FT % 4);  // a wave with fewer than four: its bytes lowest
-  uint32_t sw[kSW], st[kST];
-  auto read_scales = [&](int half, int e) {
+  uint32_t sw[2][kSW], st[2][kST];                      // of this and the next depth
+  auto read_scales = [&](int to, int half, int e) {
 #pragma unroll
     for (int q = 0; q < kSW; ++q)
-      sw[q] = *reinterpret_cast<const uint32_t*>(lds_s + half * C::kScales + scale_w + 1024 * q + 256 * e);
+      sw[to][q] = *reinterpret_cast<const uint32_t*>(lds_s + half * C::kScales + scale_w + 1024 * q + 256 * e);
 #pragma unroll
     for (int q = 0; q < kST; ++q)
-      st[q] = *reinterpret_cast<const uint32_t*>(lds_s + half * C::kScales + scale_t + 1024 * q + 256 * e) >> shift_t;
+      st[to][q] = *reinterpret_cast<const uint32_t*>(lds_s + half * C::kScales + scale_t + 1024 * q + 256 * e) >> shift_t;
   };
 
   f32x4_t acc[FK][FT];
   i32x4_t tok[2][FT];  // token operands of this and the next depth
   i32x4_t wf[FK + 2];
 
+  // Loads of a stage: the first kLate after the barrier that frees its place, in
+  // that stage's last two blocks, the others in the next stage's first blocks.
+  constexpr int kLate = C::kLoads / 2, kEarly = C::kLoads - kLate;
+  static_assert(kEarly <= 2 * FK - 2, "a load a block before the barrier");
+  static_assert(!ORDERED || S == 2, "loaded to LDS in the stage before their quad");
+
+  constexpr int kScaleLoads = (ORDERED ? 1 : 4) * C::kPer;
   set_source();
   place();
-  load_scales();
+  load_scales(0);
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
-    if (s == C::kSteps) {
+  for (int s = 0; s < S; ++s) {
+    if (s == 2) {
       advance();
-      wave::wait_vmcnt<C::kSteps * C::kLoads>();
+      wave::wait_vmcnt<2 * C::kLoads>();
       __builtin_amdgcn_sched_barrier(0);
       turn_scales(0);
-      load_scales();
+      load_scales(1);
     }
 #pragma unroll
-    for (int l = 0; l < C::kLoads; ++l) issue(l, s % C::kSteps, s);
+    for (int l = 0; l < (s == S - 1 ? kLate : C::kLoads); ++l) issue(l, s % 2, s);
   }
-  if (C::kSteps >= S - 1) {
-    wave::wait_vmcnt<(S - 1) * C::kLoads>();
+  if (S == 2 && !ORDERED) {
+    wave::wait_vmcnt<C::kLoads + kLate>();
     __builtin_amdgcn_sched_barrier(0);
     turn_scales(0);
   }
-  wave::wait_vmcnt<(S - 3) * C::kLoads>();
+  wave::wait_vmcnt<(S - 2) * C::kLoads + kLate + (S == 4 ? kScaleLoads : 0)>();
   wave::lds_barrier();
   wf[0] = weight(0, 0, 0);
   wf[1] = weight(0, 0, 1);
 #pragma unroll
   for (int j = 0; j < FT; ++j) tok[0][j] = token(0, 0, j);
+  read_scales(0, 0, 0);
 
-  // Step j of a quad at ring position pos: its depths, and the loads of the step
-  // three ahead, in step 1 the first of a quad.  The scales of a quad's first depth
-  // are read as it starts (published by the barrier before), the others' a depth
-  // ahead.
-  auto step = [&](auto J, int pos, int half) {
+  // Stage j of a quad at ring position pos.
+  auto stage = [&](auto J, int pos, int half) {
     constexpr int j = decltype(J)::value;
-    const int next = (pos + 1) % S, to = (pos + 3) % S;
-    if (j == 0) read_scales(half, 0);
-    if (j == 3 % C::kSteps) turn_scales(half ^ 1);  // loaded two steps ago
-    if (j == 1) load_scales();
-    unrolled<KU>([&](auto UC) {
-      constexpr int u = decltype(UC)::value, e = j * KU + u;
-      i32x4_t(&now)[FT] = tok[e & 1];
-      i32x4_t(&then)[FT] = tok[(e + 1) & 1];
-      const int then_pos = u + 1 < KU ? pos : next, then_depth = u + 1 < KU ? u + 1 : 0;
-      uint32_t cw[kSW], ct[kST];
-#pragma unroll
-      for (int q = 0; q < kSW; ++q) cw[q] = sw[q];
-#pragma unroll
-      for (int q = 0; q < kST; ++q) ct[q] = st[q];
+    const int next = (pos + 1) % S, before = (pos + S - 1) % S;
+    unrolled<2>([&](auto UC) {
+      constexpr int u = decltype(UC)::value;
+      i32x4_t(&now)[FT] = tok[u];
+      i32x4_t(&then)[FT] = tok[u ^ 1];
       unrolled<FK>([&](auto F) {
-        constexpr int f = decltype(F)::value;
+        constexpr int f = decltype(F)::value, b = u * FK + f;
+        if constexpr (b == 2 * FK - 2) {
+          // S = 2: the next stage's loads have landed, S = 4: those of the two after it
+          // may be in flight, with the scales that one of them began with.  The
+          // scales loaded two (S = 2: one) stages ago go to LDS.
+          constexpr bool turn = !ORDERED && j == (S == 2 ? 1 : 0);
+          wave::wait_vmcnt<(S - 2) * C::kLoads + (S == 4 && j == 1 ? kScaleLoads : 0)>();
+          __builtin_amdgcn_sched_barrier(0);
+          if (turn) turn_scales(half ^ 1);
+          wave::lds_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          if (j == 0) {
+            advance();
+            load_scales(half ^ 1);
+          }
+        }
         // The reads follow the block's first MFMA: the wait before that one is
         // then for reads a whole block old.
-        mfma_to<f % 4, 0, C::kAgpr>(acc[f][0], wf[f], now[0], cw[f / 4], ct[0]);
+        mfma_to<f % 4, 0, C::kAgpr>(acc[f][0], wf[f], now[0], sw[u][f / 4], st[u][0]);
         __builtin_amdgcn_sched_barrier(0);
-        // two reads ahead, the last two from the next depth or step
-        wf[f + 2] = f + 2 < FK ? weight(pos, u, f + 2) : weight(then_pos, then_depth, f + 2 - FK);
+        wf[f + 2] = f + 2 < FK ? weight(pos, u, f + 2) : weight(u == 0 ? pos : next, u ^ 1, f + 2 - FK);
+        if (u == 0) {
 #pragma unroll
-        for (int t = f * FT / FK; t < (f + 1) * FT / FK; ++t) then[t] = token(then_pos, then_depth, t);
-        if (f == FK - 1 && e + 1 < kQuad) read_scales(half, e + 1);
-        constexpr int kBlocks = KU * FK, b = u * FK + f;
+          for (int t = f * FT / FK; t < (f + 1) * FT / FK; ++t) then[t] = token(pos, 1, t);
+          if (f == FK - 1) read_scales(1, half, 2 * j + 1);
+        } else if (f >= FK - 2) {
 #pragma unroll
-        for (int l = b * C::kLoads / kBlocks; l < (b + 1) * C::kLoads / kBlocks; ++l) issue(l, (j + 3) % C::kSteps, to);
+          for (int t = (f - FK + 2) * FT / 2; t < (f - FK + 3) * FT / 2; ++t) then[t] = token(next, 0, t);
+          if (f == FK - 1) read_scales(0, half ^ j, 2 * (j ^ 1));
+        }
+        if (b < kEarly) issue(kLate + b, j ^ 1, before);
+        if (b >= 2 * FK - 2) {
+#pragma unroll
+          for (int l = (b - 2 * FK + 2) * kLate / 2; l < (b - 2 * FK + 3) * kLate / 2; ++l) issue(l, j, pos);
+        }
         unrolled<FT - 1>([&](auto T) {
           constexpr int t = decltype(T)::value + 1;
-          mfma_to<f % 4, t % 4, C::kAgpr>(acc[f][t], wf[f], now[t], cw[f / 4], ct[t / 4]);
+          mfma_to<f % 4, t % 4, C::kAgpr>(acc[f][t], wf[f], now[t], sw[u][f / 4], st[u][t / 4]);
         });
         __builtin_amdgcn_sched_barrier(0);
       });
       wf[0] = wf[FK];
       wf[1] = wf[FK + 1];
     });
-    if (j == 0) advance();
-    wave::wait_vmcnt<(S - 3) * C::kLoads + (j == 1 ? 4 * C::kPer : 0)>();
-    if (j == 3 % C::kSteps)
-      wave::lds_barrier();  // the scales are written
-    else
-      __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
   };
 
   int pos = 0, half = 0;
@@ -461,8 +494,8 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     const int count = first(part + 1) - first(part);
 #pragma clang loop unroll(disable)
     for (int q = 0; q < count; ++q) {
-      unrolled<C::kSteps>([&](auto J) { step(J, (C::kSteps == S ? 0 : pos) + J, half); });
-      if (C::kSteps != S) pos ^= C::kSteps;
+      unrolled<2>([&](auto J) { stage(J, (S == 2 ? 0 : pos) + J, half); });
+      if (S != 2) pos ^= 2;
       half ^= 1;
     }
 
@@ -480,17 +513,13 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
 
     // Lane (g, i): token 16 j + i, channels 8 g .. 8 g + 7 of every 32.  Stored from
     // there, neighbouring lanes would write sixteen rows, 16 bytes a request; so
-    // sixteen rows of 128 bytes at a time, a unit, go through LDS and leave as whole
-    // lines: through the places that the wave itself fills next in the ring position
-    // of the last step, which all waves have done with.  Chunk c of row r sits at
-    // chunk c ^ ((r >> 1) & 7): the sixteen lanes that an access serves at a time
-    // cover the banks once.  Units alternate between two places; a wave's LDS
-    // accesses are done in order, so that the next unit is written before this
-    // one has been read back.
-    const int last = C::kSteps == S ? S - 1 : (pos ^ C::kSteps) + C::kSteps - 1;
-    auto chunk_at = [&](int odd, int r, int c) {
-      uint8_t* const mine = odd ? lds_t + C::kTStage * last + 1024 * C::kTLoads * wid
-                                : lds_w + C::kWStage * last + 1024 * C::kWLoads * wid;
+    // sixteen rows of 128 bytes at a time, a unit, go through 2 KiB of LDS of the
+    // wave's own and leave as whole lines.  Chunk c of row r sits at chunk
+    // c ^ ((r >> 1) & 7): the sixteen lanes that an access serves at a time cover the
+    // banks once.  A wave's LDS accesses are done in order, so the next unit is
+    // written as soon as the reads of this one are on their way.
+    uint8_t* const mine = lds + C::kRing + 2 * C::kScales + 2048 * wid;
+    auto chunk_at = [&](int r, int c) {
       return reinterpret_cast<wave::u32x4_t*>(mine + 128 * r + 16 * (c ^ ((r >> 1) & 7)));
     };
     const int t_wave = m0 + 16 * wt * FT, k_wave = n0 + 16 * wk * FK;
@@ -507,32 +536,25 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           bias[q][e] = a.bias[min(k_wave + 64 * q + 32 * (e >> 3) + 8 * g + (e & 7), a.R - 1)];
     }
     auto results = [&](auto BF16) {
-      constexpr int per = BF16 ? 8 : 4;                   // results of a chunk
-      constexpr int parts = BF16 ? 1 : 2;                 // units of 64 channels
+      constexpr int per = BF16 ? 8 : 4;    // results of a chunk
+      constexpr int parts = BF16 ? 1 : 2;  // units of 64 channels
       constexpr int units = FK / 4 * FT * parts;
       auto put = [&](auto U) {
         constexpr int u = decltype(U)::value, part = u % parts, j = u / parts % FT, q = u / parts / FT;
-        if constexpr (BF16) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wave::u32x4_t v;
+        for (int h = 0; h < 2; ++h) {
+          wave::u32x4_t v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (BF16)
               v[e] = row::pack_bf16(
                   value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1)]) + bias[q][8 * h + 2 * e],
                   value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1) + 1]) + bias[q][8 * h + 2 * e + 1]);
-            *chunk_at(u & 1, i, 4 * h + g) = v;
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wave::u32x4_t v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
+            else
               v[e] = __float_as_uint(value_of<C::kAgpr>(acc[4 * q + 2 * part + h][j][e]) +
                                      bias[q][8 * part + 4 * h + e]);
-            *chunk_at(u & 1, i, 2 * g + h) = v;
           }
+          *chunk_at(i, BF16 ? 4 * h + g : 2 * g + h) = v;
         }
       };
       const int r0 = lane >> 3, c = lane & 7;
@@ -561,14 +583,13 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           }
         }
       };
-      put(std::integral_constant<int, 0>{});
       unrolled<units>([&](auto U) {
         constexpr int u = decltype(U)::value;
-        if constexpr (u + 1 < units) put(std::integral_constant<int, u + 1>{});
+        put(U);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) got[u & 1][h] = *chunk_at(u & 1, 8 * h + r0, c);
+        for (int h = 0; h < 2; ++h) got[u & 1][h] = *chunk_at(8 * h + r0, c);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if constexpr (u > 0) send(std::integral_constant<int, u - 1>{});
@@ -583,18 +604,60 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   wave::wait_vmcnt<0>();
 }
 
-template <int WK, int WT, int FK, int FT, int KU, bool SPLIT>
+// Scales of all 64-row groups of tokens and weights in the order that the tiles
+// read them, [group][quad][depth][lane]: a wave takes a group and a quad.  Blocks
+// beyond n get 2^-127.
+struct Order {
+  const uint8_t* src[2];  // tokens, weights
+  int64_t ld[2];
+  uint8_t* dst[2];
+  int rows[2], groups[2];
+  int blocks, quads;
+  int words;  // 1: rows of aligned words
+};
+__global__ __launch_bounds__(256) void mx_order_kernel(Order o) {
+  const int lane = threadIdx.x & 63, s = lane >> 4, i = lane & 15;
+  const int q = 4 * static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x >> 6);
+  if (q >= o.quads) return;
+  const int total = o.groups[0] + o.groups[1];
+  for (int g = blockIdx.y; g < total; g += gridDim.y) {
+    const int of_w = g >= o.groups[0];
+    const int group = of_w ? g - o.groups[0] : g;
+    const int at = 16 * q + 4 * s;
+    uint32_t d[4], t[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int r = min(64 * group + (of_w ? channel_of(f, i) : 16 * f + i), o.rows[of_w] - 1);
+      const uint8_t* const p = o.src[of_w] + r * o.ld[of_w] + at;
+      d[f] = 0;
+      if (o.words) {
+        if (at < o.blocks) d[f] = *reinterpret_cast<const uint32_t*>(p);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (at + b < o.blocks) d[f] |= static_cast<uint32_t>(p[b]) << (8 * b);
+      }
+    }
+    turned_words(d, t);
+    uint32_t* const to = reinterpret_cast<uint32_t*>(o.dst[of_w] + 1024 * (static_cast<int64_t>(group) * o.quads + q)) +
+                         64 * s + i;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) to[16 * b] = at + b < o.blocks ? t[b] : 0;
+  }
+}
+
+template <int WK, int WT, int FK, int FT, int S, bool SPLIT, bool ORDERED>
 __global__ __launch_bounds__(64 * WK * WT) __attribute__((
-    amdgpu_waves_per_eu(Tile<WK, WT, FK, FT, KU>::kWaves * Tile<WK, WT, FK, FT, KU>::kFit / 4)))
+    amdgpu_waves_per_eu(Tile<WK, WT, FK, FT, S>::kWaves * Tile<WK, WT, FK, FT, S>::kFit / 4)))
 void mx_tile_kernel(MxArgs a, int tiles_m, int tiles_n, int splits) {
-  mx_tile<WK, WT, FK, FT, KU, SPLIT>(a, tiles_m, tiles_n, SPLIT ? splits : 1);
+  mx_tile<WK, WT, FK, FT, S, SPLIT, ORDERED>(a, tiles_m, tiles_n, SPLIT ? splits : 1);
 }
 
 // Sums the parts of a tile's results and finishes them: a thread takes one
 // lane's four channels of a 16 x 16 result.
-template <int WK, int WT, int FK, int FT, int KU>
+template <int WK, int WT, int FK, int FT, int S>
 __global__ __launch_bounds__(256) void mx_join_kernel(MxArgs a, int tiles_m, int tiles_n, int splits) {
-  using C = Tile<WK, WT, FK, FT, KU>;
+  using C = Tile<WK, WT, FK, FT, S>;
   const int tiles = tiles_m * tiles_n;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // f32x4 of a part
   const int tile = static_cast<int>(e / (C::kPart / 4));
@@ -615,22 +678,22 @@ __global__ __launch_bounds__(256) void mx_join_kernel(MxArgs a, int tiles_m, int
   store_results(a, t, k, o);
 }
 
-template <int WK, int WT, int FK, int FT, int KU>
-hipError_t run_tile(const MxArgs& a, int splits, hipStream_t s) {
-  using C = Tile<WK, WT, FK, FT, KU>;
+template <int WK, int WT, int FK, int FT, int S, bool ORDERED>
+hipError_t run_tile(const MxArgs& a, int splits, hipStream_t stream) {
+  using C = Tile<WK, WT, FK, FT, S>;
   const int tiles_m = (a.T + C::kBM - 1) / C::kBM, tiles_n = (a.R + C::kBN - 1) / C::kBN;
   const int items = tiles_m * tiles_n * splits;
   const int most = (device_cu_count() & ~7) * C::kFit;
   const dim3 grid(static_cast<unsigned>(most > 0 && items > most ? most : items)), block(C::kThreads);
   if (splits == 1) {
-    mx_tile_kernel<WK, WT, FK, FT, KU, false><<<grid, block, 0, s>>>(a, tiles_m, tiles_n, 1);
+    mx_tile_kernel<WK, WT, FK, FT, S, false, ORDERED><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n, 1);
     return hipGetLastError();
   }
-  mx_tile_kernel<WK, WT, FK, FT, KU, true><<<grid, block, 0, s>>>(a, tiles_m, tiles_n, splits);
+  mx_tile_kernel<WK, WT, FK, FT, S, true, ORDERED><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n, splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  mx_join_kernel<WK, WT, FK, FT, KU><<<dim3(static_cast<unsigned>(tiles_m * tiles_n * (C::kPart / 1024))), dim3(256), 0,
-                                       s>>>(a, tiles_m, tiles_n, splits);
+  mx_join_kernel<WK, WT, FK, FT, S><<<dim3(static_cast<unsigned>(tiles_m * tiles_n * (C::kPart / 1024))), dim3(256), 0,
+                                       stream>>>(a, tiles_m, tiles_n, splits);
   return hipGetLastError();
 }
 
@@ -711,23 +774,48 @@ bool aligned_rows(const uint8_t* p, int64_t ld, int64_t to) {
   return ld % to == 0 && (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0 && ld < kMaxPitch;
 }
 
-// The copies that the operands need, from `at` of the workspace on; a takes them.
-int lay_out(MxArgs& a, int64_t& at, Copies& all) {
+// The workspace after the partial sums: the copies that the operands need and, for
+// tiles that take them so, the ordered scales.  a takes what is laid out anew.
+struct Layout {
+  Copies copies = {};
   int count = 0;
-  auto need = [&](const uint8_t*& p, int64_t& ld, int64_t rows, int bytes, int64_t to) {
+  Order order = {};
+  int64_t end = 0;
+  Layout(MxArgs& a, int64_t at, bool ordered) : end(at) {
+    copy(a, a.a, a.lda, a.T, a.n / 2, 16);
+    copy(a, a.w, a.ldw, a.R, a.n / 2, 16);
+    if (!ordered) {
+      copy(a, a.scale, a.lds, a.T, a.n / 32, 4);
+      copy(a, a.w_scale, a.ldws, a.R, a.n / 32, 4);
+      return;
+    }
+    order.blocks = a.n / mx::kBlock;
+    order.quads = (order.blocks + 15) / 16;
+    order.words = aligned_rows(a.scale, a.lds, 4) && aligned_rows(a.w_scale, a.ldws, 4);
+    end = (end + 15) & ~int64_t{15};
+    sort(a, 0, a.scale, a.lds, a.T);
+    sort(a, 1, a.w_scale, a.ldws, a.R);
+  }
+
+ private:
+  void copy(const MxArgs& a, const uint8_t*& p, int64_t& ld, int64_t rows, int bytes, int64_t to) {
     if (aligned_rows(p, ld, to)) return;
-    uint8_t* const dst = a.workspace + at;
-    all.c[count++] = {p, ld, dst, rows, bytes};
+    uint8_t* const dst = a.workspace + end;
+    copies.c[count++] = {p, ld, dst, rows, bytes};
     p = dst;
     ld = copy_pitch(bytes);
-    at += rows * ld;
-  };
-  need(a.a, a.lda, a.T, a.n / 2, 16);
-  need(a.scale, a.lds, a.T, a.n / 32, 4);
-  need(a.w, a.ldw, a.R, a.n / 2, 16);
-  need(a.w_scale, a.ldws, a.R, a.n / 32, 4);
-  return count;
-}
+    end += rows * ld;
+  }
+  void sort(const MxArgs& a, int k, const uint8_t*& p, int64_t ld, int rows) {
+    order.src[k] = p;
+    order.ld[k] = ld;
+    order.dst[k] = a.workspace + end;
+    order.rows[k] = rows;
+    order.groups[k] = (rows + 255) / 256 * 4;  // whole tiles
+    p = order.dst[k];
+    end += int64_t{1024} * order.quads * order.groups[k];
+  }
+};
 
 int64_t partial_bytes(const MxArgs& a) {
   const Plan p = tile_plan(a.T, a.n, a.R);
@@ -743,10 +831,7 @@ int64_t mx_workspace(const MxArgs& a) {
   if (a.T == 0 || a.R == 0) return 0;
   MxArgs b = a;
   b.workspace = nullptr;
-  Copies all;
-  int64_t at = partial_bytes(a);
-  lay_out(b, at, all);
-  return at;
+  return Layout(b, partial_bytes(a), tile_plan(a.T, a.n, a.R).kind == 0).end;
 }
 
 const char* mx_name(const MxArgs& a) {
@@ -757,19 +842,25 @@ const char* mx_name(const MxArgs& a) {
 hipError_t launch_mx(const MxArgs& args, hipStream_t s) {
   MxArgs a = args;
   const Plan plan = tile_plan(a.T, a.n, a.R);
-  Copies all = {};
-  int64_t at = partial_bytes(a);
-  const int copies = lay_out(a, at, all);
-  if (copies > 0) {
-    mx_copy_kernel<<<dim3(1024, static_cast<unsigned>(copies)), 256, 0, s>>>(all);
+  const Layout lay(a, partial_bytes(args), plan.kind == 0);
+  if (lay.count > 0) {
+    mx_copy_kernel<<<dim3(1024, static_cast<unsigned>(lay.count)), 256, 0, s>>>(lay.copies);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (plan.kind == 0) {
+    const int groups = lay.order.groups[0] + lay.order.groups[1];
+    mx_order_kernel<<<dim3(static_cast<unsigned>((lay.order.quads + 3) / 4),
+                           static_cast<unsigned>(groups < 65535 ? groups : 65535)),
+                      256, 0, s>>>(lay.order);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   switch (plan.kind) {
-    case 0: return run_tile<4, 2, 4, 8, 1>(a, plan.splits, s);
-    case 1: return run_tile<2, 2, 4, 4, 2>(a, plan.splits, s);
-    case 2: return run_tile<2, 2, 4, 2, 2>(a, plan.splits, s);
-    default: return run_tile<1, 4, 4, 1, 2>(a, plan.splits, s);
+    case 0: return run_tile<4, 2, 4, 8, 2, true>(a, plan.splits, s);
+    case 1: return run_tile<2, 2, 4, 4, 4, false>(a, plan.splits, s);
+    case 2: return run_tile<2, 2, 4, 2, 4, false>(a, plan.splits, s);
+    default: return run_tile<1, 4, 4, 1, 4, false>(a, plan.splits, s);
   }
 }
 
