@@ -731,6 +731,189 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R) {
   return best;
 }
 
+// ---- few tokens ---------------------------------------------------------------
+//
+// The weights are read once and bound the time.  A work-group takes 16 FK
+// channels and all tokens (FT groups of sixteen); its waves share the row: wave w
+// takes the 128-byte units w, w + waves, ... of the codes (eight blocks), so that
+// the work-group reads its rows side by side.  Each wave has a ring of D units of
+// its own in LDS, codes and scales, and waits for its own loads only; the partial
+// sums meet in LDS at the end, joined in the waves' order.
+//
+// The loads go through LDS because a lane (g, i) holds 16 bytes of row i: sixteen
+// neighbouring lanes would read sixteen rows, 64 cache accesses an instruction
+// instead of eight whole lines.
+//
+// LDS rows of 128 bytes: chunk c of row r sits at chunk c ^ h(r), h(r) = (r & 7) ^
+// ((r >> 3) & 1): lane (g, i) reads chunks 2 g and 2 g + 1 of row i, the sixteen
+// lanes a read serves at a time on banks of their own.  So its blocks of MFMA s = 0,
+// 1 are 2 g + s, and their scales the bytes of one 16-bit word; a row's eight
+// scales of a unit are loaded as two words.  Beyond n the codes are the unit's
+// first and the scales of both operands 2^-127: products that are zero in binary32.
+constexpr int kUnit = 128;
+
+template <int FK, int FT, int D>
+struct Few {
+  static constexpr int kWBytes = 16 * FK * kUnit, kTBytes = 16 * FT * kUnit;
+  static constexpr int kWLoads = kWBytes / 1024, kTLoads = kTBytes / 1024;
+  static constexpr int kSLoads = (32 * (FK + FT) + 63) / 64;  // of 64 words of scales
+  static constexpr int kLoads = kWLoads + kTLoads + kSLoads;
+  static constexpr int kSlot = kWBytes + kTBytes + 256 * kSLoads;
+  static constexpr int kPart = 1024 * FK * FT;  // bytes of a wave's partial sums
+  static constexpr int kWave = D * kSlot + kPart;
+  static_assert(8 * kWave <= 160 * 1024, "eight waves");
+};
+
+template <int FK, int FT, int D>
+__device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
+  using C = Few<FK, FT, D>;
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int g = lane >> 4, i = lane & 15;
+  const int n0 = 16 * FK * blockIdx.x;
+  const int bytes = a.n / 2, blocks = a.n / mx::kBlock;
+  const int units = (bytes + kUnit - 1) / kUnit;
+  const int count = units > wid ? (units - wid - 1) / waves + 1 : 0;
+  uint8_t* const ring = few_lds + wid * D * C::kSlot;
+  float* const part = reinterpret_cast<float*>(few_lds + waves * D * C::kSlot);
+
+  // rows and tokens beyond the tensors are clamped (their results are not stored)
+  const int rows_w = min(16 * FK, a.R - n0);
+  const __amdgpu_buffer_rsrc_t src_w =
+      wave::buffer_rsrc(a.w + static_cast<int64_t>(n0) * a.ldw,
+                        static_cast<uint32_t>(rows_w - 1) * static_cast<uint32_t>(a.ldw) + bytes);
+  const __amdgpu_buffer_rsrc_t src_t =
+      wave::buffer_rsrc(a.a, static_cast<uint32_t>(a.T - 1) * static_cast<uint32_t>(a.lda) + bytes);
+  auto h = [](int r) { return (r & 7) ^ ((r >> 3) & 1); };
+  // sources of the lane: load l of either operand fills rows 8 l .. 8 l + 7
+  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];
+  auto chunk_at = [&](int l) { return 16 * ((lane & 7) ^ h((8 * l + (lane >> 3)) & 15)); };
+#pragma unroll
+  for (int l = 0; l < C::kWLoads; ++l)
+    off_w[l] = static_cast<uint32_t>(min(8 * l + (lane >> 3), rows_w - 1)) * static_cast<uint32_t>(a.ldw);
+#pragma unroll
+  for (int l = 0; l < C::kTLoads; ++l)
+    off_t[l] = static_cast<uint32_t>(min(8 * l + (lane >> 3), a.T - 1)) * static_cast<uint32_t>(a.lda);
+  // words of scales: two a row, weights' rows first
+  const uint8_t* src_s[C::kSLoads];
+#pragma unroll
+  for (int q = 0; q < C::kSLoads; ++q) {
+    const int r = (64 * q + lane) >> 1;
+    src_s[q] = r < 16 * FK ? a.w_scale + static_cast<int64_t>(n0 + min(r, rows_w - 1)) * a.ldws
+                           : a.scale + static_cast<int64_t>(min(r - 16 * FK, a.T - 1)) * a.lds;
+  }
+  // unit x of this wave into ring slot x % D
+  auto issue = [&](int x) {
+    const int u = wid + x * waves;
+    const int left = bytes - u * kUnit;
+    uint8_t* const slot = ring + (x % D) * C::kSlot;
+#pragma unroll
+    for (int l = 0; l < C::kWLoads; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src_w, (__attribute__((address_space(3))) void*)(slot + 1024 * l), 16,
+                                               off_w[l] + (chunk_at(l) < left ? chunk_at(l) : 0), kUnit * u, 0, 0);
+#pragma unroll
+    for (int l = 0; l < C::kTLoads; ++l)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src_t,
+                                               (__attribute__((address_space(3))) void*)(slot + C::kWBytes + 1024 * l), 16,
+                                               off_t[l] + (chunk_at(l) < left ? chunk_at(l) : 0), kUnit * u, 0, 0);
+    const int word = 4 * (lane & 1);
+#pragma unroll
+    for (int q = 0; q < C::kSLoads; ++q)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(src_s[q] + 8 * u + (word < left / mx::kBlockBytes ? word : 0)),
+          (__attribute__((address_space(3))) void*)(slot + C::kWBytes + C::kTBytes + 256 * q), 4, 0, 0);
+  };
+
+  f32x4_t acc[FK][FT];
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[f][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int x = 0; x < min(D, count); ++x) issue(x);
+  for (int x = 0; x < count; ++x) {
+    if (x + D <= count)
+      wave::wait_vmcnt<(D - 1) * C::kLoads>();
+    else
+      wave::wait_vmcnt<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* const sw = ring + (x % D) * C::kSlot;
+    const uint8_t* const st = sw + C::kWBytes;
+    const uint8_t* const ss = st + C::kTBytes;
+    i32x4_t w[2][FK], tok[2][FT];
+    uint32_t cw[FK], ct[FT];
+#pragma unroll
+    for (int f = 0; f < FK; ++f) cw[f] = *reinterpret_cast<const uint16_t*>(ss + 8 * (16 * f + i) + 2 * g);
+#pragma unroll
+    for (int j = 0; j < FT; ++j) ct[j] = *reinterpret_cast<const uint16_t*>(ss + 8 * (16 * (FK + j) + i) + 2 * g);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int f = 0; f < FK; ++f)
+        w[s][f] = *reinterpret_cast<const i32x4_t*>(sw + 2048 * f + kUnit * i + 16 * ((2 * g + s) ^ h(i)));
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        tok[s][j] = *reinterpret_cast<const i32x4_t*>(st + 2048 * j + kUnit * i + 16 * ((2 * g + s) ^ h(i)));
+    }
+    const int here = blocks - 8 * (wid + x * waves);  // blocks from this unit on
+    if (here < 8) {
+      const uint32_t keep = 2 * g + 1 < here ? 0xffffu : 2 * g < here ? 0xffu : 0u;
+#pragma unroll
+      for (int f = 0; f < FK; ++f) cw[f] &= keep;
+#pragma unroll
+      for (int j = 0; j < FT; ++j) ct[j] &= keep;
+    }
+#pragma unroll
+    for (int f = 0; f < FK; ++f)
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        acc[f][j] = mfma<0, 0>(w[0][f], tok[0][j], acc[f][j], cw[f], ct[j]);
+        acc[f][j] = mfma<1, 1>(w[1][f], tok[1][j], acc[f][j], cw[f], ct[j]);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    if (x + D < count) issue(x + D);
+  }
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+      *reinterpret_cast<f32x4_t*>(part + 4 * (((wid * FK + f) * FT + j) * 64 + lane)) = acc[f][j];
+  __syncthreads();
+  // sums [wave][FK][FT][64][4]: result e is channel e % 4 + 4 (e / 64 % 4) of group
+  // e / 256 / FT, token e / 4 % 16 of group e / 256 % FT
+  for (int e = threadIdx.x; e < 256 * FK * FT; e += blockDim.x) {
+    const int k = n0 + 16 * ((e >> 8) / FT) + (e & 3) + 4 * ((e >> 6) & 3);
+    const int t = 16 * ((e >> 8) % FT) + ((e >> 2) & 15);
+    if (k >= a.R || t >= a.T) continue;
+    float sum = part[e];
+    for (int v = 1; v < waves; ++v) sum += part[256 * FK * FT * v + e];
+    row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, sum + (a.bias ? a.bias[k] : 0.f), a.out_bf16);
+  }
+}
+
+template <int FK, int FT, int D>
+__global__ __launch_bounds__(512) void mx_few_kernel(MxArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
+  mx_few<FK, FT, D>(a, few_lds);
+}
+
+template <int FK, int FT, int D>
+hipError_t run_few_as(const MxArgs& a, hipStream_t s) {
+  using C = Few<FK, FT, D>;
+  const int groups = (a.R + 16 * FK - 1) / (16 * FK), units = (a.n / 2 + kUnit - 1) / kUnit;
+  int waves = 8;
+  while (waves > 2 && (groups * waves > 8 * kCus || units < waves)) waves /= 2;
+  mx_few_kernel<FK, FT, D><<<dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(64 * waves)),
+                            static_cast<unsigned>(waves * C::kWave), s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t run_few(const MxArgs& a, hipStream_t s) {
+  return a.T <= 16 ? run_few_as<1, 1, 4>(a, s) : run_few_as<1, 2, 2>(a, s);
+}
+
+bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24); }
+
 constexpr int64_t kMaxPitch = 1 << 23;  // a tile's offsets stay below 2^32
 
 // ---- any stride and alignment ---------------------------------------------------
@@ -817,7 +1000,10 @@ struct Layout {
   }
 };
 
+bool takes_ordered(const MxArgs& a) { return !takes_few(a.T, a.R) && tile_plan(a.T, a.n, a.R).kind == 0; }
+
 int64_t partial_bytes(const MxArgs& a) {
+  if (takes_few(a.T, a.R)) return 0;
   const Plan p = tile_plan(a.T, a.n, a.R);
   if (p.splits == 1) return 0;
   const TileCost& t = kTiles[p.kind];
@@ -831,24 +1017,27 @@ int64_t mx_workspace(const MxArgs& a) {
   if (a.T == 0 || a.R == 0) return 0;
   MxArgs b = a;
   b.workspace = nullptr;
-  return Layout(b, partial_bytes(a), tile_plan(a.T, a.n, a.R).kind == 0).end;
+  return Layout(b, partial_bytes(a), takes_ordered(a)).end;
 }
 
 const char* mx_name(const MxArgs& a) {
   static const char* const names[] = {"mx_tile256x256", "mx_tile128x128", "mx_tile64x128", "mx_tile64x64"};
+  if (takes_few(a.T, a.R)) return a.T <= 16 ? "mx_few16" : "mx_few32";
   return names[tile_plan(a.T, a.n, a.R).kind];
 }
 
 hipError_t launch_mx(const MxArgs& args, hipStream_t s) {
   MxArgs a = args;
-  const Plan plan = tile_plan(a.T, a.n, a.R);
-  const Layout lay(a, partial_bytes(args), plan.kind == 0);
+  const bool ordered = takes_ordered(args);
+  const Layout lay(a, partial_bytes(args), ordered);
   if (lay.count > 0) {
     mx_copy_kernel<<<dim3(1024, static_cast<unsigned>(lay.count)), 256, 0, s>>>(lay.copies);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (plan.kind == 0) {
+  if (takes_few(a.T, a.R)) return run_few(a, s);
+  const Plan plan = tile_plan(a.T, a.n, a.R);
+  if (ordered) {
     const int groups = lay.order.groups[0] + lay.order.groups[1];
     mx_order_kernel<<<dim3(static_cast<unsigned>((lay.order.quads + 3) / 4),
                            static_cast<unsigned>(groups < 65535 ? groups : 65535)),
