@@ -251,8 +251,9 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   int src_p = p, lq, lq_end;
   const uint8_t *base_w, *base_t, *base_s;
   int rows_w, rows_t;
-  uint32_t size_w, size_t_;
-  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];  // row and chunk of the lane
+  uint32_t size_w, size_t_, size_s;
+  uint32_t off_w[C::kWLoads], off_t[C::kTLoads];  // of the lane's rows
+  uint32_t off_s[C::kPer][4];                     // of its rows of scales
   // byte of the lane's chunk in a stage: rows 8 (k wave + l) + lane / 8
   auto chunk_of = [&](int lines) { return 16 * ((lane & 7) ^ swizzle_of(8 * lines + row8)); };
   // This wave's first group of 64 rows of scales (waves beyond the groups repeat the last).
@@ -288,6 +289,18 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       const int r = 8 * (C::kTLoads * wid + l) + row8;
       off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda);
     }
+    if (ORDERED) return;
+    size_s = static_cast<uint32_t>((of_w ? rows_w : rows_t) - 1) * static_cast<uint32_t>(of_w ? a.ldws : a.lds) +
+             ((blocks + 3) & ~3);
+    const int i = lane_here() & 15;
+#pragma unroll
+    for (int x = 0; x < C::kPer; ++x)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int r = 64 * (group + x - (of_w ? 0 : C::kGroupsW)) + (of_w ? channel_of(f, i) : 16 * f + i);
+        off_s[x][f] =
+            static_cast<uint32_t>(min(r, (of_w ? rows_w : rows_t) - 1)) * static_cast<uint32_t>(of_w ? a.ldws : a.lds);
+      }
   };
   int at_quad;  // its first byte in a row
   int left;     // bytes of it
@@ -333,26 +346,17 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
             1024 / kQuadBytes * at_quad, 0, 0);
       return;
     }
-    const uint32_t ld = static_cast<uint32_t>(of_w ? a.ldws : a.lds);
-    const int rows = of_w ? rows_w : rows_t;
-    const int here = lane_here(), g = here >> 4, i = here & 15;
-    const int r0 = 64 * (of_w ? group : group - C::kGroupsW);
     raw_left = left / mx::kBlockBytes;
     const uint32_t word = 4 * g < raw_left ? 4 * g : 0;
-    const __amdgpu_buffer_rsrc_t src =
-        wave::buffer_rsrc(base_s, static_cast<uint32_t>(rows - 1) * ld + ((blocks + 3) & ~3));
+    const __amdgpu_buffer_rsrc_t src = wave::buffer_rsrc(base_s, size_s);
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x)
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int r = r0 + 64 * x + (of_w ? channel_of(f, i) : 16 * f + i);
-        raw[x][f] = __builtin_amdgcn_raw_buffer_load_b32(src, static_cast<uint32_t>(min(r, rows - 1)) * ld + word,
-                                                         at_quad / mx::kBlockBytes, 0);
-      }
+      for (int f = 0; f < 4; ++f)
+        raw[x][f] = __builtin_amdgcn_raw_buffer_load_b32(src, off_s[x][f] + word, at_quad / mx::kBlockBytes, 0);
   };
   auto turn_scales = [&](int half) {
-    const int here = lane_here(), g = here >> 4;
-    uint32_t* const turned = reinterpret_cast<uint32_t*>(lds_s + 1024 * group + 256 * g) + (here & 15);
+    uint32_t* const turned = reinterpret_cast<uint32_t*>(lds_s + 1024 * group + 256 * g) + i;
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x) {
       uint32_t o[4];
@@ -697,34 +701,43 @@ hipError_t run_tile(const MxArgs& a, int splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The tiles there are, and what they cost: microseconds for a quad with one
+// work-group on a CU and with two side by side, and for a tile's start and stores,
+// fitted to 1021 timings of 23 shapes (40 x 4096 x 4096 to 8192 x 4096 x 4096; 9 %
+// rms) beside the call's 5.5 us.  The least estimate picked the fastest of the timed
+// choices or one within 3 % of it at 22 of them (128 x 14336 x 4096 20.0 us, the
+// best 19.1).
 struct TileCost {
   int bm, bn, fit;
   double one, two, tile;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.35, 0, 2.8},      // 4 x 2 waves of 64 channels x 128 tokens
-                               {128, 128, 1, 0.453, 0, 1.4},     // 2 x 2 waves of 64 x 64
-                               {64, 128, 1, 0.280, 0, 1.2},      // 2 x 2 waves of 64 x 32
-                               {64, 64, 2, 0.184, 0.341, 1.4}};  // 1 x 4 waves of 64 x 16
+constexpr TileCost kTiles[] = {{256, 256, 1, 3.2, 0, 6.0},       // 4 x 2 waves of 64 channels x 128 tokens
+                               {128, 128, 1, 1.38, 0, 0.63},     // 2 x 2 waves of 64 x 64, four stages
+                               {128, 128, 2, 1.65, 2.66, 0.44},  // the same, two stages
+                               {64, 128, 1, 1.10, 0, 0.58},      // 2 x 2 waves of 64 x 32
+                               {64, 64, 2, 0.88, 1.54, 0.84}};   // 1 x 4 waves of 64 x 16
 
 struct Plan {
   int kind, splits;
   double us;
 };
 
+// The least estimate over the tiles and over parts of the row joined by a second
+// kernel (3.4 us, and 3.6 TB/s over the partial sums), or what the bytes take.
 Plan tile_plan(int64_t T, int64_t n, int64_t R) {
   Plan best{0, 1, 1e30};
   const double bytes = static_cast<double>(T + R) * n * 17 / 32 + 2.0 * T * R;
-  for (int c = 0; c < 4; ++c) {
+  const int64_t quads = (n + 511) / 512;
+  for (int c = 0; c < 5; ++c) {
     const TileCost& t = kTiles[c];
     const double tiles = static_cast<double>((T + t.bm - 1) / t.bm) * static_cast<double>((R + t.bn - 1) / t.bn);
-    const int64_t quads = (n + 511) / 512;
     for (const int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (splits > 1 && (splits > quads || tiles * splits > 4 * kCus)) break;
       const double per_cu = ceil(tiles * splits / kCus);
-      const double k = 2.0 * quads / splits;  // 256 channels
+      const double k = static_cast<double>(quads) / splits;
       double us = t.fit == 1 ? per_cu * (k * t.one + t.tile)
                              : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
-      us = fmax(us, bytes / 7e6) + (splits > 1 ? 3.5 + tiles * splits * t.bm * t.bn * 4 / 3.3e6 : 0);
+      us = fmax(us, bytes / 6.6e6) + (splits > 1 ? 3.4 + tiles * splits * t.bm * t.bn * 4 / 3.6e6 : 0);
       if (us < best.us) best = {c, splits, us};
     }
   }
@@ -1021,7 +1034,8 @@ int64_t mx_workspace(const MxArgs& a) {
 }
 
 const char* mx_name(const MxArgs& a) {
-  static const char* const names[] = {"mx_tile256x256", "mx_tile128x128", "mx_tile64x128", "mx_tile64x64"};
+  static const char* const names[] = {"mx_tile256x256", "mx_tile128x128_s4", "mx_tile128x128_s2", "mx_tile64x128",
+                                      "mx_tile64x64"};
   if (takes_few(a.T, a.R)) return a.T <= 16 ? "mx_few16" : "mx_few32";
   return names[tile_plan(a.T, a.n, a.R).kind];
 }
@@ -1048,7 +1062,8 @@ hipError_t launch_mx(const MxArgs& args, hipStream_t s) {
   switch (plan.kind) {
     case 0: return run_tile<4, 2, 4, 8, 2, true>(a, plan.splits, s);
     case 1: return run_tile<2, 2, 4, 4, 4, false>(a, plan.splits, s);
-    case 2: return run_tile<2, 2, 4, 2, 4, false>(a, plan.splits, s);
+    case 2: return run_tile<2, 2, 4, 4, 2, false>(a, plan.splits, s);
+    case 3: return run_tile<2, 2, 4, 2, 4, false>(a, plan.splits, s);
     default: return run_tile<1, 4, 4, 1, 4, false>(a, plan.splits, s);
   }
 }
