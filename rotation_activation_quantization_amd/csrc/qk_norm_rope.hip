@@ -8,6 +8,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "row_ops.h"
 
@@ -30,6 +32,16 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// The value of the lane G / 2 away in the head (exclusive or).
+template <int G>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+  if (G == 2) return row::dpp<0xB1>(v);
+  if (G == 4) return row::dpp<0x4E>(v);
+  if (G == 8) return row::dpp<0x1B>(row::dpp<0x141>(v));  // 7, then 3
+  if (G == 16) return row::dpp<0x128>(v);                 // row_ror:8
+  return __shfl_xor(v, G / 2);
+}
+
 __device__ __forceinline__ int64_t place_of(const Args& a, int64_t t) {
   if (!a.positions) return t;
   const int64_t p = a.positions_64 ? static_cast<const int64_t*>(a.positions)[t]
@@ -37,19 +49,61 @@ __device__ __forceinline__ int64_t place_of(const Args& a, int64_t t) {
   return p < 0 ? 0 : (p >= a.places ? a.places - 1 : p);
 }
 
+// 1 / sqrt(x): the hardware's estimate (1 ulp) and a Newton step, below 2^-100
+// (where the estimate may not take its argument) the library's root.
+__device__ __forceinline__ float inverse_root(float x) {
+  if (x < 0x1p-100f) return 1.f / sqrtf(x);
+  const float r = __builtin_amdgcn_rsqf(x);
+  return fmaf(r, fmaf(-0.5f * x * r, r, 0.5f), r);
+}
+
 // Squares of values around 2^64 and more pass binary32's range; such a head is
 // summed again, scaled by this (eps is then below a rounding of the mean).
 constexpr float kSmall = 0x1p-80f;
 
+// Eight values as they lie in memory.
+struct Raw {
+  row::u32x4_t w[2];
+};
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ Raw load_raw(const void* p, int64_t j) {
+  Raw r = {};
+  if (BF16) {
+    r.w[0] = row::load_as<WHOLE, row::u32x4_t>(static_cast<const uint16_t*>(p) + j);
+  } else {
+    r.w[0] = row::load_as<WHOLE, row::u32x4_t>(static_cast<const float*>(p) + j);
+    r.w[1] = row::load_as<WHOLE, row::u32x4_t>(static_cast<const float*>(p) + j + 4);
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void widen(const Raw& r, float (&v)[8]) {
+  if (BF16) {
+    row::widen_bf16(r.w[0], v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.w[e >> 2][e & 3]);
+  }
+}
+
+// Where a channel's partner is: in the lane (interleaved pairs), in the lane G / 2
+// away (halves of a head of 8 G channels, all of them rotated), or anywhere in the
+// head, reached through LDS.
+enum Pairs { kOwn, kAcross, kAnywhere };
+
 // A lane holds eight channels of a head, G lanes a head, so that a wave takes
-// 64 / G heads of a token at a time, read and written once.  The channels'
-// partners come from the lane itself (interleaved pairs) or through 2 KiB of
-// LDS (halves).  A wave keeps its token's angles and goes over the token's
-// heads, every parts-th group of them.
-template <int G, bool WHOLE>
+// 64 / G heads of a token at a time, read and written once.  Bound by memory
+// where tokens are many.  A wave goes over its token's queries, every parts-th
+// group of heads, then over the keys; the next group's loads are on their way while
+// one is computed.  With weight w, bias b and angles of the token, channel j with
+// partner p and the sign of p's part in the sine,
+//   out_j = r (x_j - mean) w_j cos_j + r (x_p - mean) w_p sin_j + (b_j cos_j + b_p sin_j):
+// the factors w_j cos_j, w_p sin_j and the last sum are formed once a token and kept
+// for all its heads.
+template <int G, bool BF16, bool WHOLE, int PAIRS>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int parts) {
-  __shared__ float sh[kWaves][64 * 8];
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  __shared__ float sh[PAIRS == kAnywhere ? kWaves : 1][64 * 8];
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWaves + wid;
   const int64_t t = item / parts;
   const int part = static_cast<int>(item - t * parts);
@@ -60,150 +114,172 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
   const bool live = 8 * c < head;
   const row::Chunk<WHOLE> ch(live ? c : 0, head);
   const float inv_n = 1.f / static_cast<float>(head);
+  const int64_t angles = place_of(a, t) * a.ldt;
+  float* const mine = &sh[PAIRS == kAnywhere ? wid : 0][(lane / G) * 8 * G];
 
-  // the angles of the lane's channels: number p(e)
-  float cs[8], sn[8];
-  {
-    const int64_t at = place_of(a, t) * a.ldt;
+  // channel j's partner, itself where it is not rotated
+  auto partner = [&](int j) { return j >= rotary ? j : PAIRS == kOwn ? j ^ 1 : j < half ? j + half : j - half; };
+
+  auto side = [&](const void* src, int64_t ld, int64_t hs, void* dst, int64_t ldo, int64_t hso, int heads,
+                  const void* weight, const void* bias, int gr) {
+    const int groups = (heads + kHeads - 1) / kHeads;
+    if (gr >= groups) return;
+    const int bf16_out = a.out_type == SIGNROT_BF16, bf16_param = a.param_type == SIGNROT_BF16;
+    const bool normed = a.norm != SIGNROT_NORM_NONE;
+    src = static_cast<const uint8_t*>(src) + t * ld * (BF16 ? 2 : 4);
+    dst = static_cast<uint8_t*>(dst) + t * ldo * (bf16_out ? 2 : 4);
+    auto load = [&](int g) {
+      const int h = g * kHeads + lane / G;
+      Raw r = {};
+      if (live && h < heads) r = load_raw<BF16, WHOLE>(src, h * hs + ch.at);
+      return r;
+    };
+    Raw next = load(gr);
+    float wc[8], ws[8], add[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int j = ch.at + e;
-      const int p = a.interleaved ? j >> 1 : (j < half ? j : j - half);
+      const int j = ch.at + e, p = partner(j);
       const bool turn = live && j < rotary;
-      cs[e] = turn ? a.cos[at + p] : 1.f;
-      sn[e] = turn ? a.sin[at + p] : 0.f;
-      if (a.interleaved ? !(j & 1) : j < half) sn[e] = -sn[e];  // the first of a pair
+      const int k = PAIRS == kOwn ? j >> 1 : j < half ? j : j - half;  // number of the pair
+      const float cs = turn ? a.cos[angles + k] : 1.f;
+      float sn = turn ? a.sin[angles + k] : 0.f;
+      if (PAIRS == kOwn ? !(j & 1) : j < half) sn = -sn;  // the first of a pair
+      const float wj = normed && weight ? row::load_elem(weight, j, bf16_param) : 1.f;
+      const float wp = normed && weight ? row::load_elem(weight, p, bf16_param) : 1.f;
+      wc[e] = wj * cs;
+      ws[e] = wp * sn;
+      add[e] = 0.f;
+      if (normed && bias) add[e] = fmaf(row::load_elem(bias, p, bf16_param), sn, row::load_elem(bias, j, bf16_param) * cs);
     }
-  }
-  const int heads = a.q_heads + a.k_heads;
-  const int groups = (heads + kHeads - 1) / kHeads;
-  for (int gr = part; gr < groups; gr += parts) {
-    const int h0 = gr * kHeads + lane / G;
-    const bool on = live && h0 < heads;
-    const bool key = h0 >= a.q_heads;
-    const int h = key ? h0 - a.q_heads : h0;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      const void* const src = key ? a.k : a.q;
-      row::load8<WHOLE>(src, t * (key ? a.ldk : a.ldq) + h * (key ? a.hsk : a.hsq) + ch.at, a.in_type == SIGNROT_BF16, v);
-    }
-    if (a.norm != SIGNROT_NORM_NONE) {
-      float m[8];
+    for (; gr < groups; gr += parts) {
+      const Raw raw = next;
+      if (gr + parts < groups) next = load(gr + parts);
+      const int h = gr * kHeads + lane / G;
+      const bool on = live && h < heads;
+      float v[8], o[8];
+      widen<BF16>(raw, v);
+      float mean = 0.f, r = 1.f;
+      if (normed) {
+        if (a.norm == SIGNROT_NORM_LAYER) {
+          float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[e] = ch.own(e) ? 1.f : 0.f;
-      float mean = 0.f;
-      if (a.norm == SIGNROT_NORM_LAYER) {
-        float s = 0.f;
+          for (int e = 0; e < 8; ++e) s += ch.own(e) ? v[e] : 0.f;
+          s = head_sum<G>(s);
+          const float q = s * inv_n;
+          mean = fmaf(fmaf(-q, static_cast<float>(head), s), inv_n, q);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += ch.own(e) ? v[e] : 0.f;
-        s = head_sum<G>(s);
-        const float q = s * inv_n;
-        mean = fmaf(fmaf(-q, static_cast<float>(head), s), inv_n, q);
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = on ? v[e] - mean : 0.f;
-        if (ch.own(e)) ss = fmaf(v[e], v[e], ss);
-      }
-      ss = head_sum<G>(ss);
-      float r = 1.f / sqrtf(fmaf(ss, inv_n, a.eps));
-      if (!(ss < INFINITY)) {  // the same in all lanes of a head
-        float sm = 0.f;
+          for (int e = 0; e < 8; ++e) v[e] -= mean;
+        }
+        float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (ch.own(e)) sm = fmaf(v[e] * kSmall, v[e] * kSmall, sm);
-        sm = head_sum<G>(sm);
-        r = kSmall / sqrtf(fmaf(sm, inv_n, a.eps * kSmall * kSmall));
+          if (ch.own(e)) ss = fmaf(v[e], v[e], ss);
+        ss = head_sum<G>(live ? ss : 0.f);
+        r = inverse_root(fmaf(ss, inv_n, a.eps));
+        if (!(ss < INFINITY)) {  // the same in all lanes of a head
+          float sm = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (ch.own(e)) sm = fmaf(v[e] * kSmall, v[e] * kSmall, sm);
+          sm = head_sum<G>(live ? sm : 0.f);
+          r = kSmall * inverse_root(fmaf(sm, inv_n, a.eps * kSmall * kSmall));
+        }
       }
-      const void* const w = key ? a.k_weight : a.q_weight;
-      const void* const b = key ? a.k_bias : a.q_bias;
-      float f[8];
+      float other[8];
+      if (PAIRS == kOwn) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= r;
-      if (w && on) {
-        row::load8<WHOLE>(w, ch.at, a.param_type == SIGNROT_BF16, f);
+        for (int e = 0; e < 8; ++e) other[e] = v[e ^ 1];
+      } else if (PAIRS == kAcross) {
+        Raw far;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f[e];
+        for (int i = 0; i < 4; ++i) {
+          far.w[0][i] = across<G>(raw.w[0][i]);
+          if (!BF16) far.w[1][i] = across<G>(raw.w[1][i]);
+        }
+        widen<BF16>(far, other);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) other[e] -= mean;
+      } else {
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mine[ch.at + e] = v[e];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) other[e] = mine[partner(ch.at + e)];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      if (b && on) {
-        row::load8<WHOLE>(b, ch.at, a.param_type == SIGNROT_BF16, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += f[e];
-      }
-    }
-    float o[8];
-    if (a.interleaved) {
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(fmaf(other[e], ws[e], v[e] * wc[e]), r, add[e]);
+      if (!on) continue;
+      const int64_t to = h * hso + ch.at;
+      if (WHOLE || ch.dup == 0) {
+        if (bf16_out) {
+          row::store_as<WHOLE>(static_cast<uint16_t*>(dst) + to,
+                               row::u32x4_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3]),
+                                            row::pack_bf16(o[4], o[5]), row::pack_bf16(o[6], o[7])});
+        } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e ^ 1], sn[e], v[e] * cs[e]);
-    } else {
-      float* const mine = &sh[wid][(lane / G) * 8 * G];
-      if (live) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mine[ch.at + e] = v[e];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = ch.at + e;
-        const float other = j < rotary ? mine[j < half ? j + half : j - half] : 0.f;
-        o[e] = fmaf(other, sn[e], v[e] * cs[e]);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    if (!on) continue;
-    const bool bf16 = a.out_type == SIGNROT_BF16;
-    void* const dst = key ? a.k_out : a.q_out;
-    const int64_t to = t * (key ? a.ldko : a.ldqo) + h * (key ? a.hsko : a.hsqo) + ch.at;
-    if (WHOLE || ch.dup == 0) {
-      if (bf16) {
-        row::store_as<WHOLE>(static_cast<uint16_t*>(dst) + to,
-                             row::u32x4_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3]),
-                                          row::pack_bf16(o[4], o[5]), row::pack_bf16(o[6], o[7])});
+          for (int q = 0; q < 2; ++q)
+            row::store_as<WHOLE>(static_cast<float*>(dst) + to + 4 * q,
+                                 row::u32x4_t{__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                                              __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])});
+        }
       } else {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          row::store_as<WHOLE>(static_cast<float*>(dst) + to + 4 * q,
-                               row::u32x4_t{__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
-                                            __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])});
+        for (int e = 0; e < 8; ++e)
+          if (ch.own(e)) row::store_elem(dst, to + e, o[e], bf16_out);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (ch.own(e)) row::store_elem(dst, to + e, o[e], bf16);
     }
-  }
+  };
+  side(a.q, a.ldq, a.hsq, a.q_out, a.ldqo, a.hsqo, a.q_heads, a.q_weight, a.q_bias, part);
+  // the keys' groups follow the queries': every parts-th of them all
+  const int queries = (a.q_heads + kHeads - 1) / kHeads;
+  if (a.k_heads > 0)
+    side(a.k, a.ldk, a.hsk, a.k_out, a.ldko, a.hsko, a.k_heads, a.k_weight, a.k_bias,
+         (part + parts - queries % parts) % parts);
 }
 
 template <int G>
 void run(const Args& a, bool whole, hipStream_t s) {
-  const int groups = (a.q_heads + a.k_heads + 64 / G - 1) / (64 / G);
+  constexpr int kHeads = 64 / G;
+  const int groups = (a.q_heads + kHeads - 1) / kHeads + (a.k_heads + kHeads - 1) / kHeads;
   int parts = 1;
   while (parts < groups && a.tokens * parts < 4096) parts *= 2;
   if (parts > groups) parts = groups;
+  const bool bf16 = a.in_type == SIGNROT_BF16;
+  const int pairs = a.interleaved || a.rotary == 0 ? kOwn
+                    : whole && G > 1 && a.rotary == a.head && a.head == 8 * G ? kAcross
+                                                                             : kAnywhere;
   // a launch holds fewer than 2^32 threads
   const int64_t most = (int64_t{1} << 25) / parts;
   for (int64_t t = 0; t < a.tokens; t += most) {
     Args b = a;
     b.tokens = a.tokens - t < most ? a.tokens - t : most;
-    const int in = a.in_type == SIGNROT_BF16 ? 2 : 4, out = a.out_type == SIGNROT_BF16 ? 2 : 4;
+    const int in = bf16 ? 2 : 4, out = a.out_type == SIGNROT_BF16 ? 2 : 4;
     b.q = static_cast<const uint8_t*>(a.q) + t * a.ldq * in;
     b.q_out = static_cast<uint8_t*>(a.q_out) + t * a.ldqo * out;
     if (a.k) b.k = static_cast<const uint8_t*>(a.k) + t * a.ldk * in;
     if (a.k) b.k_out = static_cast<uint8_t*>(a.k_out) + t * a.ldko * out;
     if (a.positions) {
       b.positions = static_cast<const uint8_t*>(a.positions) + t * (a.positions_64 ? 8 : 4);
-    } else {
+    } else if (a.rotary > 0) {
       b.cos = a.cos + t * a.ldt;
       b.sin = a.sin + t * a.ldt;
     }
     const dim3 grid(static_cast<unsigned>((b.tokens * parts + kWaves - 1) / kWaves));
-    if (whole)
-      qk_norm_rope_kernel<G, true><<<grid, 64 * kWaves, 0, s>>>(b, parts);
-    else
-      qk_norm_rope_kernel<G, false><<<grid, 64 * kWaves, 0, s>>>(b, parts);
+    const auto go = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, s>>>(b, parts); };
+    const auto pick = [&](auto BF16) {
+      constexpr bool kBf16 = decltype(BF16)::value;
+      if (pairs == kAcross) go(qk_norm_rope_kernel<G, kBf16, true, kAcross>);
+      else if (pairs == kOwn)
+        whole ? go(qk_norm_rope_kernel<G, kBf16, true, kOwn>) : go(qk_norm_rope_kernel<G, kBf16, false, kOwn>);
+      else
+        whole ? go(qk_norm_rope_kernel<G, kBf16, true, kAnywhere>) : go(qk_norm_rope_kernel<G, kBf16, false, kAnywhere>);
+    };
+    bf16 ? pick(std::true_type{}) : pick(std::false_type{});
   }
 }
 
