@@ -104,16 +104,6 @@ __device__ __forceinline__ void widen(const Raw& r, float (&v)[8]) {
   }
 }
 
-// Sixteen bytes out; `stream`: past the caches.
-template <bool WHOLE>
-__device__ __forceinline__ void store_chunk(void* p, const row::u32x4_t& v, int stream) {
-  typedef row::u32x4_t any_u32x4_t __attribute__((aligned(2)));
-  if (stream)
-    __builtin_nontemporal_store(v, static_cast<any_u32x4_t*>(p));
-  else
-    row::store_as<WHOLE>(p, v);
-}
-
 // Where a channel's partner is: in the lane (interleaved pairs), in the lane G / 2
 // away (halves of a head of 8 G channels, all of them rotated), or elsewhere in the
 // head, reached through LDS: in whole chunks, or one by one.
@@ -281,17 +271,16 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       const int64_t to = h * hso + ch.at;
       if (WHOLE || ch.dup == 0) {
         if (bf16_out) {
-          store_chunk<WHOLE>(static_cast<uint16_t*>(dst) + to,
+          row::store_chunk<WHOLE>(static_cast<uint16_t*>(dst) + to,
                              row::u32x4_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3]),
                                           row::pack_bf16(o[4], o[5]), row::pack_bf16(o[6], o[7])},
                              stream);
         } else {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            store_chunk<WHOLE>(static_cast<float*>(dst) + to + 4 * q,
-                               row::u32x4_t{__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
-                                            __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])},
-                               stream);
+            row::store_as<WHOLE>(static_cast<float*>(dst) + to + 4 * q,
+                                 row::u32x4_t{__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                                              __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])});
         }
       } else {
 #pragma unroll
@@ -316,9 +305,7 @@ void run(const Args& a, bool whole, hipStream_t s) {
   while (parts < groups && a.tokens * parts < 4096) parts *= 2;
   if (parts > groups) parts = groups;
   const bool bf16 = a.in_type == SIGNROT_BF16;
-  // Results that the caches would not hold until they are read go past them: 8192
-  // tokens of 64 + 8 heads of 128 took 76.6 us without, 70.0 so.
-  const int stream = a.tokens * (a.q_heads + a.k_heads) * a.head * (a.out_type == SIGNROT_BF16 ? 2 : 4) > (64 << 20);
+  const int stream = row::past_caches(a.tokens * (a.q_heads + a.k_heads) * a.head, a.out_type == SIGNROT_BF16);
   const int pairs = a.interleaved || a.rotary == 0 ? kOwn
                     : whole && G > 1 && a.rotary == a.head && a.head == 8 * G ? kAcross
                     : whole && a.rotary % 16 == 0                             ? kChunks

@@ -75,7 +75,7 @@ template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void dequant_mx_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                               const uint8_t* __restrict__ scale, int64_t lds, int n,
                                                               void* __restrict__ y, int64_t ldy, uint32_t chunks,
-                                                              uint32_t per) {
+                                                              uint32_t per, int stream) {
   const uint32_t c = blockIdx.x * kThreads + threadIdx.x;
   if (c >= chunks) return;
   const At at(c, per);
@@ -95,15 +95,16 @@ __global__ __launch_bounds__(kThreads) void dequant_mx_kernel(const uint8_t* __r
   const int64_t out = at.row * ldy + j;
   if (j + 8 <= n) {
     if (BF16) {
-      row::store_as<WHOLE>(static_cast<uint16_t*>(y) + out,
-                           row::u32x4_t{row::pack_bf16(v[0], v[1]), row::pack_bf16(v[2], v[3]),
-                                        row::pack_bf16(v[4], v[5]), row::pack_bf16(v[6], v[7])});
+      row::store_chunk<WHOLE>(static_cast<uint16_t*>(y) + out,
+                              row::u32x4_t{row::pack_bf16(v[0], v[1]), row::pack_bf16(v[2], v[3]),
+                                           row::pack_bf16(v[4], v[5]), row::pack_bf16(v[6], v[7])},
+                              stream);
     } else {
-      typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         row::store_as<WHOLE>(static_cast<float*>(y) + out + 4 * h,
-                             f32x4_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
+                             row::u32x4_t{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                                          __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])});
     }
   } else {
 #pragma unroll
@@ -151,10 +152,11 @@ hipError_t launch_dequant_mx(const uint8_t* codes, int64_t ldc, const uint8_t* s
   const uint32_t per = static_cast<uint32_t>(n + 7) / 8;
   const int size = bf16 ? 2 : 4;
   const bool whole = n % 8 == 0 && ldy % (16 / size) == 0 && aligned_to(y, 16) && ldc % 4 == 0 && aligned_to(codes, 4);
+  const int stream = row::past_caches(tokens * n, bf16);
   return over_rows(tokens, per, [&](int64_t t, uint32_t chunks, dim3 grid) {
     const auto run = [&](auto kernel) {
       kernel<<<grid, kThreads, 0, s>>>(codes + t * ldc, ldc, scale + t * lds, lds, n,
-                                       static_cast<uint8_t*>(y) + t * ldy * size, ldy, chunks, per);
+                                       static_cast<uint8_t*>(y) + t * ldy * size, ldy, chunks, per, stream);
     };
     if (bf16)
       whole ? run(dequant_mx_kernel<true, true>) : run(dequant_mx_kernel<true, false>);
