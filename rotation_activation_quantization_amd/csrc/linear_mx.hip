@@ -175,7 +175,10 @@ struct Tile {
 //
 // A work-group takes the tiles p, p + stride, ... below `end`, and the ring
 // runs on from tile to tile: the last stages of a tile load the first ones of
-// the next, which arrive while its results are stored.
+// the next, which arrive while its results are stored.  With two stages the second
+// stage's loads all go out before the stores, so that the wait in the next tile's
+// first stage can leave the stores on their way (8192 x 4096 x 4096 71.2 us, 72.9
+// with the wait for them).
 //
 // A row is cut into quads of four depths (512 channels, two stages).  Quad 0 of
 // a tile is the row's last, possibly short one.  Its chunks beyond n are read
@@ -415,14 +418,14 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       load_scales(1);
     }
 #pragma unroll
-    for (int l = 0; l < (s == S - 1 ? kLate : C::kLoads); ++l) issue(l, s % 2, s);
+    for (int l = 0; l < (S > 2 && s == S - 1 ? kLate : C::kLoads); ++l) issue(l, s % 2, s);
   }
   if (S == 2 && !ORDERED) {
-    wave::wait_vmcnt<C::kLoads + kLate>();
+    wave::wait_vmcnt<2 * C::kLoads>();
     __builtin_amdgcn_sched_barrier(0);
     turn_scales(0);
   }
-  wave::wait_vmcnt<(S - 2) * C::kLoads + kLate + (S == 4 ? kScaleLoads : 0)>();
+  wave::wait_vmcnt<S == 2 ? C::kLoads : 2 * C::kLoads + kLate + kScaleLoads>();
   wave::lds_barrier();
   wf[0] = weight(0, 0, 0);
   wf[1] = weight(0, 0, 1);
@@ -430,8 +433,14 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   for (int j = 0; j < FT; ++j) tok[0][j] = token(0, 0, j);
   read_scales(0, 0, 0);
 
-  // Stage j of a quad at ring position pos.
-  auto stage = [&](auto J, int pos, int half) {
+  // Stores that the results of the tile before have on their way behind the loads of
+  // the first stage (S = 2), when their number is certain.
+  int stored = 0;
+  constexpr int kStores = FK * FT / 2;  // of bf16 results; binary32: twice as many
+
+  // Stage j of a quad at ring position pos; fresh: a tile's first with S = 2, before
+  // which all loads of the next have been issued.
+  auto stage = [&](auto J, bool fresh, int pos, int half) {
     constexpr int j = decltype(J)::value;
     const int next = (pos + 1) % S, before = (pos + S - 1) % S;
     unrolled<2>([&](auto UC) {
@@ -445,7 +454,12 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           // may be in flight, with the scales that one of them began with.  The
           // scales loaded two (S = 2: one) stages ago go to LDS.
           constexpr bool turn = !ORDERED && j == (S == 2 ? 1 : 0);
-          wave::wait_vmcnt<(S - 2) * C::kLoads + (S == 4 && j == 1 ? kScaleLoads : 0)>();
+          if (S == 2 && j == 0 && fresh && stored == kStores)
+            wave::wait_vmcnt<kStores>();
+          else if (S == 2 && j == 0 && fresh && stored == 2 * kStores)
+            wave::wait_vmcnt<2 * kStores>();
+          else
+            wave::wait_vmcnt<(S - 2) * C::kLoads + (S == 4 && j == 1 ? kScaleLoads : 0)>();
           __builtin_amdgcn_sched_barrier(0);
           if (turn) turn_scales(half ^ 1);
           wave::lds_barrier();
@@ -469,7 +483,9 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           for (int t = (f - FK + 2) * FT / 2; t < (f - FK + 3) * FT / 2; ++t) then[t] = token(next, 0, t);
           if (f == FK - 1) read_scales(0, half ^ j, 2 * (j ^ 1));
         }
-        if (b < kEarly) issue(kLate + b, j ^ 1, before);
+        if constexpr (b < kEarly) {
+          if (S != 2 || j == 1 || !fresh) issue(kLate + b, j ^ 1, before);
+        }
         if (b >= 2 * FK - 2) {
 #pragma unroll
           for (int l = (b - 2 * FK + 2) * kLate / 2; l < (b - 2 * FK + 3) * kLate / 2; ++l) issue(l, j, pos);
@@ -498,9 +514,15 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     const int count = first(part + 1) - first(part);
 #pragma clang loop unroll(disable)
     for (int q = 0; q < count; ++q) {
-      unrolled<2>([&](auto J) { stage(J, (S == 2 ? 0 : pos) + J, half); });
+      unrolled<2>([&](auto J) { stage(J, q == 0, (S == 2 ? 0 : pos) + J, half); });
       if (S != 2) pos ^= 2;
       half ^= 1;
+    }
+    if (S == 2) {
+      // the rest of the next tile's second stage, before the stores that its first
+      // need not wait for
+#pragma unroll
+      for (int l = kLate; l < C::kLoads; ++l) issue(l, 1, 1);
     }
 
     settle();
@@ -523,6 +545,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
     // banks once.  A wave's LDS accesses are done in order, so the next unit is
     // written as soon as the reads of this one are on their way.
     uint8_t* const mine = lds + C::kRing + 2 * C::kScales + 2048 * wid;
+    const int lane = lane_here(), g = lane >> 4, i = lane & 15;
     auto chunk_at = [&](int r, int c) {
       return reinterpret_cast<wave::u32x4_t*>(mine + 128 * r + 16 * (c ^ ((r >> 1) & 7)));
     };
@@ -538,8 +561,9 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           bias[q][e] = a.bias[min(k_wave + 64 * q + 32 * (e >> 3) + 8 * g + (e & 7), a.R - 1)];
+      wave::wait_vmcnt<0>();  // here, or the compiler waits for it, and all stores, in the next tile
     }
-    auto results = [&](auto BF16) {
+    auto results = [&](auto BF16, auto WHOLE) {
       constexpr int per = BF16 ? 8 : 4;    // results of a chunk
       constexpr int parts = BF16 ? 1 : 2;  // units of 64 channels
       constexpr int units = FK / 4 * FT * parts;
@@ -573,7 +597,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           const int t = t_wave + 16 * j + 8 * h + r0;
           uint8_t* const at = to + (static_cast<int64_t>(16 * j + 8 * h) * a.ldo + 64 * q + 32 * part) * (16 / per);
           const wave::u32x4_t v = got[u & 1][h];
-          if (t < a.T && k + per <= a.R) {
+          if (WHOLE || (t < a.T && k + per <= a.R)) {
             row::store_as<false>(at, v);
           } else if (t < a.T) {
 #pragma unroll
@@ -600,10 +624,16 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       });
       send(std::integral_constant<int, units - 1>{});
     };
-    if (a.out_bf16)
-      results(std::true_type{});
+    const bool whole = m0 + C::kBM <= a.T && n0 + C::kBN <= a.R;
+    stored = !whole ? 0 : a.out_bf16 ? kStores : 2 * kStores;
+    if (a.out_bf16 && whole)
+      results(std::true_type{}, std::true_type{});
+    else if (a.out_bf16)
+      results(std::true_type{}, std::false_type{});
+    else if (whole)
+      results(std::false_type{}, std::true_type{});
     else
-      results(std::false_type{});
+      results(std::false_type{}, std::false_type{});
   }
   wave::wait_vmcnt<0>();
 }
