@@ -1,5 +1,5 @@
-// Shared by the fast rotate+INT4 kernels for gfx950 (rq_fast.hip: n = 28 * 2^k,
-// k = 7..9, and n = 2^12..2^14; rq_halves.hip: n = 28 * 2^10): the row shape
+// Shared by the fast rotate+INT4 kernels for gfx950 (rq_fast_impl.h: n = 28 * 2^k,
+// k = 7..9, and n = 2^12..2^14; rq_halves_impl.h: n = 28 * 2^10): the row shape
 // and LDS slot of a quad, the fused SwiGLU producer of the input, and guarded
 // 16-byte stores.
 #pragma once
@@ -12,8 +12,10 @@
 
 namespace signrot {
 
-// n = 28672 (rq_halves.hip)
+// n = 28672 (rq_halves_impl.h)
 hipError_t launch_rq_halves(const RqArgs& a, hipStream_t stream);
+// the same widths with MXFP4 output (rq_mx.hip)
+hipError_t launch_rq_mx(const RqArgs& a, hipStream_t stream);
 
 namespace {
 
