@@ -776,7 +776,7 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R) {
 
 // ---- few tokens ---------------------------------------------------------------
 //
-// The weights are read once and bound the time.  A work-group takes 16 FK
+// The weights are read once and bound the time (1 x 28672 x 8192 22.8 us, 5.4 TB/s).  A work-group takes 16 FK
 // channels and all tokens (FT groups of sixteen); its waves share the row: wave w
 // takes the 128-byte units w, w + waves, ... of the codes (eight blocks), so that
 // the work-group reads its rows side by side.  Each wave has a ring of D units of
@@ -802,9 +802,9 @@ struct Few {
   static constexpr int kSLoads = (32 * (FK + FT) + 63) / 64;  // of 64 words of scales
   static constexpr int kLoads = kWLoads + kTLoads + kSLoads;
   static constexpr int kSlot = kWBytes + kTBytes + 256 * kSLoads;
-  static constexpr int kPart = 1024 * FK * FT;  // bytes of a wave's partial sums
-  static constexpr int kWave = D * kSlot + kPart;
+  static constexpr int kWave = D * kSlot;
   static_assert(8 * kWave <= 160 * 1024, "eight waves");
+  static_assert(1024 * FK * FT <= kWave, "a wave's partial sums take its ring's place");
 };
 
 template <int FK, int FT, int D>
@@ -818,8 +818,7 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
   const int bytes = a.n / 2, blocks = a.n / mx::kBlock;
   const int units = (bytes + kUnit - 1) / kUnit;
   const int count = units > wid ? (units - wid - 1) / waves + 1 : 0;
-  uint8_t* const ring = few_lds + wid * D * C::kSlot;
-  float* const part = reinterpret_cast<float*>(few_lds + waves * D * C::kSlot);
+  uint8_t* const ring = few_lds + wid * C::kWave;
 
   // rows and tokens beyond the tensors are clamped (their results are not stored)
   const int rows_w = min(16 * FK, a.R - n0);
@@ -920,16 +919,16 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
   for (int f = 0; f < FK; ++f)
 #pragma unroll
     for (int j = 0; j < FT; ++j)
-      *reinterpret_cast<f32x4_t*>(part + 4 * (((wid * FK + f) * FT + j) * 64 + lane)) = acc[f][j];
+      *reinterpret_cast<f32x4_t*>(ring + 16 * ((f * FT + j) * 64 + lane)) = acc[f][j];
   __syncthreads();
-  // sums [wave][FK][FT][64][4]: result e is channel e % 4 + 4 (e / 64 % 4) of group
+  // sums [FK][FT][64][4] of each wave: result e is channel e % 4 + 4 (e / 64 % 4) of group
   // e / 256 / FT, token e / 4 % 16 of group e / 256 % FT
   for (int e = threadIdx.x; e < 256 * FK * FT; e += blockDim.x) {
     const int k = n0 + 16 * ((e >> 8) / FT) + (e & 3) + 4 * ((e >> 6) & 3);
     const int t = 16 * ((e >> 8) % FT) + ((e >> 2) & 15);
     if (k >= a.R || t >= a.T) continue;
-    float sum = part[e];
-    for (int v = 1; v < waves; ++v) sum += part[256 * FK * FT * v + e];
+    float sum = reinterpret_cast<const float*>(few_lds)[e];
+    for (int v = 1; v < waves; ++v) sum += reinterpret_cast<const float*>(few_lds + v * C::kWave)[e];
     row::store_elem(a.out, static_cast<int64_t>(t) * a.ldo + k, sum + (a.bias ? a.bias[k] : 0.f), a.out_bf16);
   }
 }
@@ -951,11 +950,21 @@ hipError_t run_few_as(const MxArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// 32 channels a work-group halve what it reads of the tokens, which up to sixteen
+// tokens' rows is as much as the weights (16 x 28672 x 8192 26.8 us, 30.3 with sixteen
+// channels; 32 tokens 32.5 and 40.8), where that still gives more than half of the CUs
+// a work-group (16 x 14336 x 4096 12.8 and 9.7); up to four tokens it gains nothing
+// (2 x 28672 x 8192 24.0 and 22.8).  Times on weights that no cache holds.
+bool few_wide(int64_t T, int64_t R) { return T > 4 && R > 16 * kCus; }
+
+// Beyond sixteen tokens and two work-groups a CU the tiles are faster (32 x 8192 x
+// 20480 26.5 us, 30.3 here; 32 x 8192 x 7168 here 11.1).
+bool takes_few(int64_t T, int64_t R) { return (T <= 16 && R <= (int64_t{1} << 24)) || (T <= 32 && R <= 64 * kCus); }
+
 hipError_t run_few(const MxArgs& a, hipStream_t s) {
+  if (few_wide(a.T, a.R)) return a.T <= 16 ? run_few_as<2, 1, 2>(a, s) : run_few_as<2, 2, 2>(a, s);
   return a.T <= 16 ? run_few_as<1, 1, 4>(a, s) : run_few_as<1, 2, 2>(a, s);
 }
-
-bool takes_few(int64_t T, int64_t R) { return T <= 32 && R <= (int64_t{1} << 24); }
 
 constexpr int64_t kMaxPitch = 1 << 23;  // a tile's offsets stay below 2^32
 
@@ -1066,6 +1075,7 @@ int64_t mx_workspace(const MxArgs& a) {
 const char* mx_name(const MxArgs& a) {
   static const char* const names[] = {"mx_tile256x256", "mx_tile128x128_s4", "mx_tile128x128_s2", "mx_tile64x128",
                                       "mx_tile64x64"};
+  if (takes_few(a.T, a.R) && few_wide(a.T, a.R)) return a.T <= 16 ? "mx_few16_k32" : "mx_few32_k32";
   if (takes_few(a.T, a.R)) return a.T <= 16 ? "mx_few16" : "mx_few32";
   return names[tile_plan(a.T, a.n, a.R).kind];
 }

@@ -58,8 +58,10 @@ def splits_of(x, w, name):
 
 CASES = [
     # name, parts, tokens, n, rows
-    ("mx_few16", 1, 1, 32, 1), ("mx_few16", 1, 1, 4096, 14336), ("mx_few16", 1, 16, 8224, 40), ("mx_few16", 1, 7, 2080, 8199),
+    ("mx_few16", 1, 1, 32, 1), ("mx_few16", 1, 1, 4096, 14336), ("mx_few16", 1, 16, 8224, 40), ("mx_few16", 1, 4, 2080, 8199),
+    ("mx_few16_k32", 1, 7, 2080, 8199), ("mx_few16_k32", 1, 16, 14336, 4100), ("mx_few16_k32", 1, 13, 32, 28673),
     ("mx_few32", 1, 17, 32, 3), ("mx_few32", 1, 32, 4128, 1040), ("mx_few32", 1, 29, 14336, 777),
+    ("mx_few32_k32", 1, 17, 96, 4097), ("mx_few32_k32", 1, 32, 8224, 16384), ("mx_few32_k32", 1, 25, 4128, 5119),
     ("mx_tile64x64", 1, 33, 544, 40), ("mx_tile64x64", 1, 300, 1024, 2100), ("mx_tile64x64", 3, 4100, 4096, 40),
     ("mx_tile64x64", 8, 33, 4128, 40), ("mx_tile64x64", 16, 33, 8224, 40),
     ("mx_tile64x128", 1, 33, 32, 40), ("mx_tile64x128", 1, 100, 96, 4099), ("mx_tile64x128", 2, 33, 8224, 14340),
