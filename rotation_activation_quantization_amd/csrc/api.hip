@@ -909,13 +909,14 @@ int signrot_mxfp4_linear(const uint8_t* codes, int64_t ldc, const uint8_t* scale
   a.out = out;
   a.ldo = ldo;
   a.out_bf16 = out_type == SIGNROT_BF16;
-  const int64_t need = mx_workspace(a);
+  const MxPlan plan = mx_plan(a);
+  const int64_t need = mx_workspace(a, plan);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return fail_einval("workspace too small");
     if (!aligned16(workspace)) return fail_einval("workspace must be 16-byte aligned");
   }
   a.workspace = static_cast<uint8_t*>(workspace);
-  const hipError_t e = launch_mx(a, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_mx(a, plan, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail_hip(e, "mxfp4_linear launch");
   return SIGNROT_OK;
 }
@@ -925,8 +926,8 @@ int64_t signrot_mxfp4_linear_workspace(const uint8_t* codes, int64_t ldc, const 
                                        const uint8_t* w_scale, int64_t ldws, int64_t rows) {
   g_last_error[0] = '\0';
   MxArgs a;
-  return mx_operands(a, codes, ldc, scale, lds, tokens, n, w, ldw, w_scale, ldws, rows) == SIGNROT_OK ? mx_workspace(a)
-                                                                                                      : -1;
+  if (mx_operands(a, codes, ldc, scale, lds, tokens, n, w, ldw, w_scale, ldws, rows) != SIGNROT_OK) return -1;
+  return mx_workspace(a, mx_plan(a));
 }
 
 const char* signrot_mxfp4_linear_kernel_name(const uint8_t* codes, int64_t ldc, const uint8_t* scale, int64_t lds,

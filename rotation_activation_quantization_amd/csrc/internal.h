@@ -207,9 +207,15 @@ struct MxArgs {
   int n;  // a multiple of 32
 };
 constexpr int kMxMaxN = 131072;
-int64_t mx_workspace(const MxArgs& a);
+// The kernel for the sizes: a tile (its place in the list) and the parts of a row, or
+// -1: few tokens.
+struct MxPlan {
+  int kind, splits;
+};
+MxPlan mx_plan(const MxArgs& a);
+int64_t mx_workspace(const MxArgs& a, const MxPlan& plan);
 const char* mx_name(const MxArgs& a);
-hipError_t launch_mx(const MxArgs& a, hipStream_t s);
+hipError_t launch_mx(const MxArgs& a, const MxPlan& plan, hipStream_t s);
 
 hipError_t launch_qk_norm_rope(const signrot_qk_norm_rope_args& a, hipStream_t s);
 

@@ -747,15 +747,12 @@ constexpr TileCost kTiles[] = {{256, 256, 1, 3.2, 0, 6.0},       // 4 x 2 waves 
                                {64, 128, 1, 1.10, 0, 0.58},      // 2 x 2 waves of 64 x 32
                                {64, 64, 2, 0.88, 1.54, 0.84}};   // 1 x 4 waves of 64 x 16
 
-struct Plan {
-  int kind, splits;
-  double us;
-};
 
 // The least estimate over the tiles and over parts of the row joined by a second
 // kernel (3.4 us, and 3.6 TB/s over the partial sums), or what the bytes take.
-Plan tile_plan(int64_t T, int64_t n, int64_t R) {
-  Plan best{0, 1, 1e30};
+MxPlan tile_plan(int64_t T, int64_t n, int64_t R) {
+  MxPlan best{0, 1};
+  double least = 1e30;
   const double bytes = static_cast<double>(T + R) * n * 17 / 32 + 2.0 * T * R;
   const int64_t quads = (n + 511) / 512;
   for (int c = 0; c < 5; ++c) {
@@ -768,7 +765,10 @@ Plan tile_plan(int64_t T, int64_t n, int64_t R) {
       double us = t.fit == 1 ? per_cu * (k * t.one + t.tile)
                              : floor(per_cu / 2) * (k * t.two + t.tile) + fmod(per_cu, 2) * (k * t.one + t.tile);
       us = fmax(us, bytes / 6.6e6) + (splits > 1 ? 3.4 + tiles * splits * t.bm * t.bn * 4 / 3.6e6 : 0);
-      if (us < best.us) best = {c, splits, us};
+      if (us < least) {
+        least = us;
+        best = {c, splits};
+      }
     }
   }
   return best;
@@ -1052,11 +1052,7 @@ struct Layout {
   }
 };
 
-bool takes_ordered(const MxArgs& a) { return !takes_few(a.T, a.R) && tile_plan(a.T, a.n, a.R).kind == 0; }
-
-int64_t partial_bytes(const MxArgs& a) {
-  if (takes_few(a.T, a.R)) return 0;
-  const Plan p = tile_plan(a.T, a.n, a.R);
+int64_t partial_bytes(const MxArgs& a, const MxPlan& p) {
   if (p.splits == 1) return 0;
   const TileCost& t = kTiles[p.kind];
   const int64_t tiles = static_cast<int64_t>((a.T + t.bm - 1) / t.bm) * ((a.R + t.bn - 1) / t.bn);
@@ -1065,32 +1061,37 @@ int64_t partial_bytes(const MxArgs& a) {
 
 }  // namespace
 
-int64_t mx_workspace(const MxArgs& a) {
+MxPlan mx_plan(const MxArgs& a) {
+  if (a.T == 0 || a.R == 0 || takes_few(a.T, a.R)) return {-1, 1};
+  return tile_plan(a.T, a.n, a.R);
+}
+
+int64_t mx_workspace(const MxArgs& a, const MxPlan& plan) {
   if (a.T == 0 || a.R == 0) return 0;
   MxArgs b = a;
   b.workspace = nullptr;
-  return Layout(b, partial_bytes(a), takes_ordered(a)).end;
+  return Layout(b, partial_bytes(a, plan), plan.kind == 0).end;
 }
 
 const char* mx_name(const MxArgs& a) {
   static const char* const names[] = {"mx_tile256x256", "mx_tile128x128_s4", "mx_tile128x128_s2", "mx_tile64x128",
                                       "mx_tile64x64"};
-  if (takes_few(a.T, a.R) && few_wide(a.T, a.R)) return a.T <= 16 ? "mx_few16_k32" : "mx_few32_k32";
-  if (takes_few(a.T, a.R)) return a.T <= 16 ? "mx_few16" : "mx_few32";
-  return names[tile_plan(a.T, a.n, a.R).kind];
+  const MxPlan plan = mx_plan(a);
+  if (plan.kind >= 0) return names[plan.kind];
+  if (few_wide(a.T, a.R)) return a.T <= 16 ? "mx_few16_k32" : "mx_few32_k32";
+  return a.T <= 16 ? "mx_few16" : "mx_few32";
 }
 
-hipError_t launch_mx(const MxArgs& args, hipStream_t s) {
+hipError_t launch_mx(const MxArgs& args, const MxPlan& plan, hipStream_t s) {
   MxArgs a = args;
-  const bool ordered = takes_ordered(args);
-  const Layout lay(a, partial_bytes(args), ordered);
+  const bool ordered = plan.kind == 0;
+  const Layout lay(a, partial_bytes(args, plan), ordered);
   if (lay.count > 0) {
     mx_copy_kernel<<<dim3(1024, static_cast<unsigned>(lay.count)), 256, 0, s>>>(lay.copies);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (takes_few(a.T, a.R)) return run_few(a, s);
-  const Plan plan = tile_plan(a.T, a.n, a.R);
+  if (plan.kind < 0) return run_few(a, s);
   if (ordered) {
     const int groups = lay.order.groups[0] + lay.order.groups[1];
     mx_order_kernel<<<dim3(static_cast<unsigned>((lay.order.quads + 3) / 4),
