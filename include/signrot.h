@@ -571,10 +571,11 @@ int signrot_dequant_mxfp4(const uint8_t* codes, int64_t ldc, const uint8_t* scal
  *                     call's work has ended.
  *
  * n a multiple of 32 (whole blocks), 32 <= n <= 131072; tokens and rows below
- * 2^30; any alignment and stride (code rows on 16-byte boundaries and scale rows
- * on 4-byte ones are the fast case; others are laid out anew in the workspace).
- * Scale rows are read in aligned words of four: bytes of the word that holds a
- * row's last scale may be read too; their values do not matter.  tokens == 0 or
+ * 2^30; any alignment and stride (code rows that do not start on 16-byte
+ * boundaries are laid out anew in the workspace, and so are rows of fewer than
+ * four scales that do not start on 4-byte ones).  Scales may be read in aligned
+ * words of four: bytes beside a row's in the words that hold its ends may be
+ * read too; their values do not matter.  tokens == 0 or
  * rows == 0 is a no-op.  Negative sizes, a leading dimension below its row, an
  * unknown out_type, a workspace that is too small or a null pointer ->
  * SIGNROT_EINVAL.  No allocation.  Asynchronous.

@@ -254,7 +254,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   int src_p = p, lq, lq_end;
   const uint8_t *base_w, *base_t, *base_s;
   int rows_w, rows_t;
-  uint32_t size_w, size_t_, size_s;
+  uint32_t size_w, size_t_;
   uint32_t off_w[C::kWLoads], off_t[C::kTLoads];  // of the lane's rows
   uint32_t off_s[C::kPer][4];                     // of its rows of scales
   // byte of the lane's chunk in a stage: rows 8 (k wave + l) + lane / 8
@@ -293,8 +293,6 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       off_t[l] = static_cast<uint32_t>(min(r, rows_t - 1)) * static_cast<uint32_t>(a.lda);
     }
     if (ORDERED) return;
-    size_s = static_cast<uint32_t>((of_w ? rows_w : rows_t) - 1) * static_cast<uint32_t>(of_w ? a.ldws : a.lds) +
-             ((blocks + 3) & ~3);
     const int i = lane_here() & 15;
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x)
@@ -337,7 +335,11 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
   };
 
   // The scales of the quad, words s = g of the rows; those beyond n read the quad's first.
-  uint32_t raw[C::kPer][4];
+  // Words at any address: a row's last one ends at its end, shifted into place later
+  // (rows of fewer than four blocks start on words).  Laying them out on words first
+  // took 3.3 us of the 11.1 of 613 x 1120 x 777.
+  typedef uint32_t any_u32_t __attribute__((aligned(1)));
+  uint32_t raw[C::kPer][4], raw_shift = 0;
   int raw_left = 0;
   auto load_scales = [&](int half) {
     if (ORDERED) {
@@ -350,20 +352,23 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       return;
     }
     raw_left = left / mx::kBlockBytes;
-    const uint32_t word = 4 * g < raw_left ? 4 * g : 0;
-    const __amdgpu_buffer_rsrc_t src = wave::buffer_rsrc(base_s, size_s);
+    const int word = at_quad / mx::kBlockBytes + (4 * g < raw_left ? 4 * g : 0);
+    const int from = min(word, max(blocks - 4, 0));
+    raw_shift = 8 * (word - from);
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x)
 #pragma unroll
       for (int f = 0; f < 4; ++f)
-        raw[x][f] = __builtin_amdgcn_raw_buffer_load_b32(src, off_s[x][f] + word, at_quad / mx::kBlockBytes, 0);
+        raw[x][f] = *reinterpret_cast<const any_u32_t*>(base_s + (off_s[x][f] + static_cast<uint32_t>(from)));
   };
   auto turn_scales = [&](int half) {
     uint32_t* const turned = reinterpret_cast<uint32_t*>(lds_s + 1024 * group + 256 * g) + i;
 #pragma unroll
     for (int x = 0; x < C::kPer; ++x) {
-      uint32_t o[4];
-      turned_words(raw[x], o);
+      uint32_t d[4], o[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) d[f] = raw[x][f] >> raw_shift;
+      turned_words(d, o);
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         turned[half * (C::kScales / 4) + 256 * x + 16 * b] = 4 * g + b < raw_left ? o[b] : 0;
@@ -793,13 +798,19 @@ MxPlan tile_plan(int64_t T, int64_t n, int64_t R) {
 // 1 are 2 g + s, and their scales the bytes of one 16-bit word; a row's eight
 // scales of a unit are loaded as two words.  Beyond n the codes are the unit's
 // first and the scales of both operands 2^-127: products that are zero in binary32.
+//
+// BYTES: rows of scales at any address (16 x 28704 x 8192 35.8 us, 33.8 on words).  A
+// row's eight lie in three words then.
 constexpr int kUnit = 128;
+constexpr int64_t kMaxPitch = 1 << 23;  // a tile's offsets stay below 2^32
 
-template <int FK, int FT, int D>
+template <int FK, int FT, int D, bool BYTES>
 struct Few {
   static constexpr int kWBytes = 16 * FK * kUnit, kTBytes = 16 * FT * kUnit;
   static constexpr int kWLoads = kWBytes / 1024, kTLoads = kTBytes / 1024;
-  static constexpr int kSLoads = (32 * (FK + FT) + 63) / 64;  // of 64 words of scales
+  // scales: words of a row's eight, and loads of 64 of them
+  static constexpr int kWords = BYTES ? 3 : 2;
+  static constexpr int kSLoads = (16 * kWords * (FK + FT) + 63) / 64;
   static constexpr int kLoads = kWLoads + kTLoads + kSLoads;
   static constexpr int kSlot = kWBytes + kTBytes + 256 * kSLoads;
   static constexpr int kWave = D * kSlot;
@@ -807,9 +818,9 @@ struct Few {
   static_assert(1024 * FK * FT <= kWave, "a wave's partial sums take its ring's place");
 };
 
-template <int FK, int FT, int D>
+template <int FK, int FT, int D, bool BYTES>
 __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
-  using C = Few<FK, FT, D>;
+  using C = Few<FK, FT, D, BYTES>;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -837,13 +848,22 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
 #pragma unroll
   for (int l = 0; l < C::kTLoads; ++l)
     off_t[l] = static_cast<uint32_t>(min(8 * l + (lane >> 3), a.T - 1)) * static_cast<uint32_t>(a.lda);
-  // words of scales: two a row, weights' rows first
+  // words of scales, weights' rows first: of the word that a row starts in, and the
+  // row's end from there
+  auto scales_of = [&](int r) {
+    return r < 16 * FK ? a.w_scale + static_cast<int64_t>(n0 + min(r, rows_w - 1)) * a.ldws
+                       : a.scale + static_cast<int64_t>(min(r - 16 * FK, a.T - 1)) * a.lds;
+  };
+  auto shift_of = [&](int r) {
+    return BYTES ? static_cast<int>(reinterpret_cast<uintptr_t>(scales_of(r)) & 3) : 0;
+  };
   const uint8_t* src_s[C::kSLoads];
+  int end_s[C::kSLoads];
 #pragma unroll
   for (int q = 0; q < C::kSLoads; ++q) {
-    const int r = (64 * q + lane) >> 1;
-    src_s[q] = r < 16 * FK ? a.w_scale + static_cast<int64_t>(n0 + min(r, rows_w - 1)) * a.ldws
-                           : a.scale + static_cast<int64_t>(min(r - 16 * FK, a.T - 1)) * a.lds;
+    const int r = (64 * q + lane) / C::kWords;
+    src_s[q] = scales_of(r) - shift_of(r);
+    end_s[q] = blocks + shift_of(r);
   }
   // unit x of this wave into ring slot x % D
   auto issue = [&](int x) {
@@ -859,13 +879,24 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(src_t,
                                                (__attribute__((address_space(3))) void*)(slot + C::kWBytes + 1024 * l), 16,
                                                off_t[l] + (chunk_at(l) < left ? chunk_at(l) : 0), kUnit * u, 0, 0);
-    const int word = 4 * (lane & 1);
 #pragma unroll
-    for (int q = 0; q < C::kSLoads; ++q)
+    for (int q = 0; q < C::kSLoads; ++q) {
+      const int word = 4 * ((64 * q + lane) % C::kWords);
       __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(src_s[q] + 8 * u + (word < left / mx::kBlockBytes ? word : 0)),
+          (const __attribute__((address_space(1))) void*)(src_s[q] + 8 * u + (8 * u + word < end_s[q] ? word : 0)),
           (__attribute__((address_space(3))) void*)(slot + C::kWBytes + C::kTBytes + 256 * q), 4, 0, 0);
+    }
   };
+  // the lane's rows of scales in a slot, blocks 2 g and 2 g + 1
+  int at_w[FK], at_t[FT];
+#pragma unroll
+  for (int f = 0; f < FK; ++f) at_w[f] = 4 * C::kWords * (16 * f + i) + shift_of(16 * f + i) + 2 * g;
+#pragma unroll
+  for (int j = 0; j < FT; ++j)
+    at_t[j] = 4 * C::kWords * (16 * (FK + j) + i) + shift_of(16 * (FK + j) + i) + 2 * g;
+  // (16-bit accesses: bytes would alias the loads to LDS, and the compiler wait for all)
+  typedef uint16_t any_u16_t __attribute__((aligned(1)));
+  auto pair_at = [](const uint8_t* p) -> uint32_t { return *reinterpret_cast<const any_u16_t*>(p); };
 
   f32x4_t acc[FK][FT];
 #pragma unroll
@@ -885,9 +916,9 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
     i32x4_t w[2][FK], tok[2][FT];
     uint32_t cw[FK], ct[FT];
 #pragma unroll
-    for (int f = 0; f < FK; ++f) cw[f] = *reinterpret_cast<const uint16_t*>(ss + 8 * (16 * f + i) + 2 * g);
+    for (int f = 0; f < FK; ++f) cw[f] = pair_at(ss + at_w[f]);
 #pragma unroll
-    for (int j = 0; j < FT; ++j) ct[j] = *reinterpret_cast<const uint16_t*>(ss + 8 * (16 * (FK + j) + i) + 2 * g);
+    for (int j = 0; j < FT; ++j) ct[j] = pair_at(ss + at_t[j]);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -897,6 +928,11 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
       for (int j = 0; j < FT; ++j)
         tok[s][j] = *reinterpret_cast<const i32x4_t*>(st + 2048 * j + kUnit * i + 16 * ((2 * g + s) ^ h(i)));
     }
+    // The slot is free once the reads are done; they are not ordered with the loads.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (x + D < count) issue(x + D);
+    __builtin_amdgcn_sched_barrier(0);
     const int here = blocks - 8 * (wid + x * waves);  // blocks from this unit on
     if (here < 8) {
       const uint32_t keep = 2 * g + 1 < here ? 0xffffu : 2 * g < here ? 0xffu : 0u;
@@ -912,8 +948,6 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
         acc[f][j] = mfma<0, 0>(w[0][f], tok[0][j], acc[f][j], cw[f], ct[j]);
         acc[f][j] = mfma<1, 1>(w[1][f], tok[1][j], acc[f][j], cw[f], ct[j]);
       }
-    __builtin_amdgcn_sched_barrier(0);
-    if (x + D < count) issue(x + D);
   }
 #pragma unroll
   for (int f = 0; f < FK; ++f)
@@ -933,21 +967,31 @@ __device__ __forceinline__ void mx_few(const MxArgs& a, uint8_t* few_lds) {
   }
 }
 
-template <int FK, int FT, int D>
+template <int FK, int FT, int D, bool BYTES>
 __global__ __launch_bounds__(512) void mx_few_kernel(MxArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
-  mx_few<FK, FT, D>(a, few_lds);
+  mx_few<FK, FT, D, BYTES>(a, few_lds);
+}
+
+template <int FK, int FT, int D, bool BYTES>
+hipError_t run_few_rows(const MxArgs& a, hipStream_t s) {
+  using C = Few<FK, FT, D, BYTES>;
+  const int groups = (a.R + 16 * FK - 1) / (16 * FK), units = (a.n / 2 + kUnit - 1) / kUnit;
+  int waves = 8;
+  while (waves > 2 && (groups * waves > 8 * kCus || units < waves)) waves /= 2;
+  mx_few_kernel<FK, FT, D, BYTES><<<dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(64 * waves)),
+                            static_cast<unsigned>(waves * C::kWave), s>>>(a);
+  return hipGetLastError();
+}
+
+bool aligned_rows(const uint8_t* p, int64_t ld, int64_t to) {
+  return ld % to == 0 && (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0 && ld < kMaxPitch;
 }
 
 template <int FK, int FT, int D>
 hipError_t run_few_as(const MxArgs& a, hipStream_t s) {
-  using C = Few<FK, FT, D>;
-  const int groups = (a.R + 16 * FK - 1) / (16 * FK), units = (a.n / 2 + kUnit - 1) / kUnit;
-  int waves = 8;
-  while (waves > 2 && (groups * waves > 8 * kCus || units < waves)) waves /= 2;
-  mx_few_kernel<FK, FT, D><<<dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(64 * waves)),
-                            static_cast<unsigned>(waves * C::kWave), s>>>(a);
-  return hipGetLastError();
+  return aligned_rows(a.scale, a.lds, 4) && aligned_rows(a.w_scale, a.ldws, 4) ? run_few_rows<FK, FT, D, false>(a, s)
+                                                                               : run_few_rows<FK, FT, D, true>(a, s);
 }
 
 // 32 channels a work-group halve what it reads of the tokens, which up to sixteen
@@ -966,12 +1010,10 @@ hipError_t run_few(const MxArgs& a, hipStream_t s) {
   return a.T <= 16 ? run_few_as<1, 1, 4>(a, s) : run_few_as<1, 2, 2>(a, s);
 }
 
-constexpr int64_t kMaxPitch = 1 << 23;  // a tile's offsets stay below 2^32
-
 // ---- any stride and alignment ---------------------------------------------------
 //
-// Rows that do not start on 16-byte boundaries (codes) or 4-byte ones (scales)
-// are laid out anew in the workspace, in rows of whole 16-byte chunks.
+// Rows that do not start on 16-byte boundaries (codes), or 4-byte ones (fewer than four
+// scales), are laid out anew in the workspace, in rows of whole 16-byte chunks.
 struct Copy {
   const uint8_t* src;
   int64_t ld;
@@ -1005,10 +1047,6 @@ __global__ __launch_bounds__(256) void mx_copy_kernel(Copies all) {
   }
 }
 
-bool aligned_rows(const uint8_t* p, int64_t ld, int64_t to) {
-  return ld % to == 0 && (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0 && ld < kMaxPitch;
-}
-
 // The workspace after the partial sums: the copies that the operands need and, for
 // tiles that take them so, the ordered scales.  a takes what is laid out anew.
 struct Layout {
@@ -1020,8 +1058,9 @@ struct Layout {
     copy(a, a.a, a.lda, a.T, a.n / 2, 16);
     copy(a, a.w, a.ldw, a.R, a.n / 2, 16);
     if (!ordered) {
-      copy(a, a.scale, a.lds, a.T, a.n / 32, 4);
-      copy(a, a.w_scale, a.ldws, a.R, a.n / 32, 4);
+      const int blocks = a.n / mx::kBlock;
+      copy(a, a.scale, a.lds, a.T, blocks, blocks < 4 ? 4 : 1);
+      copy(a, a.w_scale, a.ldws, a.R, blocks, blocks < 4 ? 4 : 1);
       return;
     }
     order.blocks = a.n / mx::kBlock;

@@ -150,3 +150,26 @@ def test_products_on_two_streams_at_once():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("t", [1, 3, 16, 29, 33, 70, 300])
+@pytest.mark.parametrize("n,rows", [(32, 300), (64, 40), (96, 8200), (160, 77), (1120, 777), (2080, 8200), (4256, 2100)])
+def test_scales_at_any_address(t, n, rows):
+    """The same bits as from aligned rows, whatever stands beside them (0xff: NaN)."""
+    x, w = operand(t, n, t + 3), operand(rows, n, n)
+    want = R.mxfp4_linear(*x, *w, dtype=F32)
+    assert torch.isfinite(want).all()
+
+    def moved(scale, off, pitch):
+        count, nb = scale.shape
+        room = torch.full((off + count * pitch + 64,), 255, dtype=torch.uint8, device="cuda")
+        view = room[off:off + count * pitch].view(count, pitch)[:, :nb]
+        view.copy_(scale)
+        return view
+
+    nb = n // 32
+    for off_x, off_w, wide in ((0, 0, 0), (1, 2, 0), (3, 1, 1), (2, 0, 2), (0, 3, 3)):
+        a, b = moved(x[1], off_x, nb + wide), moved(w[1], off_w, nb + wide)
+        assert torch.equal(R.mxfp4_linear(x[0], a, w[0], b, dtype=F32), want), (off_x, off_w, wide)
+        assert torch.equal(R.mxfp4_linear(x[0], x[1], w[0], b, dtype=F32), want)
+        assert torch.equal(R.mxfp4_linear(x[0], a, *w, dtype=F32), want)
