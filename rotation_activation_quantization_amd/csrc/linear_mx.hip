@@ -46,54 +46,30 @@ __device__ __forceinline__ f32x4_t mfma(const i32x4_t& a, const i32x4_t& b, cons
 
 // acc += a b in place, for the tiles: left to itself the compiler gives results
 // and sums registers of their own, which a tile that takes nearly all of them
-// does not have, and moves them about.  AGPR: the sums are accumulation
-// registers.  The leading s_nop covers a VALU write of an operand just before.
-// The reader of a sum has to wait for the last one (settle).
-template <int OA, int OB, bool AGPR>
+// does not have, and moves them about.  The leading s_nop covers a VALU write of an
+// operand just before.  The reader of a sum has to wait for the last one (settle).
+template <int OA, int OB>
 __device__ __forceinline__ void mfma_to(f32x4_t& acc, const i32x4_t& a, const i32x4_t& b, uint32_t sa, uint32_t sb) {
-#define SR_MFMA "s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
-  if constexpr (AGPR)
-    asm volatile(SR_MFMA
-                 : "+a"(acc)
-                 : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
-  else
-    asm volatile(SR_MFMA
-                 : "+v"(acc)
-                 : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
-#undef SR_MFMA
-}
-// A sum's value, read where it is asked for and not before.
-template <bool AGPR>
-__device__ __forceinline__ float value_of(float sum) {
-  if constexpr (!AGPR) return sum;
-  float v;
-  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(sum));
-  return v;
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] "
+               "op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+               : "+v"(acc)
+               : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// Results of token t from channel k on: vectors at whatever address they have,
+// Four results of token t from channel k on: a vector at whatever address it has,
 // single ones at the row's end.
-template <int N>
-__device__ __forceinline__ void store_results(const MxArgs& a, int t, int k, const float (&o)[N]) {
+__device__ __forceinline__ void store_results(const MxArgs& a, int t, int k, const float (&o)[4]) {
   const int64_t at = static_cast<int64_t>(t) * a.ldo + k;
-  const bool whole = k + N <= a.R;
+  const bool whole = k + 4 <= a.R;
   if (whole && a.out_bf16) {
-    uint16_t* const out = static_cast<uint16_t*>(a.out) + at;
-    uint32_t h[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) h[e] = row::pack_bf16(o[2 * e], o[2 * e + 1]);
-    if (N == 4) row::store_as<false>(out, wave::u32x2_t{h[0], h[1]});
-#pragma unroll
-    for (int e = 0; e < N / 8; ++e)
-      row::store_as<false>(out + 8 * e, wave::u32x4_t{h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]});
+    row::store_as<false>(static_cast<uint16_t*>(a.out) + at,
+                         wave::u32x2_t{row::pack_bf16(o[0], o[1]), row::pack_bf16(o[2], o[3])});
   } else if (whole) {
-    float* const out = static_cast<float*>(a.out) + at;
-#pragma unroll
-    for (int e = 0; e < N; e += 4) row::store_as<false>(out + e, f32x4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
+    row::store_as<false>(static_cast<float*>(a.out) + at, f32x4_t{o[0], o[1], o[2], o[3]});
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < 4; ++e)
       if (k + e < a.R) row::store_elem(a.out, at + e, o[e], a.out_bf16);
   }
 }
@@ -144,7 +120,6 @@ struct Tile {
   static constexpr int kWStage = kBN * kStage, kTStage = kBM * kStage;
   static constexpr int kWLoads = kWStage / 1024 / kWaves, kTLoads = kTStage / 1024 / kWaves;
   static constexpr int kLoads = kWLoads + kTLoads;
-  static constexpr bool kAgpr = FK * FT > 32;
   static constexpr int kPart = 256 * FK * FT * kWaves;  // floats of a tile's partial sums
   // scales: groups of 64 rows (weights, then tokens), a word of four rows' for
   // each lane and depth
@@ -179,6 +154,14 @@ struct Tile {
 // stage's loads all go out before the stores, so that the wait in the next tile's
 // first stage can leave the stores on their way (8192 x 4096 x 4096 71.2 us, 72.9
 // with the wait for them).
+//
+// What bounds a large product is the matrix units at the clock that their power leaves:
+// 8192 x 4096 x 14336 takes 230 to 250 us (3.9 to 4.2 PFLOP/s) with the units 65 % busy
+// at 1.8 GHz; all zeros run at 2.3 GHz.  Alone, on values in registers, the instruction
+// reaches 7.0 PFLOP/s of random codes and 9.3 of zeros.  Of the rest, loads cost some
+// 15 % of the cycles, LDS reads 9 %, a tile's start and stores 6 us.  Four waves of 128 x
+// 128 (a third fewer LDS reads) were slower, as were stores past the caches and staggered
+// starts.
 //
 // A row is cut into quads of four depths (512 channels, two stages).  Quad 0 of
 // a tile is the row's last, possibly short one.  Its chunks beyond n are read
@@ -476,7 +459,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
         }
         // The reads follow the block's first MFMA: the wait before that one is
         // then for reads a whole block old.
-        mfma_to<f % 4, 0, C::kAgpr>(acc[f][0], wf[f], now[0], sw[u][f / 4], st[u][0]);
+        mfma_to<f % 4, 0>(acc[f][0], wf[f], now[0], sw[u][f / 4], st[u][0]);
         __builtin_amdgcn_sched_barrier(0);
         wf[f + 2] = f + 2 < FK ? weight(pos, u, f + 2) : weight(u == 0 ? pos : next, u ^ 1, f + 2 - FK);
         if (u == 0) {
@@ -497,7 +480,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
         }
         unrolled<FT - 1>([&](auto T) {
           constexpr int t = decltype(T)::value + 1;
-          mfma_to<f % 4, t % 4, C::kAgpr>(acc[f][t], wf[f], now[t], sw[u][f / 4], st[u][t / 4]);
+          mfma_to<f % 4, t % 4>(acc[f][t], wf[f], now[t], sw[u][f / 4], st[u][t / 4]);
         });
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -581,10 +564,10 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
           for (int e = 0; e < 4; ++e) {
             if constexpr (BF16)
               v[e] = row::pack_bf16(
-                  value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1)]) + bias[q][8 * h + 2 * e],
-                  value_of<C::kAgpr>(acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1) + 1]) + bias[q][8 * h + 2 * e + 1]);
+                  acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1)] + bias[q][8 * h + 2 * e],
+                  acc[4 * q + 2 * h + (e >> 1)][j][2 * (e & 1) + 1] + bias[q][8 * h + 2 * e + 1]);
             else
-              v[e] = __float_as_uint(value_of<C::kAgpr>(acc[4 * q + 2 * part + h][j][e]) +
+              v[e] = __float_as_uint(acc[4 * q + 2 * part + h][j][e] +
                                      bias[q][8 * part + 4 * h + e]);
           }
           *chunk_at(i, BF16 ? 4 * h + g : 2 * g + h) = v;

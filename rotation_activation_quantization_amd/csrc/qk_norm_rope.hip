@@ -76,7 +76,7 @@ __device__ __forceinline__ float inverse_root(float x) {
 }
 
 // Squares of values around 2^64 and more pass binary32's range; such a head is
-// summed again, scaled by this (eps is then below a rounding of the mean).
+// normed again, its values scaled by this.
 constexpr float kSmall = 0x1p-80f;
 
 // Eight values as they lie in memory.
@@ -110,14 +110,19 @@ __device__ __forceinline__ void widen(const Raw& r, float (&v)[8]) {
 enum Pairs { kOwn, kAcross, kChunks, kAnywhere };
 
 // A lane holds eight channels of a head, G lanes a head, so that a wave takes
-// 64 / G heads of a token at a time, read and written once.  Bound by memory
-// where tokens are many.  A wave goes over its token's queries, every parts-th
-// group of heads, then over the keys; the next group's loads are on their way while
-// one is computed.  With weight w, bias b and angles of the token, channel j with
-// partner p and the sign of p's part in the sine,
+// 64 / G heads of a token at a time, read and written once.  A wave goes over its
+// token's queries, every parts-th group of heads, then over the keys; the next
+// group's loads are on their way while one is computed.  With weight w, bias b and
+// angles of the token, channel j with partner p and the sign of p's part in the sine,
 //   out_j = r (x_j - mean) w_j cos_j + r (x_p - mean) w_p sin_j + (b_j cos_j + b_p sin_j):
 // the factors w_j cos_j, w_p sin_j and the last sum are formed once a token and kept
-// for all its heads.
+// for all its heads (8192 tokens of 64 + 8 heads of 128, bf16: 106 us with angles and
+// weights read for each head, 77 so).
+//
+// Bound by memory where tokens are many: that shape now 52 us, 5.8 TB/s; with
+// interleaved pairs 57; through LDS, half of the channels rotated, 52; 80 channels,
+// where six of a head's sixteen lanes idle, 40; binary32 (4096 tokens of 64 heads) 55,
+// 4.9 TB/s.  That takes eight waves a SIMD, 64 registers.
 template <int G, bool BF16, bool WHOLE, int PAIRS>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int parts, int stream) {
   __shared__ __attribute__((aligned(16))) float sh[PAIRS >= kChunks ? kWaves : 1][64 * 8];
@@ -200,6 +205,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (PAIRS == kOwn ? !(e & 1) : ch.at + e < half) sn[e] = -sn[e];  // the first of a pair
+        if (PAIRS != kAcross && ch.at + e >= rotary) wp[e] = bp[e] = 0.f;
         wc[e] = w[e] * cs[e];
         ws[e] = wp[e] * sn[e];
         add[e] = biased ? fmaf(bp[e], sn[e], b[e] * cs[e]) : 0.f;
@@ -212,8 +218,9 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       const bool on = live && h < heads;
       float v[8], o[8];
       widen<BF16>(raw, v);
-      float mean = 0.f, r = 1.f;
-      if (normed) {
+      float mean = 0.f, r = 1.f, scale = 1.f;
+      // (a second time if a head is large; which one is the same in all lanes of it)
+      for (bool more = normed; more;) {
         if (a.norm == SIGNROT_NORM_LAYER) {
           float s = 0.f;
 #pragma unroll
@@ -229,14 +236,14 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         for (int e = 0; e < 8; ++e)
           if (ch.own(e)) ss = fmaf(v[e], v[e], ss);
         ss = head_sum<G>(live ? ss : 0.f);
-        r = inverse_root(fmaf(ss, inv_n, a.eps));
-        if (!(ss < INFINITY)) {  // the same in all lanes of a head
-          float sm = 0.f;
+        r = inverse_root(fmaf(ss, inv_n, a.eps * scale * scale));
+        const bool large = scale == 1.f && !(ss < INFINITY);
+        more = __builtin_amdgcn_ballot_w64(large) != 0;
+        if (more) {
+          scale = large ? kSmall : scale;
+          widen<BF16>(load(gr), v);  // read again: raw does not have to stay
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (ch.own(e)) sm = fmaf(v[e] * kSmall, v[e] * kSmall, sm);
-          sm = head_sum<G>(live ? sm : 0.f);
-          r = kSmall * inverse_root(fmaf(sm, inv_n, a.eps * kSmall * kSmall));
+          for (int e = 0; e < 8; ++e) v[e] *= scale;
         }
       }
       float other[8];
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         }
         widen<BF16>(far, other);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] -= mean;
+        for (int e = 0; e < 8; ++e) other[e] = fmaf(other[e], scale, -mean);
       } else {
         if (live) {
 #pragma unroll
@@ -264,6 +271,14 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         for (int e = 0; e < 8; ++e) other[e] = mine[PAIRS == kChunks ? partner(ch.at) + e : partner(ch.at + e)];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+      }
+      if (PAIRS != kAcross && rotary < head) {
+        // (a channel that is not rotated takes nothing of another one, not even of an infinity)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int at = ch.at + (PAIRS == kChunks ? 0 : PAIRS == kOwn ? e & 6 : e);
+          other[e] = at < rotary ? other[e] : 0.f;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = fmaf(fmaf(other[e], ws[e], v[e] * wc[e]), r, add[e]);
@@ -310,7 +325,8 @@ void run(const Args& a, bool whole, hipStream_t s) {
                     : whole && G > 1 && a.rotary == a.head && a.head == 8 * G ? kAcross
                     : whole && a.rotary % 16 == 0                             ? kChunks
                                                                               : kAnywhere;
-  // a launch holds fewer than 2^32 threads
+  // Fewer than 4096 tokens: several waves a token, up to one a group of heads, to have
+  // waves for 1024 SIMDs.  A launch holds fewer than 2^32 threads.
   const int64_t most = (int64_t{1} << 25) / parts;
   for (int64_t t = 0; t < a.tokens; t += most) {
     Args b = a;

@@ -18,6 +18,8 @@ struct At {
   __device__ __forceinline__ At(uint32_t c, uint32_t per) : row(c / per), chunk(c - row * per) {}
 };
 
+// Bound by memory: 8192 x 14336 bf16 55.6 us (5.35 TB/s), binary32 91.6 (5.8).
+//
 // A lane takes eight values and four neighbouring lanes a block, so that a
 // wave reads 1 KiB (bf16) of one row side by side and writes 256 bytes of codes.
 // The block's maximum is two DPP steps over the four lanes' bits.

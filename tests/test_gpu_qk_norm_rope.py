@@ -185,6 +185,41 @@ def test_large_and_non_finite_heads():
         assert not torch.isfinite(g[bad]).all() and torch.equal(g[keep], c[keep])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rotary", [(128, 128), (128, 64), (80, 36), (24, 10), (36, 18), (512, 512), (8, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_heads_at_the_end_of_the_range(d, rotary, dtype, interleaved):
+    """Values whose sums, squares, and products with the weights pass binary32's range, beside ordinary heads."""
+    q, k, p = make(9, 6, 3, d, rotary, F32, 8)
+    q[2, 1] = q[2, 1] / q[2, 1].abs().max() * 3e38
+    q[5] = q[5] / q[5].abs().max() * 1e30
+    k[4, 2] = 3e38 + 0 * k[4, 2]
+    k[4, 2, 1] = -3e38
+    k[8, 0] *= 0
+    q, k = q.to(dtype), k.to(dtype)
+    for name in ("q_weight", "k_weight"):
+        p[name] = p[name] * 8
+    at = p["positions"].cpu().numpy()
+    for norm in ("rms", "layer"):
+        got = call(q, k, p, norm=norm, interleaved=interleaved, dtype=F32)
+        check(got[0], q, p, "q", norm, interleaved, F32, at)
+        check(got[1], k, p, "k", norm, interleaved, F32, at)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rotary", [(128, 64), (128, 32), (80, 36), (24, 10), (36, 18), (128, 0)])
+def test_channels_that_are_not_rotated_take_nothing_of_others(d, rotary, interleaved):
+    q, k, p = make(6, 5, 2, d, rotary, F32, 9)
+    clean = call(q, k, p, norm="none", interleaved=interleaved)
+    q[1, 3, rotary + 2] = float("inf")
+    q[2, 4, d - 1] = float("nan")
+    k[3, 1, rotary] = -float("inf")
+    got = call(q, k, p, norm="none", interleaved=interleaved)
+    for x, g, c in ((q, got[0], clean[0]), (k, got[1], clean[1])):
+        odd = ~torch.isfinite(x)
+        assert torch.equal(g[~odd], c[~odd]) and torch.equal(g[odd].nan_to_num(7.0), x[odd].nan_to_num(7.0))
+
+
 def test_equal_channels_center_to_the_bias():
     q = torch.full((3, 2, 72), 1.1, dtype=BF16, device="cuda")
     got, _ = R.qk_norm_rope(q, norm="layer")
