@@ -119,10 +119,11 @@ enum Pairs { kOwn, kAcross, kChunks, kAnywhere };
 // for all its heads (8192 tokens of 64 + 8 heads of 128, bf16: 106 us with angles and
 // weights read for each head, 77 so).
 //
-// Bound by memory where tokens are many: that shape now 52 us, 5.8 TB/s; with
+// Bound by memory where tokens are many: that shape now 61 us on inputs from HBM
+// (5.0 TB/s), and in a loop over the same ones, which the caches hold in part, 52; with
 // interleaved pairs 57; through LDS, half of the channels rotated, 52; 80 channels,
-// where six of a head's sixteen lanes idle, 40; binary32 (4096 tokens of 64 heads) 55,
-// 4.9 TB/s.  That takes eight waves a SIMD, 64 registers.
+// where six of a head's sixteen lanes idle, 40; binary32 (4096 tokens of 64 heads) 55.
+// That takes eight waves a SIMD, 64 registers (67: 58 us for the 52).
 template <int G, bool BF16, bool WHOLE, int PAIRS>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int parts, int stream) {
   __shared__ __attribute__((aligned(16))) float sh[PAIRS >= kChunks ? kWaves : 1][64 * 8];
@@ -316,6 +317,9 @@ template <int G>
 void run(const Args& a, bool whole, hipStream_t s) {
   constexpr int kHeads = 64 / G;
   const int groups = (a.q_heads + kHeads - 1) / kHeads + (a.k_heads + kHeads - 1) / kHeads;
+  // Fewer than 4096 tokens: several waves a token, up to one a group of heads, to have
+  // waves for 1024 SIMDs (16 tokens 8.5 us, 13.7 with one; 1024 13.0 and 18.1; 2048 20.8
+  // and 23.4).
   int parts = 1;
   while (parts < groups && a.tokens * parts < 4096) parts *= 2;
   if (parts > groups) parts = groups;
@@ -325,8 +329,7 @@ void run(const Args& a, bool whole, hipStream_t s) {
                     : whole && G > 1 && a.rotary == a.head && a.head == 8 * G ? kAcross
                     : whole && a.rotary % 16 == 0                             ? kChunks
                                                                               : kAnywhere;
-  // Fewer than 4096 tokens: several waves a token, up to one a group of heads, to have
-  // waves for 1024 SIMDs.  A launch holds fewer than 2^32 threads.
+  // A launch holds fewer than 2^32 threads.
   const int64_t most = (int64_t{1} << 25) / parts;
   for (int64_t t = 0; t < a.tokens; t += most) {
     Args b = a;

@@ -63,10 +63,11 @@ __device__ __forceinline__ void store_as(void* p, const T& v) {
 }
 
 // Sixteen bytes out; `stream`: past the caches, for bf16 results that they would not
-// hold until they are read (the per-head norms of 8192 tokens of 64 + 8 heads of 128
-// took 76.6 us with ordinary stores, 70.0 so).  Binary32 results leave a lane as two
-// stores, halves of lines to the memory if they went past: 8192 x 14336 values of
-// MXFP4 codes 212 us, 104 with ordinary stores.
+// hold until they are read.  Per-head norms of 8192 tokens of 64 + 8 heads of 128 take
+// 64.9 us with ordinary stores, 61.0 so; together with a read of the results 4096 tokens
+// (72 MiB) 116.5 and 111.5, but 3000 (53 MiB) 80.7 and 87.5.  Binary32 results leave a
+// lane as two stores, halves of lines to the memory if they went past: 8192 x 14336
+// values of MXFP4 codes 212 us, 104 with ordinary stores.
 inline int past_caches(int64_t results, int bf16) { return bf16 && 2 * results > (int64_t{64} << 20); }
 template <bool ALIGNED>
 __device__ __forceinline__ void store_chunk(void* p, const u32x4_t& v, int stream) {
