@@ -638,8 +638,8 @@ int signrot_swiglu_rotate_quant_mxfp4(const void* gate_bf16, const void* up_bf16
  * r = positions[t] (clamped into [0, places)), or t when positions is NULL.
  * Channels from `rotary` on are normed only.  All arithmetic is binary32; each
  * result is rounded once.  A head that holds an infinity or NaN gives
- * unspecified results in that head only; so does one whose sum, for LAYER,
- * passes binary32's range (its squares may).
+ * unspecified results in that head only, with NORM_NONE in its pair only.  Sums
+ * and squares may pass binary32's range: such a head is normed on scaled values.
  *
  *   tokens, head, rotary   0 <= tokens < 2^31; channels of a head, even, in
  *                 [8, 512]; rotated channels, even, in [0, head].
