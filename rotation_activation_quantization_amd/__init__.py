@@ -915,7 +915,8 @@ _pack_qk_args = struct.Struct("@" + "".join(
 
 
 def _heads_of(v, name, t, heads, d, dtype, gpu):
-    """(pointer, token stride, head stride) of a [T, heads, d] tensor with contiguous heads; None sizes are free."""
+    """(its shape, pointer, token stride, head stride) of a [T, heads, d] tensor with contiguous heads; None sizes
+    are free."""
     shape = v.shape
     if v.dtype is not dtype or len(shape) != 3 or v.get_device() != gpu:
         raise ValueError(f"{name} must be a 3-D {dtype} tensor on GPU {gpu}")
@@ -926,20 +927,20 @@ def _heads_of(v, name, t, heads, d, dtype, gpu):
     step, hop, unit = v.stride()
     if unit != 1:
         raise ValueError(f"{name} heads must be contiguous")
-    return v.data_ptr(), step, hop
+    return shape, v.data_ptr(), step, hop
 
 
-def _heads_out(v, name, like, dtype, gpu):
-    """(out, pointer, strides) of the result for the [T, heads, d] tensor `like`, allocated when v is None."""
+def _heads_out(v, name, shape, dtype, device, gpu):
+    """(out, pointer, strides) of the result of a [T, heads, d] shape, allocated when v is None."""
     import torch
 
-    t, heads, d = like.shape
+    t, heads, d = shape
     if v is None:
-        v = torch.empty(t, heads, d, dtype=dtype, device=like.device)
+        v = torch.empty(t, heads, d, dtype=dtype, device=device)
         return v, v.data_ptr(), heads * d, d
-    ptr, step, hop = _heads_of(v, name, t, heads, d, dtype, gpu)
+    _, ptr, step, hop = _heads_of(v, name, t, heads, d, dtype, gpu)
     reach = d  # elements of the axes so far: the next one has to step over them
-    for stride, count in sorted(((hop, heads), (step, t))):
+    for stride, count in ((hop, heads), (step, t)) if hop <= step else ((step, t), (hop, heads)):
         if count > 1:
             if stride < reach:
                 raise ValueError(f"{name} heads overlap")
@@ -966,8 +967,8 @@ def signrot_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, norm: st
 
     device, gpu = _on_gpu(q, "q")
     in_type = _type_of(q.dtype, "q")
-    qptr, ldq, hsq = _heads_of(q, "q", None, None, None, q.dtype, gpu)
-    t, heads, d = q.shape
+    q_shape, qptr, ldq, hsq = _heads_of(q, "q", None, None, None, q.dtype, gpu)
+    t, heads, d = q_shape
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}")
     for v in (q_out, k_out):
@@ -975,38 +976,43 @@ def signrot_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, norm: st
             if dtype is not None and v.dtype is not dtype:
                 raise ValueError(f"an output is {v.dtype}, dtype {dtype}")
             dtype = v.dtype
-    dtype = q.dtype if dtype is None else dtype
-    out_type = _type_of(dtype, "the result")
-    param = torch.bfloat16
-    for v in (q_weight, k_weight, q_bias, k_bias):
-        if v is not None:
+    if dtype is None or dtype is q.dtype:
+        dtype, out_type = q.dtype, in_type
+    else:
+        out_type = _type_of(dtype, "the result")
+    param, p_type, vectors = None, _BF16, []
+    for v, name in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_bias, "q_bias"), (k_bias, "k_bias")):
+        if v is None:
+            vectors.append(0)
+            continue
+        if param is None:
             param = v.dtype
-            break
-    p_type = _type_of(param, "the norm's parameters")
+            p_type = _type_of(param, "the norm's parameters")
+        vectors.append(_vector(v, name, d, param, gpu))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     cptr = zptr = pptr = ldt = places = rotary = wide = 0
     if cos is not None:
         cptr, ldt = _matrix(cos, "cos", None, None, torch.float32, gpu)
-        places, rotary = cos.shape[0], 2 * cos.shape[1]
-        zptr, lds = _matrix(sin, "sin", places, cos.shape[1], torch.float32, gpu)
+        places, half = cos.shape
+        rotary = 2 * half
+        zptr, lds = _matrix(sin, "sin", places, half, torch.float32, gpu)
         if places > 1 and ldt != lds:
             raise ValueError("cos and sin must have the same row stride")
         if positions is not None:
             wide = positions.dtype is torch.int64
             pptr = _vector(positions, "positions", t, torch.int64 if wide else torch.int32, gpu)
     kptr = ldk = hsk = koptr = ldko = hsko = kv = 0
-    q_out, qoptr, ldqo, hsqo = _heads_out(q_out, "q_out", q, dtype, gpu)
+    q_out, qoptr, ldqo, hsqo = _heads_out(q_out, "q_out", q_shape, dtype, device, gpu)
     if k is not None:
-        kptr, ldk, hsk = _heads_of(k, "k", t, None, d, q.dtype, gpu)
-        kv = k.shape[1]
-        k_out, koptr, ldko, hsko = _heads_out(k_out, "k_out", k, dtype, gpu)
+        k_shape, kptr, ldk, hsk = _heads_of(k, "k", t, None, d, q.dtype, gpu)
+        kv = k_shape[1]
+        k_out, koptr, ldko, hsko = _heads_out(k_out, "k_out", k_shape, dtype, device, gpu)
     elif k_out is not None:
         raise ValueError("k_out without k")
     args = _pack_qk_args(
         t, d, rotary, qptr, ldq, hsq, qoptr, ldqo, hsqo, kptr, ldk, hsk, koptr, ldko, hsko, cptr, zptr, ldt, places,
-        pptr, _vector(q_weight, "q_weight", d, param, gpu), _vector(k_weight, "k_weight", d, param, gpu),
-        _vector(q_bias, "q_bias", d, param, gpu), _vector(k_bias, "k_bias", d, param, gpu), heads, kv, eps,
+        pptr, *vectors, heads, kv, eps,
         _NORMS[norm], 1 if interleaved else 0, 1 if wide else 0, in_type, out_type, p_type)
     _run("signrot_qk_norm_rope", q, args)
     return q_out, k_out
