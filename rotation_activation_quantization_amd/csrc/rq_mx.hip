@@ -1,5 +1,8 @@
 // The fast kernels (rq_fast_impl.h, rq_halves_impl.h) with MXFP4 output, d given as
-// (c, sigma).
+// (c, sigma).  A block of 32 channels lies in one to four lanes after the transform, so
+// no row maximum is exchanged between waves; but every wave stores scales beside its
+// codes: 8192 x 14336 takes 71.6 us (INT4 66.7), with the producer 115 (107), 8192 x 28672
+// 136 (129).
 #include "rq_fast_impl.h"
 #include "rq_halves_impl.h"
 

@@ -113,7 +113,8 @@ __device__ __forceinline__ int one_tile_out(int nl) {
   return (nl & 9) ^ ((nl & 2) ? 6 : 0) ^ ((nl & 4) ? 3 : 0);
 }
 
-// MX: MXFP4 codes and block scales in place of the INT4 ones.
+// MX: MXFP4 codes and block scales in place of the INT4 ones (8192 x 13824 84 us, INT4
+// 78; 8192 x 5120 33 and 29).
 template <int KC, int NTL, int MTW, bool GENERAL, bool YOUT, bool ZINT = false, bool MX = false>
 __device__ void rq_outer_body(const RqArgs& a, uint8_t* lds, const uint32_t* dbits, const DForm& form, float* red,
                               float* xcl) {
