@@ -639,7 +639,9 @@ int signrot_swiglu_rotate_quant_mxfp4(const void* gate_bf16, const void* up_bf16
  * Channels from `rotary` on are normed only.  All arithmetic is binary32; each
  * result is rounded once.  A head that holds an infinity or NaN gives
  * unspecified results in that head only, with NORM_NONE in its pair only.  Sums
- * and squares may pass binary32's range: such a head is normed on scaled values.
+ * and squares may pass binary32's range, or fall below it with an eps that does
+ * not hide them: such a head is normed on scaled values.  (With eps 0 a head of
+ * zeros, or of equal values with NORM_LAYER, gives NaN.)
  *
  *   tokens, head, rotary   0 <= tokens < 2^31; channels of a head, even, in
  *                 [8, 512]; rotated channels, even, in [0, head].

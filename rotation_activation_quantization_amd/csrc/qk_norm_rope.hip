@@ -75,9 +75,14 @@ __device__ __forceinline__ float inverse_root(float x) {
   return fmaf(r, fmaf(-0.5f * x * r, r, 0.5f), r);
 }
 
-// Squares of values around 2^64 and more pass binary32's range; such a head is
-// normed again, its values scaled by this.
-constexpr float kSmall = 0x1p-80f;
+// Squares of values around 2^64 and more pass binary32's range, those of values below
+// 2^-63 lose bits or vanish.  A head whose sum of squares is not finite, or whose mean
+// square and eps are together below 2^-100 (r over kMost), is normed again, its values
+// scaled down or up.  A larger eps hides what such squares lose.  A small head's values lie below
+// 2^-45 and its mean below kMean, so that scaled up they stay below 2^80 and their sum of
+// squares finite; where a mean is larger, such a small deviation can only be zero.
+constexpr float kDown = 0x1p-80f, kUp = 0x1p100f;
+constexpr float kMost = 0x1p50f, kMean = 0x1p-20f;
 
 // Eight values as they lie in memory.
 struct Raw {
@@ -220,7 +225,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       float v[8], o[8];
       widen<BF16>(raw, v);
       float mean = 0.f, r = 1.f, scale = 1.f;
-      // (a second time if a head is large; which one is the same in all lanes of it)
+      // (a second time if a head is large or small; which one is the same in all lanes of it)
       for (bool more = normed; more;) {
         if (a.norm == SIGNROT_NORM_LAYER) {
           float s = 0.f;
@@ -238,10 +243,10 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
           if (ch.own(e)) ss = fmaf(v[e], v[e], ss);
         ss = head_sum<G>(live ? ss : 0.f);
         r = inverse_root(fmaf(ss, inv_n, a.eps * scale * scale));
-        const bool large = scale == 1.f && !(ss < INFINITY);
-        more = __builtin_amdgcn_ballot_w64(large) != 0;
+        const float to = !(ss < INFINITY) ? kDown : r > kMost && fabsf(mean) < kMean ? kUp : 1.f;
+        more = __builtin_amdgcn_ballot_w64(scale == 1.f && to != 1.f) != 0;
         if (more) {
-          scale = large ? kSmall : scale;
+          scale = scale == 1.f ? to : scale;
           widen<BF16>(load(gr), v);  // read again: raw does not have to stay
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] *= scale;
