@@ -636,7 +636,8 @@ int signrot_swiglu_rotate_quant_mxfp4(const void* gate_bf16, const void* up_bf16
  * interleaved:
  *   a' = a cos[r][p] - b sin[r][p],   b' = b cos[r][p] + a sin[r][p],
  * r = positions[t] (clamped into [0, places)), or t when positions is NULL.
- * Channels from `rotary` on are normed only.  All arithmetic is binary32; each
+ * Channels from `rotary` on are normed only; with NORM_NONE their values come
+ * through as they are, signs of zeros too.  All arithmetic is binary32; each
  * result is rounded once.  A head that holds an infinity or NaN gives
  * unspecified results in that head only, with NORM_NONE in its pair only.  Sums
  * and squares may pass binary32's range, or fall below it with an eps that does

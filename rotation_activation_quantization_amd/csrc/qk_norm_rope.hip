@@ -164,7 +164,9 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       return r;
     };
     Raw next = load(gr);
-    float wc[8], ws[8], add[8];
+    // (ws and the sum of the biases negated: what a channel that is not rotated or has no bias
+    // adds is then -0, which leaves a zero's sign)
+    float wc[8], ws[8], sub[8];
     {
       // angles, weights and biases of the lane's channels and of their partners
       float cs[8], sn[8], w[8], wp[8], b[8], bp[8];
@@ -174,7 +176,8 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         for (int k = 0; k < 4; ++k) {
           const bool turn = live && ch.at + 2 * k < rotary;
           cs[2 * k] = cs[2 * k + 1] = turn ? a.cos[angles + ch.at / 2 + k] : 1.f;
-          sn[2 * k] = sn[2 * k + 1] = turn ? a.sin[angles + ch.at / 2 + k] : 0.f;
+          sn[2 * k] = turn ? a.sin[angles + ch.at / 2 + k] : 0.f;
+          sn[2 * k + 1] = turn ? -sn[2 * k] : 0.f;
         }
       } else if (PAIRS == kChunks && ch.at >= rotary) {
 #pragma unroll
@@ -183,6 +186,10 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         const int64_t at = angles + (ch.at < half ? ch.at : ch.at - half);
         row::load8<false>(a.cos, at, 0, cs);
         row::load8<false>(a.sin, at, 0, sn);
+        if (ch.at >= half) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -190,6 +197,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
           const bool turn = live && j < rotary;
           cs[e] = turn ? a.cos[angles + (j < half ? j : j - half)] : 1.f;
           sn[e] = turn ? a.sin[angles + (j < half ? j : j - half)] : 0.f;
+          if (turn && j >= half) sn[e] = -sn[e];
         }
       }
       auto both = [&](const void* of, bool given, float none, float(&own)[8], float(&far)[8]) {
@@ -210,11 +218,10 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       both(bias, biased, 0.f, b, bp);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (PAIRS == kOwn ? !(e & 1) : ch.at + e < half) sn[e] = -sn[e];  // the first of a pair
         if (PAIRS != kAcross && ch.at + e >= rotary) wp[e] = bp[e] = 0.f;
         wc[e] = w[e] * cs[e];
         ws[e] = wp[e] * sn[e];
-        add[e] = biased ? fmaf(bp[e], sn[e], b[e] * cs[e]) : 0.f;
+        sub[e] = biased ? fmaf(bp[e], sn[e], -(b[e] * cs[e])) : 0.f;
       }
     }
     for (; gr < groups; gr += parts) {
@@ -287,7 +294,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(fmaf(other[e], ws[e], v[e] * wc[e]), r, add[e]);
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(fmaf(other[e], -ws[e], v[e] * wc[e]), r, -sub[e]);
       if (!on) continue;
       const int64_t to = h * hso + ch.at;
       if (WHOLE || ch.dup == 0) {
