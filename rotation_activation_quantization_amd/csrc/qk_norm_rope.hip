@@ -361,9 +361,13 @@ void run(const Args& a, bool whole, hipStream_t s) {
     const auto go = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, s>>>(b, parts, stream); };
     const auto pick = [&](auto BF16) {
       constexpr bool kBf16 = decltype(BF16)::value;
-      if (pairs == kAcross) go(qk_norm_rope_kernel<G, kBf16, true, kAcross>);
-      else if (pairs == kChunks) go(qk_norm_rope_kernel<G, kBf16, true, kChunks>);
-      else if (pairs == kOwn)
+      // (whole chunks in heads of one lane are the lane's own; of the sixteen channels of two
+      // lanes none or all are rotated so)
+      if constexpr (G > 1)
+        if (pairs == kAcross) return go(qk_norm_rope_kernel<G, kBf16, true, kAcross>);
+      if constexpr (G > 2)
+        if (pairs == kChunks) return go(qk_norm_rope_kernel<G, kBf16, true, kChunks>);
+      if (pairs == kOwn)
         whole ? go(qk_norm_rope_kernel<G, kBf16, true, kOwn>) : go(qk_norm_rope_kernel<G, kBf16, false, kOwn>);
       else
         whole ? go(qk_norm_rope_kernel<G, kBf16, true, kAnywhere>) : go(qk_norm_rope_kernel<G, kBf16, false, kAnywhere>);
