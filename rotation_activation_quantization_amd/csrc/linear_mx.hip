@@ -55,7 +55,15 @@ __device__ __forceinline__ void mfma_to(f32x4_t& acc, const i32x4_t& a, const i3
                : "+v"(acc)
                : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(OA & 1), "n"(OB & 1), "n"(OA >> 1), "n"(OB >> 1));
 }
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// Waits for the sums and hands them on, so that no reader, nor a move of them, comes before.
+template <int FK, int FT>
+__device__ __forceinline__ void settle(f32x4_t (&acc)[FK][FT]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < FK; ++f)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) asm volatile("" : "+v"(acc[f][j]));
+}
 
 // Four results of token t from channel k on: a vector at whatever address it has,
 // single ones at the row's end.
@@ -513,7 +521,7 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, int tiles_m, int tiles_
       for (int l = kLate; l < C::kLoads; ++l) issue(l, 1, 1);
     }
 
-    settle();
+    settle(acc);
     if (SPLIT) {
       // partial sums in operand order, [part][tile][wave][f][j][lane]
       f32x4_t* const out = reinterpret_cast<f32x4_t*>(a.workspace) +
