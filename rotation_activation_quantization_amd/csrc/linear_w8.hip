@@ -753,6 +753,9 @@ __device__ __forceinline__ void w8_few(const W8Args& a, uint8_t* lds) {
 #pragma unroll
         for (int j = 0; j < FT; ++j)
           acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][f], tok[s][j], acc[f][j], 0, 0, 0);
+    // The slot is free once its reads are done; they are not ordered with the loads, and the
+    // products that wait for them may be moved behind the barrier.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     if (x + D < count) issue(x + D);
   }

@@ -1,5 +1,6 @@
-"""What the compiled product has to keep in order beyond what the compiler knows: the readers of a sum that matrix
-instructions in inline assembly form, checked on the assembly along every path.  And the instances of the per-head norms: those that the dispatch reaches."""
+"""What the compiled products have to keep in order beyond what the compiler knows: the readers of a sum that matrix
+instructions in inline assembly form, and loads to a place of LDS that reads have just left.  Checked on the assembly
+along every path.  And the instances of the per-head norms: those that the dispatch reaches."""
 
 import os
 import re
@@ -10,7 +11,7 @@ import pytest
 
 from rotation_activation_quantization_amd import build as B
 
-SOURCES = ("linear_mx.hip", "qk_norm_rope.hip")
+SOURCES = ("linear_mx.hip", "linear_w8.hip", "qk_norm_rope.hip")
 # wait states from a matrix instruction of sixteen passes to a reader of its result, and one to spare
 SETTLED = 20
 
@@ -115,12 +116,34 @@ def unsettled(lines):
     return bad
 
 
+def early_loads(lines):
+    """Loads to LDS issued while reads of LDS may still be on their way."""
+    bad = []
+
+    def step(reading, line):
+        if line.startswith("ds_read"):
+            return True
+        if line.startswith("s_waitcnt"):
+            return reading and "lgkmcnt(0)" not in line
+        if reading and re.search(r"_load\w*_lds|_load.*\blds$", line):
+            bad.append(line)
+        return reading
+
+    flow(lines, False, step, lambda a, b: a or b)
+    return bad
+
+
 def test_the_checks_see_what_they_look_for():
     mfma = "v_mfma_scale_f32_16x16x128_f8f6f4 v[4:7], v[8:11], v[12:15], v[4:7], v1, v2 cbsz:4 blgp:4"
     assert unsettled([mfma, "s_nop 15", "v_add_f32_e32 v0, v0, v5"])
     assert not unsettled([mfma, "s_nop 15", "s_nop 15", "v_add_f32_e32 v0, v0, v5"])
     assert unsettled([mfma, "v_mov_b32_e32 v6, 0"])
     assert unsettled([".LBB0_1:", "ds_write_b128 v0, v[4:7]", mfma, "s_cbranch_scc1 .LBB0_1", "s_endpgm"])
+    load = "buffer_load_dwordx4 v60, s[0:3], s16 offen lds"
+    assert early_loads(["ds_read_b128 v[0:3], v4", load])
+    assert early_loads([".LBB0_1:", load, "ds_read_b128 v[0:3], v4", "s_cbranch_scc1 .LBB0_1", "s_endpgm"])
+    assert early_loads(["ds_read_b128 v[0:3], v4", "s_waitcnt lgkmcnt(1)", "global_load_lds_dword v[60:61], off"])
+    assert not early_loads(["ds_read_b128 v[0:3], v4", "s_waitcnt vmcnt(0) lgkmcnt(0)", load])
 
 
 def test_sums_are_read_when_they_are_there(code):
@@ -129,6 +152,15 @@ def test_sums_are_read_when_they_are_there(code):
     for name, lines in kernels.items():
         assert any(line.startswith("v_mfma_scale") for line in lines)
         assert not unsettled(lines), name
+
+
+@pytest.mark.parametrize("src,kernel", [("linear_mx.hip", "mx_few_kernel"), ("linear_w8.hip", "w8_few_kernel")])
+def test_a_slot_is_loaded_when_its_reads_are_done(code, src, kernel):
+    kernels = {k: v for k, v in code[src].items() if kernel in k}
+    assert len(kernels) == 8
+    for name, lines in kernels.items():
+        assert sum(bool(re.search(r"\blds$|_load_lds", line)) for line in lines) and sum("ds_read" in x for x in lines)
+        assert not early_loads(lines), name
 
 
 def test_no_instance_of_the_norms_that_no_call_reaches(code):
