@@ -72,15 +72,15 @@ __device__ __forceinline__ int64_t place_of(const Args& a, int64_t t) {
 __device__ __forceinline__ float inverse_root(float x) {
   if (x < 0x1p-100f) return 1.f / sqrtf(x);
   const float r = __builtin_amdgcn_rsqf(x);
-  return fmaf(r, fmaf(-0.5f * x * r, r, 0.5f), r);
+  return fmaf(r, fmaf(-0.5f * x * r, r, 0.5f), r);  // NaN where x is not finite
 }
 
 // Squares of values around 2^64 and more pass binary32's range, those of values below
-// 2^-63 lose bits or vanish.  A head whose sum of squares is not finite, or whose mean
-// square and eps are together below 2^-100 (r over kMost), is normed again, its values
-// scaled down or up.  A larger eps hides what such squares lose.  A small head's values lie below
-// 2^-45 and its mean below kMean, so that scaled up they stay below 2^80 and their sum of
-// squares finite; where a mean is larger, such a small deviation can only be zero.
+// 2^-63 lose bits or vanish.  A head whose mean square and eps are together not finite
+// (r is NaN), or below 2^-100 (r over kMost), is normed again, its values scaled down or up:
+// an eps of 2^-100 or more hides what squares below it lose.  A small head's values lie
+// below 2^-45 and its mean below kMean, so that scaled up they stay below 2^80 and their
+// sum of squares finite; where a mean is larger, such a small deviation can only be zero.
 constexpr float kDown = 0x1p-80f, kUp = 0x1p100f;
 constexpr float kMost = 0x1p50f, kMean = 0x1p-20f;
 
@@ -232,8 +232,11 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       float v[8], o[8];
       widen<BF16>(raw, v);
       float mean = 0.f, r = 1.f, scale = 1.f;
-      // (a second time if a head is large or small; which one is the same in all lanes of it)
-      for (bool more = normed; more;) {
+      // A second time if a head is large or small, which is the same in all lanes of it.  (With
+      // the first turn apart, as the compiler has it otherwise, half of the channels rotated
+      // took 72.8 us, and 61.9 so.)
+#pragma clang loop unroll(disable)
+      for (bool again = false; normed; again = true) {
         if (a.norm == SIGNROT_NORM_LAYER) {
           float s = 0.f;
 #pragma unroll
@@ -250,14 +253,11 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
           if (ch.own(e)) ss = fmaf(v[e], v[e], ss);
         ss = head_sum<G>(live ? ss : 0.f);
         r = inverse_root(fmaf(ss, inv_n, a.eps * scale * scale));
-        const float to = !(ss < INFINITY) ? kDown : r > kMost && fabsf(mean) < kMean ? kUp : 1.f;
-        more = __builtin_amdgcn_ballot_w64(scale == 1.f && to != 1.f) != 0;
-        if (more) {
-          scale = scale == 1.f ? to : scale;
-          widen<BF16>(load(gr), v);  // read again: raw does not have to stay
+        if (again || __builtin_amdgcn_ballot_w64(!(r <= kMost)) == 0) break;
+        scale = r <= kMost ? 1.f : r > kMost ? (fabsf(mean) < kMean ? kUp : 1.f) : kDown;
+        widen<BF16>(load(gr), v);  // read again: raw does not have to stay
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= scale;
-        }
+        for (int e = 0; e < 8; ++e) v[e] *= scale;
       }
       float other[8];
       if (PAIRS == kOwn) {

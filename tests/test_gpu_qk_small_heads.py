@@ -112,3 +112,14 @@ def test_small_heads_in_place():
     ref, _ = R.qk_norm_rope(x, cos=cos, sin=sin, eps=0.0, q_weight=w)
     R.qk_norm_rope(x, cos=cos, sin=sin, eps=0.0, q_weight=w, q_out=x)
     assert torch.equal(x, ref) and torch.isfinite(x).all()
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_an_eps_that_takes_the_mean_square_past_the_range(norm):
+    """Squares whose sum is finite, beside an eps near binary32's largest: their sum is not."""
+    x = torch.tensor([6e18, -6e18] * 4, device="cuda").repeat(2, 3, 1)
+    x[:, 1] *= 1e-3
+    angle = torch.rand((2, 4), device="cuda", dtype=torch.float64) * 7
+    cos, sin, w = angle.cos().float(), angle.sin().float(), torch.ones(8, device="cuda")
+    got, _ = R.qk_norm_rope(x, cos=cos, sin=sin, norm=norm, eps=3.35e38, q_weight=w)
+    check(got, x, cos, sin, norm, 3.35e38, w, None, False)
