@@ -176,8 +176,7 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         for (int k = 0; k < 4; ++k) {
           const bool turn = live && ch.at + 2 * k < rotary;
           cs[2 * k] = cs[2 * k + 1] = turn ? a.cos[angles + ch.at / 2 + k] : 1.f;
-          sn[2 * k] = turn ? a.sin[angles + ch.at / 2 + k] : 0.f;
-          sn[2 * k + 1] = turn ? -sn[2 * k] : 0.f;
+          sn[2 * k] = sn[2 * k + 1] = turn ? a.sin[angles + ch.at / 2 + k] : 0.f;
         }
       } else if (PAIRS == kChunks && ch.at >= rotary) {
 #pragma unroll
@@ -186,10 +185,6 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
         const int64_t at = angles + (ch.at < half ? ch.at : ch.at - half);
         row::load8<false>(a.cos, at, 0, cs);
         row::load8<false>(a.sin, at, 0, sn);
-        if (ch.at >= half) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
-        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -197,7 +192,6 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
           const bool turn = live && j < rotary;
           cs[e] = turn ? a.cos[angles + (j < half ? j : j - half)] : 1.f;
           sn[e] = turn ? a.sin[angles + (j < half ? j : j - half)] : 0.f;
-          if (turn && j >= half) sn[e] = -sn[e];
         }
       }
       auto both = [&](const void* of, bool given, float none, float(&own)[8], float(&far)[8]) {
@@ -218,7 +212,11 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_kernel(Args a, int p
       both(bias, biased, 0.f, b, bp);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (PAIRS != kAcross && ch.at + e >= rotary) wp[e] = bp[e] = 0.f;
+        if (PAIRS == kOwn ? e & 1 : ch.at + e >= half) sn[e] = -sn[e];  // the second of a pair
+        if (PAIRS != kAcross && ch.at + e >= rotary) {
+          wp[e] = PAIRS == kOwn && !(e & 1) ? 0.f : -0.f;  // (times sn, +-0: +0)
+          bp[e] = 0.f;
+        }
         wc[e] = w[e] * cs[e];
         ws[e] = wp[e] * sn[e];
         sub[e] = biased ? fmaf(bp[e], sn[e], -(b[e] * cs[e])) : 0.f;
