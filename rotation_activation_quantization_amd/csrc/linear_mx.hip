@@ -163,13 +163,17 @@ struct Tile {
 // first stage can leave the stores on their way (8192 x 4096 x 4096 71.2 us, 72.9
 // with the wait for them).
 //
-// What bounds a large product is the matrix units at the clock that their power leaves:
-// 8192 x 4096 x 14336 takes 230 to 250 us (3.9 to 4.2 PFLOP/s) with the units 65 % busy
-// at 1.8 GHz; all zeros run at 2.3 GHz.  Alone, on values in registers, the instruction
-// reaches 7.0 PFLOP/s of random codes and 9.3 of zeros.  Of the rest, loads cost some
-// 15 % of the cycles, LDS reads 9 %, a tile's start and stores 6 us.  Four waves of 128 x
-// 128 (a third fewer LDS reads) were slower, as were stores past the caches and staggered
-// starts.
+// What bounds a large product: 8192 x 4096 x 14336 takes 230 to 250 us (3.9 to 4.2
+// PFLOP/s), the tiles 215 of them in a loop over the same operands.  There the matrix
+// units are busy 60 % of the cycles (8192 x 14336 x 4096: 65 %) at 1.8 GHz, on all zeros
+// for as many cycles at 2.2 GHz, 176 us: the power that real operands take costs a fifth.
+// The other 40 % of the cycles are the tiles' own.  LDS serves reads and writes by index in
+// 30 % of them, the L2s deliver 21 bytes a cycle and CU, and a wave waits 38 % of its time;
+// none of that is full, but in every tile a quad's time follows the bytes staged, 22 to 25
+// ns a KiB, more than its products.  A tile's start and stores cost what two quads do.
+// Alone, on values in registers, the instruction reaches 7.0 PFLOP/s of random codes and
+// 9.3 of zeros.  Four waves of 128 x 128 (a third fewer LDS reads) were slower, as were
+// stores past the caches and staggered starts.
 //
 // A row is cut into quads of four depths (512 channels, two stages).  Quad 0 of
 // a tile is the row's last, possibly short one.  Its chunks beyond n are read
